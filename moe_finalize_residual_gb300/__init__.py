@@ -357,3 +357,11 @@ def moe_finalize_abi_version() -> int:
 def raw_library():
     """The loaded ctypes library (for callers that build the C argument block themselves)."""
     return _lib
+
+
+from . import layer as _layer  # noqa: E402  (the operators around the finalize, over the same library)
+
+_layer._bind(_lib, _check)
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += _layer.__all__

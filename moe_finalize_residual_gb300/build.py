@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_finalize.so")
-SOURCES = ["api.cu", "kernel_cluster.cu", "kernel_stream.cu", "kernel_bulk.cu"]
+SOURCES = ["api.cu", "kernel_cluster.cu", "kernel_stream.cu", "kernel_bulk.cu", "layer_api.cu", "kernel_route.cu",
+           "kernel_rows.cu", "kernel_heads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +39,7 @@ def _flags(ptxas_verbose: bool):
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
-    deps = [src, os.path.join(INCLUDE, "moe_finalize.h")] + [
+    deps = [src] + [os.path.join(INCLUDE, n) for n in os.listdir(INCLUDE) if n.endswith(".h")] + [
         os.path.join(CSRC, n) for n in os.listdir(CSRC) if n.endswith((".cuh", ".h"))]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 

@@ -21,8 +21,8 @@
 
 namespace mfr {
 namespace {
-
 thread_local char g_last_error[512] = "";
+}  // namespace
 
 int fail(int status, const char* fmt, ...) {
   va_list ap;
@@ -31,6 +31,8 @@ int fail(int status, const char* fmt, ...) {
   va_end(ap);
   return status;
 }
+
+namespace {
 
 struct DeviceInfo {
   int sms = 0;

@@ -44,6 +44,9 @@ struct LaunchGeom {
   int smem_optin;  // the device's opt-in maximum of dynamic shared memory per block
 };
 
+// Keep a message for the calling thread (moe_finalize_last_error) and return `status`.
+int fail(int status, const char* fmt, ...);
+
 cudaError_t launch_cluster_kernel(int act_dtype, const KParams& p, const LaunchGeom& g, cudaStream_t stream);
 // Cluster kernel forms: 8 routes in flight per thread with the register budget of two 512-thread CTAs
 // per SM (plans that loop over chunks); 8 in flight with a wider register budget (one-chunk plans, whose

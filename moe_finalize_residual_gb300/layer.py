@@ -1,0 +1,513 @@
+"""The operators around the fused MoE finalize: expert routing, dispatch, the finalize's gradient, and the per-head
+RMSNorm with position rotation of queries and keys.
+
+A thin binding over ``include/moe_layer.h``, as the package's ``__init__`` is over ``moe_finalize.h``: it checks and
+marshals arguments, and every step runs in the library's kernels.  Outputs that are not passed in are allocated.
+Every call takes ``stream`` (default: the tensors' device's current stream), ``pdl`` (programmatic dependent launch)
+and ``check`` (False skips the tensors' checks; the library's own stay).  Gradients are explicit calls.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Optional, Tuple
+
+import torch
+
+__all__ = [
+    "Routing", "moe_route", "moe_route_max_rows", "moe_route_workspace_bytes", "moe_route_backward", "moe_dispatch",
+    "moe_finalize_routed_backward", "head_norm_rotary", "head_norm_rotary_backward",
+    "head_norm_rotary_workspace_bytes", "SCORE", "GROUP_SCORE", "ROTARY_STYLE",
+]
+
+_P, _I, _L, _F, _U = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_uint32
+
+DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
+ROTARY_STYLE = {"half": 0, "interleaved": 1}
+_PDL, _ZERO_PADDING, _POSITIONS_64 = 1, 4, 8
+
+
+class _CRoute(ctypes.Structure):
+    _fields_ = [("T", _I), ("E", _I), ("K", _I), ("logits_dtype", _I), ("scale_dtype", _I), ("score", _I),
+                ("num_groups", _I), ("topk_groups", _I), ("group_score", _I), ("renormalize", _I), ("row_align", _I),
+                ("scale", _F), ("logits", _P), ("logits_stride", _L), ("bias", _P), ("expert_ids", _P),
+                ("expert_scale", _P), ("perm_idx", _P), ("row_route", _P), ("num_rows", _L), ("expert_offsets", _P),
+                ("expert_counts", _P), ("workspace", _P), ("workspace_bytes", _L), ("flags", _U)]
+
+
+class _CRouteBackward(ctypes.Structure):
+    _fields_ = [("T", _I), ("E", _I), ("K", _I), ("logits_dtype", _I), ("scale_dtype", _I), ("score", _I),
+                ("renormalize", _I), ("scale", _F), ("logits", _P), ("logits_stride", _L), ("expert_ids", _P),
+                ("d_scale", _P), ("d_logits", _P), ("d_logits_stride", _L), ("flags", _U)]
+
+
+class _CDispatch(ctypes.Structure):
+    _fields_ = [("T", _I), ("K", _I), ("row_bytes", _L), ("num_rows", _L), ("x", _P), ("perm_idx", _P),
+                ("row_route", _P), ("rows", _P), ("flags", _U)]
+
+
+class _CRoutedBackward(ctypes.Structure):
+    _fields_ = [("T", _I), ("H", _I), ("K", _I), ("act_dtype", _I), ("scale_dtype", _I),
+                ("routed_scaling_factor", _F), ("num_rows", _L), ("gemm2_out", _P), ("perm_idx", _P),
+                ("expert_scale", _P), ("row_route", _P), ("d_out", _P), ("d_gemm2", _P), ("d_scale", _P),
+                ("flags", _U)]
+
+
+class _CHeads(ctypes.Structure):
+    _fields_ = [("data", _P), ("token_stride", _L), ("head_stride", _L)]
+
+
+class _CHeadNorm(ctypes.Structure):
+    _fields_ = [("T", _I), ("q_heads", _I), ("k_heads", _I), ("D", _I), ("rot", _I), ("style", _I), ("act_dtype", _I),
+                ("eps", _F), ("rotary_scale", _F), ("q", _CHeads), ("k", _CHeads), ("q_out", _CHeads),
+                ("k_out", _CHeads), ("d_q_out", _CHeads), ("d_k_out", _CHeads), ("q_weight", _P), ("k_weight", _P),
+                ("positions", _P), ("inv_freq", _P), ("d_q_weight", _P), ("d_k_weight", _P), ("workspace", _P),
+                ("workspace_bytes", _L), ("flags", _U)]
+
+
+_lib = None
+_raise_status = None
+
+
+def _bind(lib, raise_status):
+    """Called once by the package: the loaded library and its status check."""
+    global _lib, _raise_status
+    _lib, _raise_status = lib, raise_status
+    for name, args in (("moe_route", _CRoute), ("moe_route_backward", _CRouteBackward),
+                       ("moe_dispatch_rows", _CDispatch), ("moe_routed_backward", _CRoutedBackward),
+                       ("moe_head_norm_rotary", _CHeadNorm), ("moe_head_norm_rotary_backward", _CHeadNorm)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = [ctypes.POINTER(args), _P], ctypes.c_int
+    for name, n in (("moe_route_max_rows", 4), ("moe_route_workspace_bytes", 3),
+                    ("moe_head_norm_rotary_workspace_bytes", 4)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = [_I] * n, _L
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _size(n: int) -> int:
+    if n < 0:
+        _raise_status(int(n))
+    return int(n)
+
+
+def _choice(table, name, value):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} is {value!r}; one of {', '.join(table)} is wanted") from None
+
+
+def _check_tensor(name, t, device, shape, dtypes, contiguous=True):
+    """``shape``: a tuple, or None.  ``dtypes``: a dtype or a container of them."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}; every tensor must be on {device} (a CUDA device)")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} is {list(t.shape)}; {list(shape)} is wanted")
+    if t.dtype != dtypes if isinstance(dtypes, torch.dtype) else t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}; {dtypes if isinstance(dtypes, torch.dtype) else ', '.join(map(str, dtypes))} is wanted")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _enqueue(fn, args, device, stream, allocated):
+    """Enqueue on ``stream`` with the tensors' device current.  What the binding allocated on the current stream
+    and hands to another one is recorded there, so that its memory is not given out again too early."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _enqueue(fn, args, device, stream, allocated)
+    if stream is None:
+        handle = torch.cuda.current_stream().cuda_stream
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}; the tensors are on {device}")
+        handle = stream.cuda_stream
+        if handle != torch.cuda.current_stream().cuda_stream:
+            # allocated memory may still be in use by work queued on the current stream before it was freed
+            stream.wait_stream(torch.cuda.current_stream()) if allocated else None
+            for t in allocated:
+                t.record_stream(stream)
+    status = fn(ctypes.byref(args), handle)
+    if status != 0:
+        _raise_status(status)
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Routing
+# ----------------------------------------------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class Routing:
+    """What ``moe_route`` writes.  ``perm_idx`` and ``expert_scale`` are those of a ``Partial``."""
+
+    expert_ids: torch.Tensor                        # [T, K] int32, best first; -1 = no expert left to take
+    expert_scale: torch.Tensor                      # [T, K] fp32/bf16/fp16 weights
+    perm_idx: Optional[torch.Tensor] = None         # [T, K] int32: the row of route (t, k), or -1
+    row_route: Optional[torch.Tensor] = None        # [rows] int32: the route t*K+k of a row, or -1
+    expert_offsets: Optional[torch.Tensor] = None   # [E + 1] int32: where each expert's rows start
+    expert_counts: Optional[torch.Tensor] = None    # [E] int32: routes of each expert
+
+
+def moe_route_max_rows(T: int, K: int, E: int, row_align: int = 1) -> int:
+    """The most rows that T*K routes fill when every expert's rows are padded to a multiple of ``row_align``."""
+    return _size(_lib.moe_route_max_rows(T, K, E, row_align))
+
+
+def moe_route_workspace_bytes(T: int, K: int, E: int) -> int:
+    """Workspace of ``moe_route`` with the expert order (0 for small batches)."""
+    return _size(_lib.moe_route_workspace_bytes(T, K, E))
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+              num_groups: int = 1, topk_groups: int = 1, group_score: str = "max", renormalize: bool = True,
+              scale: float = 1.0, scale_dtype: torch.dtype = torch.float32, row_align: int = 1, order: bool = True,
+              out: Optional[Routing] = None, workspace: Optional[torch.Tensor] = None, pdl: bool = True,
+              stream: Optional[torch.cuda.Stream] = None, check: bool = True) -> Routing:
+    """Choose ``top_k`` experts for each token and weigh them; with ``order``, sort the routes by expert.
+
+    ``logits`` is [T, E] (fp32, bf16 or fp16; rows may be strided).  The score of an expert is its softmax or
+    sigmoid; ``bias`` ([E] fp32) is added for the choice only.  With ``num_groups`` > 1 only the experts of the
+    ``topk_groups`` best groups are taken, by a group's best choice score ("max") or the sum of its two best
+    ("top2").  The weights are the scores, divided by their sum with ``renormalize``, times ``scale``.  Equal
+    scores go to the lowest expert, and the order is decided as in 64 bits.  Experts with a logit of -inf or NaN
+    are never taken; places left over get id -1, weight 0 and ``perm_idx`` -1, which the finalize skips.
+
+    The expert order makes each expert's rows start at a multiple of ``row_align``.  ``out`` takes the outputs'
+    buffers (``out.expert_offsets`` None: no order, whatever ``order`` says); ``row_route`` must hold at least
+    ``moe_route_max_rows`` rows.  ``workspace`` must not be shared by calls that may run at the same time."""
+    if check:
+        if logits.dim() != 2:
+            raise ValueError("logits must be [T, E]")
+        _check_tensor("logits", logits, logits.device, None, DTYPE, contiguous=False)
+    T, E = logits.shape
+    dev = logits.device
+    stride = logits.stride(0) if T > 1 else E
+    if check and E > 1 and logits.stride(1) != 1:
+        raise ValueError("the experts of a token must be contiguous in logits")
+    allocated = []
+    if out is None:
+        if scale_dtype not in DTYPE:
+            raise ValueError(f"scale_dtype {scale_dtype} is not supported (fp32, bf16 or fp16)")
+        out = Routing(torch.empty(T, top_k, dtype=torch.int32, device=dev),
+                      torch.empty(T, top_k, dtype=scale_dtype, device=dev))
+        if order:
+            out.perm_idx = torch.empty_like(out.expert_ids)
+            out.row_route = torch.empty(moe_route_max_rows(T, top_k, E, row_align), dtype=torch.int32, device=dev)
+            out.expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+            out.expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
+        allocated = [t for t in dataclasses.astuple(out) if t is not None] if stream is not None else []
+    ordered = out.expert_offsets is not None
+    if check:
+        if bias is not None:
+            _check_tensor("bias", bias, dev, (E,), torch.float32)
+        shape = (T, top_k)
+        _check_tensor("expert_ids", out.expert_ids, dev, shape, torch.int32)
+        _check_tensor("expert_scale", out.expert_scale, dev, shape, DTYPE)
+        if ordered:
+            _check_tensor("perm_idx", out.perm_idx, dev, shape, torch.int32)
+            _check_tensor("row_route", out.row_route, dev, None, torch.int32)
+            _check_tensor("expert_offsets", out.expert_offsets, dev, (E + 1,), torch.int32)
+            _check_tensor("expert_counts", out.expert_counts, dev, (E,), torch.int32)
+        if workspace is not None:
+            _check_tensor("workspace", workspace, dev, None, torch.uint8)
+    space = 0
+    if ordered:
+        if workspace is not None:
+            space = workspace.numel()
+        else:
+            space = moe_route_workspace_bytes(T, top_k, E)
+            if space:
+                workspace = torch.empty(space, dtype=torch.uint8, device=dev)
+                allocated.append(workspace)
+    a = _CRoute(T, E, top_k, DTYPE[logits.dtype], DTYPE[out.expert_scale.dtype], _choice(SCORE, "score", score),
+                num_groups, topk_groups, _choice(GROUP_SCORE, "group_score", group_score), 1 if renormalize else 0,
+                row_align, scale, logits.data_ptr(), stride, _ptr(bias), out.expert_ids.data_ptr(),
+                out.expert_scale.data_ptr())
+    if ordered:
+        a.perm_idx = out.perm_idx.data_ptr()
+        a.row_route = out.row_route.data_ptr()
+        a.num_rows = out.row_route.numel()
+        a.expert_offsets = out.expert_offsets.data_ptr()
+        a.expert_counts = out.expert_counts.data_ptr()
+        a.workspace = _ptr(workspace)
+        a.workspace_bytes = space
+    a.flags = _PDL if pdl else 0
+    _enqueue(_lib.moe_route, a, dev, stream, allocated)
+    return out
+
+
+def moe_route_backward(d_scale: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor, *,
+                       score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                       out: Optional[torch.Tensor] = None, pdl: bool = True,
+                       stream: Optional[torch.cuda.Stream] = None, check: bool = True) -> torch.Tensor:
+    """The gradient of ``moe_route``'s weights to the logits ([T, E], the logits' dtype), the chosen experts held
+    fixed.  ``score``, ``renormalize`` and ``scale`` are the forward call's; the bias and the groups only choose and
+    have no gradient.  ``d_scale`` is [T, K] in any of the three types."""
+    if check:
+        if logits.dim() != 2 or expert_ids.dim() != 2:
+            raise ValueError("logits must be [T, E] and expert_ids [T, K]")
+        _check_tensor("logits", logits, logits.device, None, DTYPE, contiguous=False)
+    T, E = logits.shape
+    K = expert_ids.shape[1]
+    dev = logits.device
+    allocated = []
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
+        if stream is not None:
+            allocated.append(out)
+    if check:
+        _check_tensor("expert_ids", expert_ids, dev, (T, K), torch.int32)
+        _check_tensor("d_scale", d_scale, dev, (T, K), DTYPE)
+        _check_tensor("out", out, dev, (T, E), logits.dtype, contiguous=False)
+        if E > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+            raise ValueError("the experts of a token must be contiguous in logits and out")
+    a = _CRouteBackward(T, E, K, DTYPE[logits.dtype], DTYPE[d_scale.dtype], _choice(SCORE, "score", score),
+                        1 if renormalize else 0, scale, logits.data_ptr(), logits.stride(0) if T > 1 else E,
+                        expert_ids.data_ptr(), d_scale.data_ptr(), out.data_ptr(), out.stride(0) if T > 1 else E,
+                        _PDL if pdl else 0)
+    _enqueue(_lib.moe_route_backward, a, dev, stream, allocated)
+    return out
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Dispatch and the finalize's gradient
+# ----------------------------------------------------------------------------------------------------------------
+
+def _rows_like(num_rows, like, row_route, stream, allocated):
+    """Rows in expert order: the kernel zeroes those of no route when it has ``row_route``, else they start as zeros."""
+    make = torch.empty if row_route is not None else torch.zeros
+    rows = make(num_rows, *like.shape[1:], dtype=like.dtype, device=like.device)
+    if stream is not None:
+        allocated.append(rows)
+    return rows
+
+
+def moe_dispatch(x: torch.Tensor, perm_idx: torch.Tensor, num_rows: Optional[int] = None, *,
+                 row_route: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, pdl: bool = True,
+                 stream: Optional[torch.cuda.Stream] = None, check: bool = True) -> torch.Tensor:
+    """Copy each token's row ([T, n], any dtype, rows of a multiple of 16 bytes: activations, FP8 or NVFP4 codes,
+    block scales) to the rows of its routes: ``out[perm_idx[t, k]] = x[t]``.  Routes outside the rows are skipped; no
+    two routes may name the same row.  With ``row_route`` (as ``moe_route`` wrote it) the rows of no route are set to
+    zero; without it they are left as they were, or zeros in an allocated output.  ``num_rows`` defaults to the
+    length of ``row_route``.
+
+    The gradient to ``x`` is ``moe_finalize_routed([Partial(d_rows, perm_idx)])``."""
+    dev = x.device
+    if check:
+        if x.dim() != 2 or perm_idx.dim() != 2:
+            raise ValueError("x must be [T, n] and perm_idx [T, K]")
+        if not x.is_cuda:
+            raise ValueError(f"x is on {dev}; a CUDA device is wanted")
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+    allocated = []
+    if out is None:
+        if num_rows is None:
+            if row_route is None:
+                raise ValueError("num_rows, row_route or out must say how many rows there are")
+            num_rows = row_route.shape[0]
+        out = _rows_like(num_rows, x, row_route, stream, allocated)
+    n = out.shape[0]
+    if check:
+        _check_tensor("out", out, dev, (n if num_rows is None else num_rows, x.shape[1]), x.dtype)
+        _check_tensor("perm_idx", perm_idx, dev, (x.shape[0], perm_idx.shape[1]), torch.int32)
+        if row_route is not None:
+            _check_tensor("row_route", row_route, dev, (n,), torch.int32)
+    a = _CDispatch(x.shape[0], perm_idx.shape[1], x.shape[1] * x.element_size(), n, x.data_ptr(), perm_idx.data_ptr(),
+                   _ptr(row_route), out.data_ptr(), _PDL if pdl else 0)
+    _enqueue(_lib.moe_dispatch_rows, a, dev, stream, allocated)
+    return out
+
+
+def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling_factor: float = 1.0,
+                                 row_route: Optional[torch.Tensor] = None, d_gemm2: Optional[torch.Tensor] = None,
+                                 d_scale: Optional[torch.Tensor] = None, want_d_gemm2: bool = True,
+                                 want_d_scale: bool = True, pdl: bool = True,
+                                 stream: Optional[torch.cuda.Stream] = None, check: bool = True
+                                 ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """The gradient of one partial of ``moe_finalize_routed`` to its GEMM2 rows and its expert scales, given the
+    gradient ``d_out`` ([T, H]) of the finalized output; returns ``(d_gemm2, d_scale)`` (``want_*`` False leaves one
+    out).  The gradient of ``shared_out`` is ``d_out`` itself, and every partial of a rank sum has the same ``d_out``.
+    ``d_scale`` has the scales' dtype (fp32 where the partial has none).  No two routes may name the same row, and
+    outputs overlap no input.  With ``row_route`` the rows of no route get zeros; without it they are left as they
+    were, or zeros in an allocated output."""
+    dev = d_out.device
+    x, perm, scale = partial.gemm2_out, partial.perm_idx, partial.expert_scale
+    if check:
+        if d_out.dim() != 2 or perm.dim() != 2 or x.dim() != 2:
+            raise ValueError("d_out must be [T, H], gemm2_out [rows, H] and perm_idx [T, K]")
+    T, H = d_out.shape
+    K = perm.shape[1]
+    allocated = []
+    if d_gemm2 is None and want_d_gemm2:
+        d_gemm2 = _rows_like(x.shape[0], x, row_route, stream, allocated)
+    if d_scale is None and want_d_scale:
+        d_scale = torch.empty(T, K, dtype=torch.float32 if scale is None else scale.dtype, device=dev)
+        if stream is not None:
+            allocated.append(d_scale)
+    if check:
+        act = d_out.dtype
+        _check_tensor("d_out", d_out, dev, None, (torch.bfloat16, torch.float16))
+        _check_tensor("gemm2_out", x, dev, (x.shape[0], H), act)
+        _check_tensor("perm_idx", perm, dev, (T, K), torch.int32)
+        if scale is not None:
+            _check_tensor("expert_scale", scale, dev, (T, K), DTYPE)
+        if row_route is not None:
+            _check_tensor("row_route", row_route, dev, (x.shape[0],), torch.int32)
+        if d_gemm2 is not None:
+            _check_tensor("d_gemm2", d_gemm2, dev, (x.shape[0], H), act)
+        if d_scale is not None:
+            _check_tensor("d_scale", d_scale, dev, (T, K), torch.float32 if scale is None else scale.dtype)
+    a = _CRoutedBackward(T, H, K, DTYPE[d_out.dtype], 2 if scale is None else DTYPE[scale.dtype],
+                         routed_scaling_factor, x.shape[0], x.data_ptr(), perm.data_ptr(), _ptr(scale),
+                         _ptr(row_route), d_out.data_ptr(), _ptr(d_gemm2), _ptr(d_scale), _PDL if pdl else 0)
+    _enqueue(_lib.moe_routed_backward, a, dev, stream, allocated)
+    return d_gemm2, d_scale
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Per-head norm and rotation
+# ----------------------------------------------------------------------------------------------------------------
+
+def _heads(t):
+    """The strides of a dimension of one are never used, whatever torch reports."""
+    (T, heads, D), s = t.shape, t.stride()
+    return _CHeads(t.data_ptr(), s[0] if T > 1 else heads * D, s[1] if heads > 1 else D)
+
+
+def _check_heads(name, t, dev, shape, act):
+    _check_tensor(name, t, dev, shape, act, contiguous=False)
+    if t.stride(2) != 1:
+        raise ValueError(f"the elements of a head must be contiguous in {name}")
+
+
+def _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq):
+    dev, act = q.device, q.dtype
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, heads, D] and k [T, kv_heads, D]")
+    _check_heads("q", q, dev, None, (torch.bfloat16, torch.float16))
+    _check_heads("k", k, dev, (q.shape[0], k.shape[1], q.shape[2]), act)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_tensor(name, w, dev, (q.shape[2],), act)
+    _check_tensor("positions", positions, dev, (q.shape[0],), (torch.int32, torch.int64))
+    _check_tensor("inv_freq", inv_freq, dev, None, torch.float32)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rotated elements / 2]")
+
+
+def _head_args(q, k, q_weight, k_weight, positions, inv_freq, eps, style, rotary_scale, q_out, k_out, flags):
+    T, hq, D = q.shape
+    a = _CHeadNorm(T, hq, k.shape[1], D, 2 * inv_freq.shape[0], _choice(ROTARY_STYLE, "style", style),
+                   DTYPE.get(q.dtype, -1), eps, rotary_scale, _heads(q), _heads(k), _heads(q_out), _heads(k_out))
+    a.q_weight = _ptr(q_weight)
+    a.k_weight = _ptr(k_weight)
+    a.positions = positions.data_ptr()
+    a.inv_freq = inv_freq.data_ptr()
+    a.flags = flags | (_POSITIONS_64 if positions.dtype == torch.int64 else 0)
+    return a
+
+
+def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor],
+                     k_weight: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, *,
+                     eps: float = 1e-6, style: str = "half", rotary_scale: float = 1.0,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, pdl: bool = True,
+                     stream: Optional[torch.cuda.Stream] = None, check: bool = True
+                     ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMSNorm of every head of ``q`` ([T, heads, D]) and ``k`` ([T, kv_heads, D]) with the weights ([D], or None),
+    then the rotation of its first ``2 * len(inv_freq)`` elements by ``positions[t] * inv_freq[j]`` (times
+    ``rotary_scale``); one rounding at the end.  "half" pairs elements i and i + rot/2, "interleaved" 2i and 2i + 1.
+    D is a multiple of 16 up to 512; tokens and heads may be strided (views of a packed projection), by multiples of
+    8 elements.
+
+    ``positions`` is int32 or int64.  A negative position marks a padding token: it is not read, and its output
+    rows are left as they were (zeros in an allocated output).  ``q_out`` and ``k_out`` may be ``q`` and ``k``."""
+    flags = _PDL if pdl else 0
+    allocated = []
+    if check:
+        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq)
+    if (q_out is None) != (k_out is None):
+        raise ValueError("q_out and k_out are passed both or neither")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        flags |= _ZERO_PADDING
+        if stream is not None:
+            allocated += [q_out, k_out]
+    elif check:
+        _check_heads("q_out", q_out, q.device, q.shape, q.dtype)
+        _check_heads("k_out", k_out, q.device, k.shape, q.dtype)
+    a = _head_args(q, k, q_weight, k_weight, positions, inv_freq, eps, style, rotary_scale, q_out, k_out, flags)
+    _enqueue(_lib.moe_head_norm_rotary, a, q.device, stream, allocated)
+    return q_out, k_out
+
+
+def head_norm_rotary_workspace_bytes(T: int, q_heads: int, k_heads: int, D: int) -> int:
+    """Workspace of ``head_norm_rotary_backward`` when a weight gradient is asked."""
+    return _size(_lib.moe_head_norm_rotary_workspace_bytes(T, q_heads, k_heads, D))
+
+
+def head_norm_rotary_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                              q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                              positions: torch.Tensor, inv_freq: torch.Tensor, *, eps: float = 1e-6,
+                              style: str = "half", rotary_scale: float = 1.0, d_q: Optional[torch.Tensor] = None,
+                              d_k: Optional[torch.Tensor] = None, d_q_weight: Optional[torch.Tensor] = None,
+                              d_k_weight: Optional[torch.Tensor] = None, want_weights: bool = True,
+                              workspace: Optional[torch.Tensor] = None, pdl: bool = True,
+                              stream: Optional[torch.cuda.Stream] = None, check: bool = True):
+    """The gradients of ``head_norm_rotary``, given those of its outputs and its inputs as they were before the
+    call: ``(d_q, d_k, d_q_weight, d_k_weight)``, the weights' in FP32 ([D], summed over tokens and heads in a fixed
+    order; None where the weight is None or ``want_weights`` is False).  Padding tokens add nothing to the weights'
+    gradients, and their rows of ``d_q`` and ``d_k`` are set to zero.  ``d_q`` and ``d_k`` may be ``d_q_out`` and
+    ``d_k_out``, or ``q`` and ``k``.  ``workspace`` must not be shared by calls that may run at the same time."""
+    dev = q.device
+    allocated = []
+    if check:
+        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq)
+    if (d_q is None) != (d_k is None):
+        raise ValueError("d_q and d_k are passed both or neither")
+    if d_q is None:
+        d_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        d_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        allocated += [d_q, d_k]
+    D = q.shape[2]
+    if want_weights:
+        if d_q_weight is None and q_weight is not None:
+            d_q_weight = torch.empty(D, dtype=torch.float32, device=dev)
+            allocated.append(d_q_weight)
+        if d_k_weight is None and k_weight is not None:
+            d_k_weight = torch.empty(D, dtype=torch.float32, device=dev)
+            allocated.append(d_k_weight)
+    space = 0
+    if d_q_weight is not None or d_k_weight is not None:
+        if workspace is not None:
+            space = workspace.numel()
+        else:
+            space = head_norm_rotary_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], D)
+            workspace = torch.empty(space, dtype=torch.uint8, device=dev)
+            allocated.append(workspace)
+    if check:
+        _check_heads("d_q_out", d_q_out, dev, q.shape, q.dtype)
+        _check_heads("d_k_out", d_k_out, dev, k.shape, q.dtype)
+        _check_heads("d_q", d_q, dev, q.shape, q.dtype)
+        _check_heads("d_k", d_k, dev, k.shape, q.dtype)
+        for name, w in (("d_q_weight", d_q_weight), ("d_k_weight", d_k_weight)):
+            if w is not None:
+                _check_tensor(name, w, dev, (D,), torch.float32)
+        if workspace is not None:
+            _check_tensor("workspace", workspace, dev, None, torch.uint8)
+    a = _head_args(q, k, q_weight, k_weight, positions, inv_freq, eps, style, rotary_scale, d_q, d_k,
+                   _PDL if pdl else 0)
+    a.d_q_out, a.d_k_out = _heads(d_q_out), _heads(d_k_out)
+    a.d_q_weight, a.d_k_weight = _ptr(d_q_weight), _ptr(d_k_weight)
+    if space:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), space
+    _enqueue(_lib.moe_head_norm_rotary_backward, a, dev, stream, allocated)
+    return d_q, d_k, d_q_weight, d_k_weight
