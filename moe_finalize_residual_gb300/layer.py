@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -67,19 +68,45 @@ class _CHeadNorm(ctypes.Structure):
                 ("workspace_bytes", _L), ("flags", _U)]
 
 
+_CODES = {_I: "i", _L: "q", _F: "f", _P: "P", _U: "I"}
+
+
+def _packer(cls):
+    """Packs a structure's fields, nested ones in line: several times faster than filling a ctypes structure.  The
+    trailing "0q" pads to the structure's size (every one holds a 64-bit field)."""
+    def codes(c):
+        return "".join(codes(t) if issubclass(t, ctypes.Structure) else _CODES[t] for _, t in c._fields_)
+
+    packer = struct.Struct("@" + codes(cls) + "0q")
+    assert packer.size == ctypes.sizeof(cls), cls
+
+    def pack(*values):
+        try:
+            return packer.pack(*values)
+        except struct.error as e:
+            raise ValueError(f"an argument is not a number of its range: {e}") from None
+
+    return pack
+
+
+_pack_route, _pack_route_backward, _pack_dispatch = _packer(_CRoute), _packer(_CRouteBackward), _packer(_CDispatch)
+_pack_routed_backward, _pack_head_norm = _packer(_CRoutedBackward), _packer(_CHeadNorm)
+
 _lib = None
 _raise_status = None
+_current_device = torch.cuda.current_device
+# the current stream's handle without a Stream object, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _bind(lib, raise_status):
     """Called once by the package: the loaded library and its status check."""
     global _lib, _raise_status
     _lib, _raise_status = lib, raise_status
-    for name, args in (("moe_route", _CRoute), ("moe_route_backward", _CRouteBackward),
-                       ("moe_dispatch_rows", _CDispatch), ("moe_routed_backward", _CRoutedBackward),
-                       ("moe_head_norm_rotary", _CHeadNorm), ("moe_head_norm_rotary_backward", _CHeadNorm)):
+    for name in ("moe_route", "moe_route_backward", "moe_dispatch_rows", "moe_routed_backward",
+                 "moe_head_norm_rotary", "moe_head_norm_rotary_backward"):
         f = getattr(lib, name)
-        f.argtypes, f.restype = [ctypes.POINTER(args), _P], ctypes.c_int
+        f.argtypes, f.restype = [_P, _P], ctypes.c_int
     for name, n in (("moe_route_max_rows", 4), ("moe_route_workspace_bytes", 3),
                     ("moe_head_norm_rotary_workspace_bytes", 4)):
         f = getattr(lib, name)
@@ -87,7 +114,7 @@ def _bind(lib, raise_status):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _size(n: int) -> int:
@@ -101,6 +128,11 @@ def _choice(table, name, value):
         return table[value]
     except (KeyError, TypeError):
         raise ValueError(f"{name} is {value!r}; one of {', '.join(table)} is wanted") from None
+
+
+def _good(t, index, shape, dtype):
+    """A contiguous tensor of this shape and type on this device."""
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
 
 
 def _check_tensor(name, t, device, shape, dtypes, contiguous=True):
@@ -117,24 +149,24 @@ def _check_tensor(name, t, device, shape, dtypes, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _enqueue(fn, args, device, stream, allocated):
-    """Enqueue on ``stream`` with the tensors' device current.  What the binding allocated on the current stream
-    and hands to another one is recorded there, so that its memory is not given out again too early."""
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _enqueue(fn, args, device, stream, allocated)
+def _enqueue(fn, args, index, stream, allocated):
+    """Enqueue on ``stream`` with the tensors' device (``index``) current.  What the binding allocated on the current
+    stream for use on another one is ordered behind the current stream's work, and recorded on the other, so that
+    its memory is not given out again too early."""
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return _enqueue(fn, args, index, stream, allocated)
     if stream is None:
-        handle = torch.cuda.current_stream().cuda_stream
+        status = fn(args, _raw_stream(index))
     else:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}; the tensors are on {device}")
-        handle = stream.cuda_stream
-        if handle != torch.cuda.current_stream().cuda_stream:
-            # allocated memory may still be in use by work queued on the current stream before it was freed
-            stream.wait_stream(torch.cuda.current_stream()) if allocated else None
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}; the tensors are on cuda:{index}")
+        current = torch.cuda.current_stream()
+        if allocated and stream != current:
+            stream.wait_stream(current)
             for t in allocated:
                 t.record_stream(stream)
-    status = fn(ctypes.byref(args), handle)
+        status = fn(args, stream.cuda_stream)
     if status != 0:
         _raise_status(status)
 
@@ -182,41 +214,48 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     The expert order makes each expert's rows start at a multiple of ``row_align``.  ``out`` takes the outputs'
     buffers (``out.expert_offsets`` None: no order, whatever ``order`` says); ``row_route`` must hold at least
     ``moe_route_max_rows`` rows.  ``workspace`` must not be shared by calls that may run at the same time."""
-    if check:
-        if logits.dim() != 2:
-            raise ValueError("logits must be [T, E]")
-        _check_tensor("logits", logits, logits.device, None, DTYPE, contiguous=False)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    dev = logits.device
-    stride = logits.stride(0) if T > 1 else E
-    if check and E > 1 and logits.stride(1) != 1:
-        raise ValueError("the experts of a token must be contiguous in logits")
+    index = logits.get_device()
+    stride, inner = logits.stride()
+    if check:
+        if index < 0 or logits.dtype not in DTYPE:
+            _check_tensor("logits", logits, logits.device, None, DTYPE, contiguous=False)
+        if inner != 1 and E > 1:
+            raise ValueError("the experts of a token must be contiguous in logits")
     allocated = []
     if out is None:
+        dev = logits.device
         if scale_dtype not in DTYPE:
             raise ValueError(f"scale_dtype {scale_dtype} is not supported (fp32, bf16 or fp16)")
         out = Routing(torch.empty(T, top_k, dtype=torch.int32, device=dev),
                       torch.empty(T, top_k, dtype=scale_dtype, device=dev))
+        allocated += [out.expert_ids, out.expert_scale]
         if order:
             out.perm_idx = torch.empty_like(out.expert_ids)
             out.row_route = torch.empty(moe_route_max_rows(T, top_k, E, row_align), dtype=torch.int32, device=dev)
             out.expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
             out.expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
-        allocated = [t for t in dataclasses.astuple(out) if t is not None] if stream is not None else []
-    ordered = out.expert_offsets is not None
+            allocated += [out.perm_idx, out.row_route, out.expert_offsets, out.expert_counts]
+    ids, scales, perm, rows, offsets, counts = (out.expert_ids, out.expert_scale, out.perm_idx, out.row_route,
+                                                out.expert_offsets, out.expert_counts)
+    ordered = offsets is not None
     if check:
-        if bias is not None:
-            _check_tensor("bias", bias, dev, (E,), torch.float32)
         shape = (T, top_k)
-        _check_tensor("expert_ids", out.expert_ids, dev, shape, torch.int32)
-        _check_tensor("expert_scale", out.expert_scale, dev, shape, DTYPE)
-        if ordered:
-            _check_tensor("perm_idx", out.perm_idx, dev, shape, torch.int32)
-            _check_tensor("row_route", out.row_route, dev, None, torch.int32)
-            _check_tensor("expert_offsets", out.expert_offsets, dev, (E + 1,), torch.int32)
-            _check_tensor("expert_counts", out.expert_counts, dev, (E,), torch.int32)
+        if bias is not None and not _good(bias, index, (E,), torch.float32):
+            _check_tensor("bias", bias, logits.device, (E,), torch.float32)
+        if not (_good(ids, index, shape, torch.int32) and _good(scales, index, shape, scales.dtype) and scales.dtype in DTYPE):
+            _check_tensor("expert_ids", ids, logits.device, shape, torch.int32)
+            _check_tensor("expert_scale", scales, logits.device, shape, DTYPE)
+        if ordered and not (_good(perm, index, shape, torch.int32) and _good(rows, index, rows.shape, torch.int32)
+                            and _good(offsets, index, (E + 1,), torch.int32) and _good(counts, index, (E,), torch.int32)):
+            _check_tensor("perm_idx", perm, logits.device, shape, torch.int32)
+            _check_tensor("row_route", rows, logits.device, None, torch.int32)
+            _check_tensor("expert_offsets", offsets, logits.device, (E + 1,), torch.int32)
+            _check_tensor("expert_counts", counts, logits.device, (E,), torch.int32)
         if workspace is not None:
-            _check_tensor("workspace", workspace, dev, None, torch.uint8)
+            _check_tensor("workspace", workspace, logits.device, None, torch.uint8)
     space = 0
     if ordered:
         if workspace is not None:
@@ -224,22 +263,17 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
         else:
             space = moe_route_workspace_bytes(T, top_k, E)
             if space:
-                workspace = torch.empty(space, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(space, dtype=torch.uint8, device=logits.device)
                 allocated.append(workspace)
-    a = _CRoute(T, E, top_k, DTYPE[logits.dtype], DTYPE[out.expert_scale.dtype], _choice(SCORE, "score", score),
-                num_groups, topk_groups, _choice(GROUP_SCORE, "group_score", group_score), 1 if renormalize else 0,
-                row_align, scale, logits.data_ptr(), stride, _ptr(bias), out.expert_ids.data_ptr(),
-                out.expert_scale.data_ptr())
-    if ordered:
-        a.perm_idx = out.perm_idx.data_ptr()
-        a.row_route = out.row_route.data_ptr()
-        a.num_rows = out.row_route.numel()
-        a.expert_offsets = out.expert_offsets.data_ptr()
-        a.expert_counts = out.expert_counts.data_ptr()
-        a.workspace = _ptr(workspace)
-        a.workspace_bytes = space
-    a.flags = _PDL if pdl else 0
-    _enqueue(_lib.moe_route, a, dev, stream, allocated)
+        extra = (perm.data_ptr(), rows.data_ptr(), rows.numel(), offsets.data_ptr(), counts.data_ptr(),
+                 workspace.data_ptr() if space else 0, space)
+    else:
+        extra = (0, 0, 0, 0, 0, 0, 0)
+    args = _pack_route(T, E, top_k, DTYPE[logits.dtype], DTYPE[scales.dtype], _choice(SCORE, "score", score), num_groups,
+                       topk_groups, _choice(GROUP_SCORE, "group_score", group_score), 1 if renormalize else 0, row_align,
+                       scale, logits.data_ptr(), stride if T > 1 else E, 0 if bias is None else bias.data_ptr(),
+                       ids.data_ptr(), scales.data_ptr(), *extra, _PDL if pdl else 0)
+    _enqueue(_lib.moe_route, args, index, stream, allocated)
     return out
 
 
@@ -250,29 +284,31 @@ def moe_route_backward(d_scale: torch.Tensor, logits: torch.Tensor, expert_ids: 
     """The gradient of ``moe_route``'s weights to the logits ([T, E], the logits' dtype), the chosen experts held
     fixed.  ``score``, ``renormalize`` and ``scale`` are the forward call's; the bias and the groups only choose and
     have no gradient.  ``d_scale`` is [T, K] in any of the three types."""
-    if check:
-        if logits.dim() != 2 or expert_ids.dim() != 2:
-            raise ValueError("logits must be [T, E] and expert_ids [T, K]")
-        _check_tensor("logits", logits, logits.device, None, DTYPE, contiguous=False)
+    if logits.dim() != 2 or expert_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and expert_ids [T, K]")
     T, E = logits.shape
     K = expert_ids.shape[1]
-    dev = logits.device
+    index, act = logits.get_device(), logits.dtype
     allocated = []
     if out is None:
-        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
-        if stream is not None:
-            allocated.append(out)
+        out = torch.empty(T, E, dtype=act, device=logits.device)
+        allocated.append(out)
+    stride, inner = logits.stride()
     if check:
-        _check_tensor("expert_ids", expert_ids, dev, (T, K), torch.int32)
-        _check_tensor("d_scale", d_scale, dev, (T, K), DTYPE)
-        _check_tensor("out", out, dev, (T, E), logits.dtype, contiguous=False)
-        if E > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+        dev, shape = logits.device, (T, K)
+        if index < 0 or act not in DTYPE:
+            _check_tensor("logits", logits, dev, None, DTYPE, contiguous=False)
+        if not (_good(expert_ids, index, shape, torch.int32) and _good(d_scale, index, shape, d_scale.dtype) and d_scale.dtype in DTYPE):
+            _check_tensor("expert_ids", expert_ids, dev, shape, torch.int32)
+            _check_tensor("d_scale", d_scale, dev, shape, DTYPE)
+        _check_tensor("out", out, dev, (T, E), act, contiguous=False)
+        if E > 1 and (inner != 1 or out.stride(1) != 1):
             raise ValueError("the experts of a token must be contiguous in logits and out")
-    a = _CRouteBackward(T, E, K, DTYPE[logits.dtype], DTYPE[d_scale.dtype], _choice(SCORE, "score", score),
-                        1 if renormalize else 0, scale, logits.data_ptr(), logits.stride(0) if T > 1 else E,
-                        expert_ids.data_ptr(), d_scale.data_ptr(), out.data_ptr(), out.stride(0) if T > 1 else E,
-                        _PDL if pdl else 0)
-    _enqueue(_lib.moe_route_backward, a, dev, stream, allocated)
+    args = _pack_route_backward(T, E, K, DTYPE[act], DTYPE[d_scale.dtype], _choice(SCORE, "score", score),
+                                1 if renormalize else 0, scale, logits.data_ptr(), stride if T > 1 else E,
+                                expert_ids.data_ptr(), d_scale.data_ptr(), out.data_ptr(), out.stride(0) if T > 1 else E,
+                                _PDL if pdl else 0)
+    _enqueue(_lib.moe_route_backward, args, index, stream, allocated)
     return out
 
 
@@ -280,12 +316,11 @@ def moe_route_backward(d_scale: torch.Tensor, logits: torch.Tensor, expert_ids: 
 # Dispatch and the finalize's gradient
 # ----------------------------------------------------------------------------------------------------------------
 
-def _rows_like(num_rows, like, row_route, stream, allocated):
+def _rows_like(num_rows, like, row_route, allocated):
     """Rows in expert order: the kernel zeroes those of no route when it has ``row_route``, else they start as zeros."""
     make = torch.empty if row_route is not None else torch.zeros
-    rows = make(num_rows, *like.shape[1:], dtype=like.dtype, device=like.device)
-    if stream is not None:
-        allocated.append(rows)
+    rows = make(num_rows, like.shape[1], dtype=like.dtype, device=like.device)
+    allocated.append(rows)
     return rows
 
 
@@ -299,30 +334,30 @@ def moe_dispatch(x: torch.Tensor, perm_idx: torch.Tensor, num_rows: Optional[int
     length of ``row_route``.
 
     The gradient to ``x`` is ``moe_finalize_routed([Partial(d_rows, perm_idx)])``."""
-    dev = x.device
-    if check:
-        if x.dim() != 2 or perm_idx.dim() != 2:
-            raise ValueError("x must be [T, n] and perm_idx [T, K]")
-        if not x.is_cuda:
-            raise ValueError(f"x is on {dev}; a CUDA device is wanted")
-        if not x.is_contiguous():
-            raise ValueError("x must be contiguous")
+    if x.dim() != 2 or perm_idx.dim() != 2:
+        raise ValueError("x must be [T, n] and perm_idx [T, K]")
+    index = x.get_device()
+    T, n = x.shape
+    if check and (index < 0 or not x.is_contiguous()):
+        _check_tensor("x", x, x.device, None, x.dtype)
     allocated = []
     if out is None:
         if num_rows is None:
             if row_route is None:
                 raise ValueError("num_rows, row_route or out must say how many rows there are")
             num_rows = row_route.shape[0]
-        out = _rows_like(num_rows, x, row_route, stream, allocated)
-    n = out.shape[0]
+        out = _rows_like(num_rows, x, row_route, allocated)
+    rows = out.shape[0] if num_rows is None else num_rows
+    K = perm_idx.shape[1]
     if check:
-        _check_tensor("out", out, dev, (n if num_rows is None else num_rows, x.shape[1]), x.dtype)
-        _check_tensor("perm_idx", perm_idx, dev, (x.shape[0], perm_idx.shape[1]), torch.int32)
-        if row_route is not None:
-            _check_tensor("row_route", row_route, dev, (n,), torch.int32)
-    a = _CDispatch(x.shape[0], perm_idx.shape[1], x.shape[1] * x.element_size(), n, x.data_ptr(), perm_idx.data_ptr(),
-                   _ptr(row_route), out.data_ptr(), _PDL if pdl else 0)
-    _enqueue(_lib.moe_dispatch_rows, a, dev, stream, allocated)
+        if not (_good(out, index, (rows, n), x.dtype) and _good(perm_idx, index, (T, K), torch.int32)):
+            _check_tensor("out", out, x.device, (rows, n), x.dtype)
+            _check_tensor("perm_idx", perm_idx, x.device, (T, K), torch.int32)
+        if row_route is not None and not _good(row_route, index, (rows,), torch.int32):
+            _check_tensor("row_route", row_route, x.device, (rows,), torch.int32)
+    args = _pack_dispatch(T, K, n * x.element_size(), rows, x.data_ptr(), perm_idx.data_ptr(), _ptr(row_route),
+                          out.data_ptr(), _PDL if pdl else 0)
+    _enqueue(_lib.moe_dispatch_rows, args, index, stream, allocated)
     return out
 
 
@@ -338,37 +373,38 @@ def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling
     ``d_scale`` has the scales' dtype (fp32 where the partial has none).  No two routes may name the same row, and
     outputs overlap no input.  With ``row_route`` the rows of no route get zeros; without it they are left as they
     were, or zeros in an allocated output."""
-    dev = d_out.device
     x, perm, scale = partial.gemm2_out, partial.perm_idx, partial.expert_scale
-    if check:
-        if d_out.dim() != 2 or perm.dim() != 2 or x.dim() != 2:
-            raise ValueError("d_out must be [T, H], gemm2_out [rows, H] and perm_idx [T, K]")
+    if d_out.dim() != 2 or perm.dim() != 2 or x.dim() != 2:
+        raise ValueError("d_out must be [T, H], gemm2_out [rows, H] and perm_idx [T, K]")
     T, H = d_out.shape
-    K = perm.shape[1]
+    K, rows = perm.shape[1], x.shape[0]
+    index, act = d_out.get_device(), d_out.dtype
+    sdt = torch.float32 if scale is None else scale.dtype
     allocated = []
     if d_gemm2 is None and want_d_gemm2:
-        d_gemm2 = _rows_like(x.shape[0], x, row_route, stream, allocated)
+        d_gemm2 = _rows_like(rows, x, row_route, allocated)
     if d_scale is None and want_d_scale:
-        d_scale = torch.empty(T, K, dtype=torch.float32 if scale is None else scale.dtype, device=dev)
-        if stream is not None:
-            allocated.append(d_scale)
+        d_scale = torch.empty(T, K, dtype=sdt, device=d_out.device)
+        allocated.append(d_scale)
     if check:
-        act = d_out.dtype
-        _check_tensor("d_out", d_out, dev, None, (torch.bfloat16, torch.float16))
-        _check_tensor("gemm2_out", x, dev, (x.shape[0], H), act)
-        _check_tensor("perm_idx", perm, dev, (T, K), torch.int32)
-        if scale is not None:
-            _check_tensor("expert_scale", scale, dev, (T, K), DTYPE)
-        if row_route is not None:
-            _check_tensor("row_route", row_route, dev, (x.shape[0],), torch.int32)
-        if d_gemm2 is not None:
-            _check_tensor("d_gemm2", d_gemm2, dev, (x.shape[0], H), act)
-        if d_scale is not None:
-            _check_tensor("d_scale", d_scale, dev, (T, K), torch.float32 if scale is None else scale.dtype)
-    a = _CRoutedBackward(T, H, K, DTYPE[d_out.dtype], 2 if scale is None else DTYPE[scale.dtype],
-                         routed_scaling_factor, x.shape[0], x.data_ptr(), perm.data_ptr(), _ptr(scale),
-                         _ptr(row_route), d_out.data_ptr(), _ptr(d_gemm2), _ptr(d_scale), _PDL if pdl else 0)
-    _enqueue(_lib.moe_routed_backward, a, dev, stream, allocated)
+        dev, shape = d_out.device, (T, K)
+        if index < 0 or (act is not torch.bfloat16 and act is not torch.float16) or not d_out.is_contiguous():
+            _check_tensor("d_out", d_out, dev, None, (torch.bfloat16, torch.float16))
+        if not (_good(x, index, (rows, H), act) and _good(perm, index, shape, torch.int32)):
+            _check_tensor("gemm2_out", x, dev, (rows, H), act)
+            _check_tensor("perm_idx", perm, dev, shape, torch.int32)
+        if scale is not None and not (sdt in DTYPE and _good(scale, index, shape, sdt)):
+            _check_tensor("expert_scale", scale, dev, shape, DTYPE)
+        if row_route is not None and not _good(row_route, index, (rows,), torch.int32):
+            _check_tensor("row_route", row_route, dev, (rows,), torch.int32)
+        if d_gemm2 is not None and not _good(d_gemm2, index, (rows, H), act):
+            _check_tensor("d_gemm2", d_gemm2, dev, (rows, H), act)
+        if d_scale is not None and not _good(d_scale, index, shape, sdt):
+            _check_tensor("d_scale", d_scale, dev, shape, sdt)
+    args = _pack_routed_backward(T, H, K, DTYPE[act], DTYPE[sdt], routed_scaling_factor, rows, x.data_ptr(), perm.data_ptr(),
+                                 _ptr(scale), _ptr(row_route), d_out.data_ptr(), _ptr(d_gemm2), _ptr(d_scale),
+                                 _PDL if pdl else 0)
+    _enqueue(_lib.moe_routed_backward, args, index, stream, allocated)
     return d_gemm2, d_scale
 
 
@@ -376,10 +412,10 @@ def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling
 # Per-head norm and rotation
 # ----------------------------------------------------------------------------------------------------------------
 
-def _heads(t):
-    """The strides of a dimension of one are never used, whatever torch reports."""
-    (T, heads, D), s = t.shape, t.stride()
-    return _CHeads(t.data_ptr(), s[0] if T > 1 else heads * D, s[1] if heads > 1 else D)
+def _heads(t, T, heads, D):
+    """Pointer and strides (those of a dimension of one are never used, whatever torch reports)."""
+    s = t.stride()
+    return t.data_ptr(), s[0] if T > 1 else heads * D, s[1] if heads > 1 else D
 
 
 def _check_heads(name, t, dev, shape, act):
@@ -388,31 +424,26 @@ def _check_heads(name, t, dev, shape, act):
         raise ValueError(f"the elements of a head must be contiguous in {name}")
 
 
-def _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq):
-    dev, act = q.device, q.dtype
+def _good_heads(t, index, shape, act):
+    return t.dtype is act and t.get_device() == index and t.shape == shape and t.stride(2) == 1
+
+
+def _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, heads, D] and k [T, kv_heads, D]")
-    _check_heads("q", q, dev, None, (torch.bfloat16, torch.float16))
-    _check_heads("k", k, dev, (q.shape[0], k.shape[1], q.shape[2]), act)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_tensor(name, w, dev, (q.shape[2],), act)
-    _check_tensor("positions", positions, dev, (q.shape[0],), (torch.int32, torch.int64))
-    _check_tensor("inv_freq", inv_freq, dev, None, torch.float32)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rotated elements / 2]")
-
-
-def _head_args(q, k, q_weight, k_weight, positions, inv_freq, eps, style, rotary_scale, q_out, k_out, flags):
-    T, hq, D = q.shape
-    a = _CHeadNorm(T, hq, k.shape[1], D, 2 * inv_freq.shape[0], _choice(ROTARY_STYLE, "style", style),
-                   DTYPE.get(q.dtype, -1), eps, rotary_scale, _heads(q), _heads(k), _heads(q_out), _heads(k_out))
-    a.q_weight = _ptr(q_weight)
-    a.k_weight = _ptr(k_weight)
-    a.positions = positions.data_ptr()
-    a.inv_freq = inv_freq.data_ptr()
-    a.flags = flags | (_POSITIONS_64 if positions.dtype == torch.int64 else 0)
-    return a
+    T, _, D = q.shape
+    if not (index >= 0 and (act is torch.bfloat16 or act is torch.float16) and q.stride(2) == 1
+            and _good_heads(k, index, (T, k.shape[1], D), act)):
+        _check_heads("q", q, q.device, None, (torch.bfloat16, torch.float16))
+        _check_heads("k", k, q.device, (T, k.shape[1], D), act)
+    if q_weight is not None and not _good(q_weight, index, (D,), act):
+        _check_tensor("q_weight", q_weight, q.device, (D,), act)
+    if k_weight is not None and not _good(k_weight, index, (D,), act):
+        _check_tensor("k_weight", k_weight, q.device, (D,), act)
+    if not (positions.dtype is torch.int32 and _good(positions, index, (T,), torch.int32)):
+        _check_tensor("positions", positions, q.device, (T,), (torch.int32, torch.int64))
+    if not _good(inv_freq, index, (inv_freq.numel(),), torch.float32):
+        _check_tensor("inv_freq", inv_freq, q.device, (inv_freq.numel(),), torch.float32)
 
 
 def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -431,21 +462,28 @@ def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     rows are left as they were (zeros in an allocated output).  ``q_out`` and ``k_out`` may be ``q`` and ``k``."""
     flags = _PDL if pdl else 0
     allocated = []
+    index, act = q.get_device(), q.dtype
     if check:
-        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq)
+        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act)
     if (q_out is None) != (k_out is None):
         raise ValueError("q_out and k_out are passed both or neither")
+    T, hq, D = q.shape
+    hk = k.shape[1]
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(T, hq, D, dtype=act, device=q.device)
+        k_out = torch.empty(T, hk, D, dtype=act, device=q.device)
         flags |= _ZERO_PADDING
-        if stream is not None:
-            allocated += [q_out, k_out]
-    elif check:
-        _check_heads("q_out", q_out, q.device, q.shape, q.dtype)
-        _check_heads("k_out", k_out, q.device, k.shape, q.dtype)
-    a = _head_args(q, k, q_weight, k_weight, positions, inv_freq, eps, style, rotary_scale, q_out, k_out, flags)
-    _enqueue(_lib.moe_head_norm_rotary, a, q.device, stream, allocated)
+        allocated += [q_out, k_out]
+    elif check and not (_good_heads(q_out, index, (T, hq, D), act) and _good_heads(k_out, index, (T, hk, D), act)):
+        _check_heads("q_out", q_out, q.device, (T, hq, D), act)
+        _check_heads("k_out", k_out, q.device, (T, hk, D), act)
+    if positions.dtype is torch.int64:
+        flags |= _POSITIONS_64
+    args = _pack_head_norm(T, hq, hk, D, 2 * inv_freq.numel(), _choice(ROTARY_STYLE, "style", style), DTYPE[act], eps,
+                           rotary_scale, *_heads(q, T, hq, D), *_heads(k, T, hk, D), *_heads(q_out, T, hq, D),
+                           *_heads(k_out, T, hk, D), 0, 0, 0, 0, 0, 0, _ptr(q_weight), _ptr(k_weight),
+                           positions.data_ptr(), inv_freq.data_ptr(), 0, 0, 0, 0, flags)
+    _enqueue(_lib.moe_head_norm_rotary, args, index, stream, allocated)
     return q_out, k_out
 
 
@@ -467,17 +505,20 @@ def head_norm_rotary_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: t
     order; None where the weight is None or ``want_weights`` is False).  Padding tokens add nothing to the weights'
     gradients, and their rows of ``d_q`` and ``d_k`` are set to zero.  ``d_q`` and ``d_k`` may be ``d_q_out`` and
     ``d_k_out``, or ``q`` and ``k``.  ``workspace`` must not be shared by calls that may run at the same time."""
-    dev = q.device
+    flags = _PDL if pdl else 0
     allocated = []
+    index, act = q.get_device(), q.dtype
     if check:
-        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq)
+        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act)
     if (d_q is None) != (d_k is None):
         raise ValueError("d_q and d_k are passed both or neither")
+    dev = q.device
+    T, hq, D = q.shape
+    hk = k.shape[1]
     if d_q is None:
-        d_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        d_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        d_q = torch.empty(T, hq, D, dtype=act, device=dev)
+        d_k = torch.empty(T, hk, D, dtype=act, device=dev)
         allocated += [d_q, d_k]
-    D = q.shape[2]
     if want_weights:
         if d_q_weight is None and q_weight is not None:
             d_q_weight = torch.empty(D, dtype=torch.float32, device=dev)
@@ -488,26 +529,31 @@ def head_norm_rotary_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: t
     space = 0
     if d_q_weight is not None or d_k_weight is not None:
         if workspace is not None:
+            if check:
+                _check_tensor("workspace", workspace, dev, None, torch.uint8)
             space = workspace.numel()
         else:
-            space = head_norm_rotary_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], D)
+            space = head_norm_rotary_workspace_bytes(T, hq, hk, D)
             workspace = torch.empty(space, dtype=torch.uint8, device=dev)
             allocated.append(workspace)
     if check:
-        _check_heads("d_q_out", d_q_out, dev, q.shape, q.dtype)
-        _check_heads("d_k_out", d_k_out, dev, k.shape, q.dtype)
-        _check_heads("d_q", d_q, dev, q.shape, q.dtype)
-        _check_heads("d_k", d_k, dev, k.shape, q.dtype)
-        for name, w in (("d_q_weight", d_q_weight), ("d_k_weight", d_k_weight)):
-            if w is not None:
-                _check_tensor(name, w, dev, (D,), torch.float32)
-        if workspace is not None:
-            _check_tensor("workspace", workspace, dev, None, torch.uint8)
-    a = _head_args(q, k, q_weight, k_weight, positions, inv_freq, eps, style, rotary_scale, d_q, d_k,
-                   _PDL if pdl else 0)
-    a.d_q_out, a.d_k_out = _heads(d_q_out), _heads(d_k_out)
-    a.d_q_weight, a.d_k_weight = _ptr(d_q_weight), _ptr(d_k_weight)
-    if space:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), space
-    _enqueue(_lib.moe_head_norm_rotary_backward, a, dev, stream, allocated)
+        sq, sk = (T, hq, D), (T, hk, D)
+        if not (_good_heads(d_q_out, index, sq, act) and _good_heads(d_k_out, index, sk, act)
+                and _good_heads(d_q, index, sq, act) and _good_heads(d_k, index, sk, act)):
+            _check_heads("d_q_out", d_q_out, dev, sq, act)
+            _check_heads("d_k_out", d_k_out, dev, sk, act)
+            _check_heads("d_q", d_q, dev, sq, act)
+            _check_heads("d_k", d_k, dev, sk, act)
+        if d_q_weight is not None and not _good(d_q_weight, index, (D,), torch.float32):
+            _check_tensor("d_q_weight", d_q_weight, dev, (D,), torch.float32)
+        if d_k_weight is not None and not _good(d_k_weight, index, (D,), torch.float32):
+            _check_tensor("d_k_weight", d_k_weight, dev, (D,), torch.float32)
+    if positions.dtype is torch.int64:
+        flags |= _POSITIONS_64
+    args = _pack_head_norm(T, hq, hk, D, 2 * inv_freq.numel(), _choice(ROTARY_STYLE, "style", style), DTYPE[act], eps,
+                           rotary_scale, *_heads(q, T, hq, D), *_heads(k, T, hk, D), *_heads(d_q, T, hq, D),
+                           *_heads(d_k, T, hk, D), *_heads(d_q_out, T, hq, D), *_heads(d_k_out, T, hk, D),
+                           _ptr(q_weight), _ptr(k_weight), positions.data_ptr(), inv_freq.data_ptr(), _ptr(d_q_weight),
+                           _ptr(d_k_weight), workspace.data_ptr() if space else 0, space, flags)
+    _enqueue(_lib.moe_head_norm_rotary_backward, args, index, stream, allocated)
     return d_q, d_k, d_q_weight, d_k_weight
