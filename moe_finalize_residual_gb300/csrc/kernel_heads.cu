@@ -5,9 +5,10 @@
 // the same lane:
 //   half style         vectors p and p + rot/16 (elements i and i + rot/2), then the unrotated rest in twos
 //   interleaved style  vectors 2p and 2p + 1 (neighbouring elements)
-// so the rotation needs no exchange, and a head's sum of squares takes log2(G) shuffles.  A lane turns the
-// same 8 pairs of every head of a token, so their sines and cosines are computed once a token and kept in
-// registers.  Each warp walks a contiguous range of (token, head) items, its groups on neighbouring heads.
+// so the rotation needs no exchange, and a head's sum of squares takes log2(G) shuffles.  The elements are
+// kept as the pairs' first and second elements (`a` and `b`), two to a packed FP32 register pair, so that all
+// the arithmetic runs on packed operations.  A lane turns the same 8 pairs of every head of a token: their
+// sines and cosines are computed once a token and kept in registers.
 //
 // The angle position * inv_freq is reduced without error: inv_freq / (2 pi) is held as a 64-bit fraction of
 // a turn (24-bit significand times 1 / (2 pi) to 64 bits), so the product with the position, modulo 2^64, is
@@ -23,11 +24,21 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kHeadThreads = 256;
 constexpr int kHeadWarps = kHeadThreads / 32;
 
+// How a launch cuts its work.  A warp's groups take `1 << gpt_log2` heads of a token at a time (a round) and
+// the warp as many tokens as that leaves groups for; a token's rounds are cut into `splits` ranges.  A task is a
+// block of tokens and a range.
+struct HeadCut {
+  int gpt_log2;
+  int splits;
+  int64_t tasks;
+};
+
 struct HeadParams {
   mfr_head_norm_args a;
-  int64_t items;     // (token, head) pairs of this launch
-  int64_t per_warp;  // items of one warp, a multiple of its groups
+  HeadCut cut;       // forward: over the heads of both kinds; backward: the queries'
+  HeadCut key_cut;   // backward: the keys'
   int q_blocks;      // backward: CTAs [0, q_blocks) take the queries, the rest the keys
+  int blocks;        // backward: CTAs, each leaving a row of partial weight gradients
 };
 
 // inv_freq / (2 pi) as a fraction of a turn times 2^64, modulo 2^64.
@@ -54,42 +65,46 @@ __device__ __forceinline__ uint64_t turn_of(float inv_freq) {
 // Where a lane's two vectors lie, and its 8 pairs.
 struct LaneMap {
   int off_a, off_b;  // element offsets of the vectors
-  int pair0;         // first pair (half: pairs pair0..pair0+7; interleaved: the same)
+  int pair0;         // the first of its 8 pairs
   int pairs;         // how many of the 8 are rotated
 };
 
 __device__ __forceinline__ LaneMap lane_map(int p, int rot, int style) {
   LaneMap m;
   m.pair0 = 8 * p;
-  if (style == MFR_ROTARY_INTERLEAVED) {
+  if (style == MFR_ROTARY_INTERLEAVED || 16 * p >= rot) {
     m.off_a = 16 * p;
     m.off_b = 16 * p + 8;
-  } else if (16 * p < rot) {
+  } else {
     m.off_a = 8 * p;
     m.off_b = 8 * p + rot / 2;
-  } else {
-    m.off_a = 16 * p;  // rot + 16 (p - rot/16)
-    m.off_b = 16 * p + 8;
   }
   m.pairs = min(8, max(0, rot / 2 - 8 * p));
   return m;
 }
 
-// Sines and cosines of a lane's pairs at a position, times rotary_scale; (1, 0) for unrotated pairs.
-__device__ __forceinline__ void turns(const mfr_head_norm_args& a, const LaneMap& m, int64_t pos, float cs[8], float sn[8]) {
+// Fills the CTA's table of turns (shared memory, rot / 2 entries).
+__device__ __forceinline__ void fill_turns(const mfr_head_norm_args& a, uint64_t* table) {
+  for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x) table[i] = turn_of(a.inv_freq[i]);
+  __syncthreads();
+}
+
+// Sines and cosines of a lane's pairs at a position, times rotary_scale; (0, 1) for unrotated pairs.
+__device__ __forceinline__ void turns(const mfr_head_norm_args& a, const uint64_t* table, const LaneMap& m, int64_t pos,
+                                      float2 (&cs)[4], float2 (&sn)[4]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    cs[i] = 1.0f;
-    sn[i] = 0.0f;
+    float c = 1.0f, s = 0.0f;
     if (i < m.pairs) {
-      const uint64_t u = turn_of(a.inv_freq[m.pair0 + i]) * static_cast<uint64_t>(pos);
+      const uint64_t u = table[m.pair0 + i] * static_cast<uint64_t>(pos);
       // the nearest 2^-32 turn, as a half turn in [-1, 1)
       const float h = static_cast<float>(static_cast<int32_t>((u + 0x80000000ULL) >> 32)) * 4.656612873077393e-10f;
-      float s, c;
       sincospif(h, &s, &c);
-      cs[i] = c * a.rotary_scale;
-      sn[i] = s * a.rotary_scale;
+      c *= a.rotary_scale;
+      s *= a.rotary_scale;
     }
+    (i % 2 ? cs[i / 2].y : cs[i / 2].x) = c;
+    (i % 2 ? sn[i / 2].y : sn[i / 2].x) = s;
   }
 }
 
@@ -98,42 +113,84 @@ __device__ __forceinline__ int64_t position_of(const mfr_head_norm_args& a, int6
                                            : static_cast<const int32_t*>(a.positions)[t];
 }
 
-template <typename A>
-__device__ __forceinline__ void load16(const uint8_t* base, int off_a, int off_b, bool on, float v[16]) {
-  unpack8<A>(on ? ldg16(base + 2 * off_a) : make_uint4(0, 0, 0, 0), v);
-  unpack8<A>(on ? ldg16(base + 2 * off_b) : make_uint4(0, 0, 0, 0), v + 8);
+// A lane's 16 elements of a head as they lie in memory, and as its pairs' first and second elements.
+struct Raw {
+  uint4 a, b;
+};
+struct Pairs {
+  float2 a[4], b[4];
+};
+
+__device__ __forceinline__ Raw load_raw(const uint8_t* p, const LaneMap& m, bool on) {
+  Raw r;
+  r.a = on ? ldg16(p + 2 * m.off_a) : make_uint4(0, 0, 0, 0);
+  r.b = on ? ldg16(p + 2 * m.off_b) : make_uint4(0, 0, 0, 0);
+  return r;
 }
 
-template <typename A>
-__device__ __forceinline__ void store16(uint8_t* base, int off_a, int off_b, const float v[16]) {
-  *reinterpret_cast<uint4*>(base + 2 * off_a) =
-      make_uint4(Act<A>::pack(v[0], v[1]), Act<A>::pack(v[2], v[3]), Act<A>::pack(v[4], v[5]), Act<A>::pack(v[6], v[7]));
-  *reinterpret_cast<uint4*>(base + 2 * off_b) =
-      make_uint4(Act<A>::pack(v[8], v[9]), Act<A>::pack(v[10], v[11]), Act<A>::pack(v[12], v[13]), Act<A>::pack(v[14], v[15]));
+template <typename A, int STYLE>
+__device__ __forceinline__ Pairs unpack_pairs_of(const Raw& r) {
+  Pairs v;
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (STYLE == MFR_ROTARY_HALF) {
+      v.a[j] = Act<A>::unpack(w[j]);
+      v.b[j] = Act<A>::unpack(w[j + 4]);
+    } else {
+      const float2 p = Act<A>::unpack(w[2 * j]), q = Act<A>::unpack(w[2 * j + 1]);
+      v.a[j] = make_float2(p.x, q.x);
+      v.b[j] = make_float2(p.y, q.y);
+    }
+  }
+  return v;
 }
 
-// A kind's weight at a lane's elements (ones without a weight).
-template <typename A>
-__device__ __forceinline__ void load_weight(const void* w, const LaneMap& m, bool on, float v[16]) {
+template <typename A, int STYLE>
+__device__ __forceinline__ void store_pairs(uint8_t* p, const LaneMap& m, const Pairs& v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (STYLE == MFR_ROTARY_HALF) {
+      w[j] = Act<A>::pack(v.a[j].x, v.a[j].y);
+      w[j + 4] = Act<A>::pack(v.b[j].x, v.b[j].y);
+    } else {
+      w[2 * j] = Act<A>::pack(v.a[j].x, v.b[j].x);
+      w[2 * j + 1] = Act<A>::pack(v.a[j].y, v.b[j].y);
+    }
+  }
+  *reinterpret_cast<uint4*>(p + 2 * m.off_a) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(p + 2 * m.off_b) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// A kind's weight (ones without one) as each lane's pairs, in shared memory: [4][lanes of a head] vectors of (a, b)
+// pairs, read without bank conflicts.  Threads first .. first + D / 16 - 1 of the CTA fill it.
+using WeightTable = float4[4][MFR_MAX_HEAD_DIM / 16];
+template <typename A, int STYLE>
+__device__ __forceinline__ void fill_weight(const mfr_head_norm_args& a, const void* w, int first, WeightTable& table) {
+  const int lane = static_cast<int>(threadIdx.x) - first;
+  if (lane < 0 || lane >= a.D / 16) return;
+  Pairs v;
   if (w != nullptr) {
-    load16<A>(static_cast<const uint8_t*>(w), m.off_a, m.off_b, on, v);
+    v = unpack_pairs_of<A, STYLE>(load_raw(static_cast<const uint8_t*>(w), lane_map(lane, a.rot, STYLE), true));
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 1.0f;
+    for (int j = 0; j < 4; ++j) v.a[j] = v.b[j] = make_float2(1.0f, 1.0f);
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) table[j][lane] = make_float4(v.a[j].x, v.a[j].y, v.b[j].x, v.b[j].y);
 }
 
-// Turns a lane's pairs by +angle (sign 1) or back (sign -1).
-template <int STYLE>
-__device__ __forceinline__ void turn_pairs(float v[16], const float cs[8], const float sn[8], float sign) {
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+
+// Turns a lane's pairs by the angle, or back.
+template <bool BACK>
+__device__ __forceinline__ void turn_pairs(Pairs& v, const float2 (&cs)[4], const float2 (&sn)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& x = STYLE == MFR_ROTARY_HALF ? v[i] : v[2 * i];
-    float& y = STYLE == MFR_ROTARY_HALF ? v[i + 8] : v[2 * i + 1];
-    const float s = sign * sn[i];
-    const float u = x * cs[i] - y * s;
-    y = y * cs[i] + x * s;
-    x = u;
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = v.a[j], b = v.b[j];
+    v.a[j] = __ffma2_rn(b, BACK ? sn[j] : neg2(sn[j]), __fmul2_rn(a, cs[j]));
+    v.b[j] = __ffma2_rn(a, BACK ? neg2(sn[j]) : sn[j], __fmul2_rn(b, cs[j]));
   }
 }
 
@@ -144,146 +201,209 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ uint8_t* head_row(const mfr_heads& h, int64_t t, int head) {
-  return static_cast<uint8_t*>(h.data) + 2 * (t * h.token_stride + head * h.head_stride);
-}
+// 1 / sqrt(sum / D + eps): the norm's statistic in FP32, within 2 ulp of the root.
+__device__ __forceinline__ float rstd_of(float sum, float inv_d, float eps) { return rsqrtf(__fmaf_rn(sum, inv_d, eps)); }
 
+constexpr int kUnroll = 2;  // heads of a group in flight
+
+// Rounds [r0, r1) of one kind of one token: each group's head of the round.
 template <typename A, int G, int STYLE>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_kernel(const __grid_constant__ HeadParams p) {
+__device__ __forceinline__ void norm_heads(const HeadParams& p, const mfr_heads& in, const mfr_heads& out, const WeightTable& weight, int heads,
+                                           int64_t t, bool read, bool zero, const LaneMap& m, int lane, int sub, int r0, int r1,
+                                           const float2 (&cs)[4], const float2 (&sn)[4]) {
+  if (r0 >= r1) return;
   const mfr_head_norm_args& a = p.a;
-  const int lane = threadIdx.x & 31, group = lane / G, groups = 32 / G;
-  const bool on = lane % G < a.D / 16;
-  const LaneMap m = lane_map(lane % G, a.rot, STYLE);
-  const int heads = a.q_heads + a.k_heads;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5);
-  const int64_t first = warp * p.per_warp;
-  const int64_t end = first + p.per_warp < p.items ? first + p.per_warp : p.items;
-  pdl_launch_dependents();
-  pdl_wait();
-  int64_t t_now = -1, pos = -1;
-  int kind_now = -1;
-  float cs[8], sn[8], w[16];
-  int64_t t = first / heads;
-  int h = static_cast<int>(first % heads) + group;
-  for (int64_t i = first; i < end; i += groups, h += groups) {  // the same trip count for all lanes
-    while (h >= heads) {
-      h -= heads;
-      ++t;
-    }
-    const bool live = on && i + group < end;
-    float x[16];
-    const int kind = h < a.q_heads ? 0 : 1;
-    const mfr_heads& in = kind == 0 ? a.q : a.k;
-    const mfr_heads& out = kind == 0 ? a.q_out : a.k_out;
-    const int hh = kind == 0 ? h : h - a.q_heads;
-    if (live && t != t_now) {
-      t_now = t;
-      pos = position_of(a, t);
-      if (pos >= 0) turns(a, m, pos, cs, sn);
-    }
-    if (live && kind != kind_now) {
-      kind_now = kind;
-      load_weight<A>(kind == 0 ? a.q_weight : a.k_weight, m, true, w);
-    }
-    const bool work = live && pos >= 0;
-    load16<A>(work ? head_row(in, t, hh) : nullptr, m.off_a, m.off_b, work, x);
-    float sq = 0.0f;
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  int h = (r0 << p.cut.gpt_log2) + sub;
+  const int gpt = 1 << p.cut.gpt_log2;
+  const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * (t * in.token_stride + h * in.head_stride);
+  uint8_t* dst = static_cast<uint8_t*>(out.data) + 2 * (t * out.token_stride + h * out.head_stride);
+  const int64_t src_step = 2 * in.head_stride << p.cut.gpt_log2, dst_step = 2 * out.head_stride << p.cut.gpt_log2;
+  for (int r = r0; r < r1; r += kUnroll) {
+    Raw raw[kUnroll];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) sq = __fmaf_rn(x[j], x[j], sq);
-    sq = group_sum<G>(sq);
-    if (work) {
-      const float r = rms_rstd(sq, a.D, a.eps);
+    for (int i = 0; i < kUnroll; ++i) raw[i] = load_raw(src + i * src_step, m, read && r + i < r1 && h + i * gpt < heads);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
-      turn_pairs<STYLE>(x, cs, sn, 1.0f);
-      store16<A>(head_row(out, t, hh), m.off_a, m.off_b, x);
-    } else if (live && (a.flags & MFR_FLAG_ZERO_PADDING)) {
-      store16<A>(head_row(out, t, hh), m.off_a, m.off_b, x);  // zeros
+    for (int i = 0; i < kUnroll; ++i) {
+      Pairs v = unpack_pairs_of<A, STYLE>(raw[i]);
+      float2 sq = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sq = __ffma2_rn(v.a[j], v.a[j], sq);
+        sq = __ffma2_rn(v.b[j], v.b[j], sq);
+      }
+      const float rs = rstd_of(group_sum<G>(sq.x + sq.y), inv_d, a.eps);
+      const float2 rr = make_float2(rs, rs);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = weight[j][lane];
+        v.a[j] = __fmul2_rn(__fmul2_rn(v.a[j], rr), make_float2(w.x, w.y));
+        v.b[j] = __fmul2_rn(__fmul2_rn(v.b[j], rr), make_float2(w.z, w.w));
+      }
+      turn_pairs<false>(v, cs, sn);
+      const bool live = r + i < r1 && h + i * gpt < heads;
+      if (read && live) store_pairs<A, STYLE>(dst + i * dst_step, m, v);
+      if (zero && live) {
+        *reinterpret_cast<uint4*>(dst + i * dst_step + 2 * m.off_a) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + i * dst_step + 2 * m.off_b) = make_uint4(0, 0, 0, 0);
+      }
     }
+    src += kUnroll * src_step;
+    dst += kUnroll * dst_step;
+    h += kUnroll * gpt;
   }
 }
 
-// Gradient.  CTAs [0, q_blocks) walk the queries, the rest the keys; each keeps its lanes' share of the
-// weight gradient in registers and leaves one row of partial sums in the workspace.
 template <typename A, int G, int STYLE>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
-  extern __shared__ float part[];  // [kHeadWarps][D]
+__global__ void __launch_bounds__(kHeadThreads, 3) head_norm_kernel(const __grid_constant__ HeadParams p) {
+  __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
+  __shared__ WeightTable weights[2];
   const mfr_head_norm_args& a = p.a;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G, groups = 32 / G;
+  const int lane = threadIdx.x & 31, group = lane / G;
+  const bool on = lane % G < a.D / 16;
+  const LaneMap m = lane_map(lane % G, a.rot, STYLE);
+  pdl_launch_dependents();
+  pdl_wait();
+  fill_weight<A, STYLE>(a, a.q_weight, 0, weights[0]);
+  fill_weight<A, STYLE>(a, a.k_weight, 32, weights[1]);
+  fill_turns(a, table);
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5);
+  if (task >= p.cut.tasks) return;
+  const int split = static_cast<int>(task % p.cut.splits);
+  const int64_t t = (task / p.cut.splits) * ((32 / G) >> p.cut.gpt_log2) + (group >> p.cut.gpt_log2);
+  const int sub = group & ((1 << p.cut.gpt_log2) - 1);
+  const int64_t pos = t < a.T ? position_of(a, t) : -1;
+  const bool read = on && pos >= 0;
+  const bool zero = on && t < a.T && pos < 0 && (a.flags & MFR_FLAG_ZERO_PADDING);
+  float2 cs[4], sn[4];
+  turns(a, table, m, read ? pos : 0, cs, sn);
+  const int gpt = 1 << p.cut.gpt_log2;
+  const int q_rounds = (a.q_heads + gpt - 1) >> p.cut.gpt_log2, rounds = q_rounds + ((a.k_heads + gpt - 1) >> p.cut.gpt_log2);
+  const int r0 = static_cast<int>(static_cast<int64_t>(rounds) * split / p.cut.splits);
+  const int r1 = static_cast<int>(static_cast<int64_t>(rounds) * (split + 1) / p.cut.splits);
+  norm_heads<A, G, STYLE>(p, a.q, a.q_out, weights[0], a.q_heads, t, read, zero, m, lane % G, sub, r0, min(r1, q_rounds), cs, sn);
+  norm_heads<A, G, STYLE>(p, a.k, a.k_out, weights[1], a.k_heads, t, read, zero, m, lane % G, sub, max(r0, q_rounds) - q_rounds, r1 - q_rounds, cs, sn);
+}
+
+// Gradient.  CTAs [0, q_blocks) take the queries, the rest the keys; a warp walks its tasks with its lanes' share
+// of the weight gradient in registers, the next round's vectors in flight, and the CTA leaves one row of partial
+// sums in the workspace.
+template <typename A, int G, int STYLE>
+__global__ void __launch_bounds__(kHeadThreads, 2) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
+  extern __shared__ float part[];  // [kHeadWarps][D]
+  __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
+  __shared__ WeightTable weights;
+  const mfr_head_norm_args& a = p.a;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
   const bool on = lane % G < a.D / 16;
   const LaneMap m = lane_map(lane % G, a.rot, STYLE);
   const bool keys = static_cast<int>(blockIdx.x) >= p.q_blocks;
   const int block = keys ? blockIdx.x - p.q_blocks : blockIdx.x;
   const int blocks = keys ? gridDim.x - p.q_blocks : p.q_blocks;
+  const HeadCut& cut = keys ? p.key_cut : p.cut;
   const int heads = keys ? a.k_heads : a.q_heads;
   const mfr_heads& in = keys ? a.k : a.q;
   const mfr_heads& out = keys ? a.k_out : a.q_out;
   const mfr_heads& dout = keys ? a.d_k_out : a.d_q_out;
   const bool want = (keys ? a.d_k_weight : a.d_q_weight) != nullptr;
-  // contiguous items a warp, in whole rounds of its groups
-  const int64_t items = static_cast<int64_t>(a.T) * heads;
-  const int64_t rounds = (items + groups - 1) / groups;
-  const int64_t warps = static_cast<int64_t>(blocks) * kHeadWarps, me = static_cast<int64_t>(block) * kHeadWarps + wid;
-  const int64_t first = rounds * me / warps * groups;
-  int64_t end = rounds * (me + 1) / warps * groups;
-  end = end < items ? end : items;
+  const int gpt = 1 << cut.gpt_log2, sub = group & (gpt - 1);
+  const int rounds = (heads + gpt - 1) >> cut.gpt_log2;
+  const float inv_d = 1.0f / static_cast<float>(a.D);
   pdl_launch_dependents();
   pdl_wait();
-  float w[16], dw[16];
+  fill_weight<A, STYLE>(a, keys ? a.k_weight : a.q_weight, 0, weights);
+  fill_turns(a, table);
+  Pairs dw;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) dw[j] = 0.0f;
-  load_weight<A>(keys ? a.k_weight : a.q_weight, m, on, w);
-  int64_t t_now = -1, pos = -1;
-  float cs[8], sn[8];
-  int64_t t = first / heads;
-  int h = static_cast<int>(first % heads) + group;
-  for (int64_t i = first; i < end; i += groups, h += groups) {
-    while (h >= heads) {
-      h -= heads;
-      ++t;
-    }
-    const bool live = on && i + group < end;
-    if (live && t != t_now) {
-      t_now = t;
-      pos = position_of(a, t);
-      if (pos >= 0) turns(a, m, pos, cs, sn);
-    }
-    const bool work = live && pos >= 0;
-    float x[16], g[16];
-    load16<A>(work ? head_row(in, t, h) : nullptr, m.off_a, m.off_b, work, x);
-    load16<A>(work ? head_row(dout, t, h) : nullptr, m.off_a, m.off_b, work, g);
-    if (work) turn_pairs<STYLE>(g, cs, sn, -1.0f);
-    float sq = 0.0f, dot = 0.0f;
+  for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = make_float2(0.0f, 0.0f);
+  const int64_t x_step = 2 * in.head_stride << cut.gpt_log2, g_step = 2 * dout.head_stride << cut.gpt_log2;
+  const int64_t o_step = 2 * out.head_stride << cut.gpt_log2;
+  for (int64_t task = static_cast<int64_t>(block) * kHeadWarps + wid; task < cut.tasks; task += static_cast<int64_t>(blocks) * kHeadWarps) {
+    const int split = static_cast<int>(task % cut.splits);
+    const int64_t t = (task / cut.splits) * ((32 / G) >> cut.gpt_log2) + (group >> cut.gpt_log2);
+    const int64_t pos = t < a.T ? position_of(a, t) : -1;
+    const bool write = on && t < a.T, read = on && pos >= 0;
+    const int r0 = static_cast<int>(static_cast<int64_t>(rounds) * split / cut.splits);
+    const int r1 = static_cast<int>(static_cast<int64_t>(rounds) * (split + 1) / cut.splits);
+    int h = (r0 << cut.gpt_log2) + sub;
+    const uint8_t* xp = static_cast<const uint8_t*>(in.data) + 2 * (t * in.token_stride + h * in.head_stride);
+    const uint8_t* gp = static_cast<const uint8_t*>(dout.data) + 2 * (t * dout.token_stride + h * dout.head_stride);
+    uint8_t* op = static_cast<uint8_t*>(out.data) + 2 * (t * out.token_stride + h * out.head_stride);
+    Raw xr = load_raw(xp, m, read && h < heads), gr = load_raw(gp, m, read && h < heads);
+    float2 cs[4], sn[4];
+    turns(a, table, m, read ? pos : 0, cs, sn);
+    for (int r = r0; r < r1; ++r) {
+      const Pairs x = unpack_pairs_of<A, STYLE>(xr);
+      Pairs g = unpack_pairs_of<A, STYLE>(gr);
+      xp += x_step;
+      gp += g_step;
+      const bool next = read && r + 1 < r1 && h + gpt < heads;
+      xr = load_raw(xp, m, next);
+      gr = load_raw(gp, m, next);
+      turn_pairs<true>(g, cs, sn);
+      // sums of x^2 and of (g w) x
+      float2 sq = make_float2(0.0f, 0.0f), dot = make_float2(0.0f, 0.0f);
+      Pairs gw;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      sq = __fmaf_rn(x[j], x[j], sq);
-      dot = __fmaf_rn(g[j] * w[j], x[j], dot);
-    }
-    sq = group_sum<G>(sq);
-    dot = group_sum<G>(dot);
-    if (work) {
-      const float r = rms_rstd(sq, a.D, a.eps);
-      const float c = __fdiv_rn(dot, static_cast<float>(a.D)) * r * r;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        dw[j] = __fmaf_rn(g[j] * r, x[j], dw[j]);
-        x[j] = r * (g[j] * w[j] - x[j] * c);
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = weights[j][lane % G];
+        gw.a[j] = __fmul2_rn(g.a[j], make_float2(w.x, w.y));
+        gw.b[j] = __fmul2_rn(g.b[j], make_float2(w.z, w.w));
+        sq = __ffma2_rn(x.a[j], x.a[j], sq);
+        sq = __ffma2_rn(x.b[j], x.b[j], sq);
+        dot = __ffma2_rn(gw.a[j], x.a[j], dot);
+        dot = __ffma2_rn(gw.b[j], x.b[j], dot);
       }
+      const float rs = rstd_of(group_sum<G>(sq.x + sq.y), inv_d, a.eps);
+      const float c = group_sum<G>(dot.x + dot.y) * inv_d * rs * rs * rs;
+      const float2 rr = make_float2(rs, rs), cc = make_float2(-c, -c);
+      Pairs d;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // (a padding token's x and g are zeros)
+        dw.a[j] = __ffma2_rn(g.a[j], __fmul2_rn(x.a[j], rr), dw.a[j]);
+        dw.b[j] = __ffma2_rn(g.b[j], __fmul2_rn(x.b[j], rr), dw.b[j]);
+        d.a[j] = __ffma2_rn(x.a[j], cc, __fmul2_rn(gw.a[j], rr));
+        d.b[j] = __ffma2_rn(x.b[j], cc, __fmul2_rn(gw.b[j], rr));
+      }
+      if (write && h < heads) {
+        if (!read) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d.a[j] = d.b[j] = make_float2(0.0f, 0.0f);
+        }
+        store_pairs<A, STYLE>(op, m, d);
+      }
+      op += o_step;
+      h += gpt;
     }
-    if (live) store16<A>(head_row(out, t, h), m.off_a, m.off_b, x);  // zeros for a padding token
   }
   if (!want) return;
   // over the warp's groups (lanes G apart), then over the CTA's warps in order
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
-    for (int o = 16; o >= G; o >>= 1) dw[j] += __shfl_xor_sync(kAll, dw[j], o);
+    for (int o = 16; o >= G; o >>= 1) {
+      dw.a[j].x += __shfl_xor_sync(kAll, dw.a[j].x, o);
+      dw.a[j].y += __shfl_xor_sync(kAll, dw.a[j].y, o);
+      dw.b[j].x += __shfl_xor_sync(kAll, dw.b[j].x, o);
+      dw.b[j].y += __shfl_xor_sync(kAll, dw.b[j].y, o);
+    }
   }
   if (group == 0 && on) {
+    float* row = part + wid * a.D;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      part[wid * a.D + m.off_a + j] = dw[j];
-      part[wid * a.D + m.off_b + j] = dw[j + 8];
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (STYLE == MFR_ROTARY_HALF) {
+        row[m.off_a + 2 * j] = dw.a[j].x;
+        row[m.off_a + 2 * j + 1] = dw.a[j].y;
+        row[m.off_b + 2 * j] = dw.b[j].x;
+        row[m.off_b + 2 * j + 1] = dw.b[j].y;
+      } else {
+        row[m.off_a + 4 * j] = dw.a[j].x;
+        row[m.off_a + 4 * j + 1] = dw.b[j].x;
+        row[m.off_a + 4 * j + 2] = dw.a[j].y;
+        row[m.off_a + 4 * j + 3] = dw.b[j].y;
+      }
     }
   }
   __syncthreads();
@@ -309,7 +429,7 @@ __global__ void __launch_bounds__(kSumThreads) head_weight_grad_kernel(const __g
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int d = (blockIdx.x % parts) * 32 + lane;
-  const int64_t b0 = keys ? p.q_blocks : 0, b1 = keys ? p.items : p.q_blocks;  // items: the gradient kernel's CTAs
+  const int64_t b0 = keys ? p.q_blocks : 0, b1 = keys ? p.blocks : p.q_blocks;
   float s = 0.0f;
   if (d < a.D) {
 #pragma unroll 4
@@ -358,46 +478,60 @@ int groups_of(int D) {
   return 32 / g;
 }
 
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Cuts `heads` heads (of one kind, or the larger of two) of T tokens for `warps` warps: as many groups on a token
+// as it has heads for, and a token's rounds in more ranges when the tokens alone leave warps idle.
+HeadCut cut_heads(int T, int q_heads, int k_heads, int groups, int64_t warps) {
+  HeadCut c{0, 1, 0};
+  const int most = q_heads > k_heads ? q_heads : k_heads;
+  while ((2 << c.gpt_log2) <= groups && (2 << c.gpt_log2) <= most) ++c.gpt_log2;
+  const int64_t rounds = ceil_div64(q_heads, 1 << c.gpt_log2) + ceil_div64(k_heads, 1 << c.gpt_log2);
+  const int64_t blocks = ceil_div64(T, groups >> c.gpt_log2);
+  int64_t splits = blocks > 0 ? warps / blocks : 1;
+  if (splits > rounds) splits = rounds;
+  if (splits < 1) splits = 1;
+  c.splits = static_cast<int>(splits);
+  c.tasks = blocks * splits;
+  return c;
+}
+
 }  // namespace
 
 cudaError_t launch_head_norm(const mfr_head_norm_args& a, cudaStream_t stream) {
-  HeadParams p{a, 0, 0, 0};
-  const int groups = groups_of(a.D), heads = a.q_heads + a.k_heads;
-  p.items = static_cast<int64_t>(a.T) * heads;
-  // A token's heads a warp when that gives every SM its warps, else fewer, down to one round of the groups.
-  const int64_t rounds = (p.items + groups - 1) / groups;
-  int64_t per = (heads + groups - 1) / groups;
-  const int64_t fill = (rounds + 152 * 24 - 1) / (152 * 24);  // rounds a warp at 24 warps an SM
-  if (per > fill) per = fill;
-  p.per_warp = per * groups;
-  const int64_t warps = (rounds + per - 1) / per;
-  const int64_t blocks = (warps + kHeadWarps - 1) / kHeadWarps;
+  HeadParams p{a, {}, {}, 0, 0};
+  p.cut = cut_heads(a.T, a.q_heads, a.k_heads, groups_of(a.D), 152 * 3 * kHeadWarps);
+  const int64_t blocks = ceil_div64(p.cut.tasks, kHeadWarps);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   return a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, static_cast<int>(blocks), false, stream)
                                  : launch_s<__half>(p, static_cast<int>(blocks), false, stream);
 }
 
 cudaError_t launch_head_norm_backward(const mfr_head_norm_args& a, cudaStream_t stream) {
-  HeadParams p{a, 0, 0, 0};
-  const int groups = groups_of(a.D);
-  // CTAs in proportion to the heads of each kind, at least one where there are any
-  const int64_t warps = (static_cast<int64_t>(a.T) * (a.q_heads + a.k_heads) + groups - 1) / groups;
-  int64_t blocks = (warps + kHeadWarps - 1) / kHeadWarps;
-  if (blocks > kHeadGradBlocks) blocks = kHeadGradBlocks;
-  if (blocks < 2) blocks = 2;
-  int q = static_cast<int>(blocks * a.q_heads / (a.q_heads + a.k_heads));
-  if (a.q_heads > 0 && q == 0) q = 1;
-  if (a.k_heads > 0 && q == blocks) q = static_cast<int>(blocks) - 1;
-  p.q_blocks = q;
-  p.items = blocks;
+  HeadParams p{a, {}, {}, 0, 0};
   cudaError_t e = cudaSuccess;
-  if (a.T == 0) {
-    p.q_blocks = 0;
-    p.items = 0;  // no partial sums: the weight gradients are zeros
-  } else {
-    e = a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, static_cast<int>(blocks), true, stream)
-                                : launch_s<__half>(p, static_cast<int>(blocks), true, stream);
+  if (a.T > 0) {
+    const int groups = groups_of(a.D);
+    // CTAs in proportion to the kinds' work: a token's rounds, and its sines and cosines (about two rounds)
+    auto weight = [&](int heads) { return heads > 0 ? ceil_div64(heads, groups) + 2 : 0; };
+    const int64_t wq = weight(a.q_heads), wk = weight(a.k_heads);
+    int q = static_cast<int>(kHeadGradBlocks * wq / (wq + wk)), k = kHeadGradBlocks - q;
+    if (a.q_heads > 0 && q == 0) q = 1;
+    if (a.k_heads > 0 && k == 0) k = 1;
+    if (q + k > kHeadGradBlocks) (q > k ? q : k) -= 1;
+    auto plan = [&](int heads, int most, HeadCut* cut) {
+      if (heads == 0) return 0;
+      *cut = cut_heads(a.T, heads, 0, groups, static_cast<int64_t>(most) * kHeadWarps);
+      const int64_t want = ceil_div64(cut->tasks, kHeadWarps);
+      return static_cast<int>(want < most ? want : most);
+    };
+    q = plan(a.q_heads, q, &p.cut);
+    k = plan(a.k_heads, k, &p.key_cut);
+    p.q_blocks = q;
+    p.blocks = q + k;
+    e = a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, p.blocks, true, stream) : launch_s<__half>(p, p.blocks, true, stream);
   }
+  // (no tokens: no partial sums, and the weight gradients are zeros)
   if (e != cudaSuccess || (a.d_q_weight == nullptr && a.d_k_weight == nullptr)) return e;
   return launch_pdl<HeadParams>(head_weight_grad_kernel, dim3(2 * ((a.D + 31) / 32)), kSumThreads, 0, a.flags & MFR_FLAG_PDL, stream, p);
 }
