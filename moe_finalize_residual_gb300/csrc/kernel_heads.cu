@@ -7,8 +7,8 @@
 //   interleaved style  vectors 2p and 2p + 1 (neighbouring elements)
 // so the rotation needs no exchange, and a head's sum of squares takes log2(G) shuffles.  The elements are
 // kept as the pairs' first and second elements (`a` and `b`), two to a packed FP32 register pair, so that all
-// the arithmetic runs on packed operations.  A lane turns the same 8 pairs of every head of a token: their
-// sines and cosines are computed once a token and kept in registers.
+// the arithmetic runs on packed operations.  A warp computes the sines and cosines of its token's pairs once, in
+// shared memory, and turns every head of the token by them.
 //
 // The angle position * inv_freq is reduced without error: inv_freq / (2 pi) is held as a 64-bit fraction of
 // a turn (24-bit significand times 1 / (2 pi) to 64 bits), so the product with the position, modulo 2^64, is
@@ -24,21 +24,21 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kHeadThreads = 256;
 constexpr int kHeadWarps = kHeadThreads / 32;
 
-// How a launch cuts its work.  A warp's groups take `1 << gpt_log2` heads of a token at a time (a round) and
-// the warp as many tokens as that leaves groups for; a token's rounds are cut into `splits` ranges.  A task is a
-// block of tokens and a range.
+// How a launch cuts one kind's work (queries or keys).  A warp's groups take `1 << gpt_log2` heads of a token at a
+// time (a round) and the warp as many tokens as that leaves groups for; a token's rounds are cut into `splits`
+// ranges.  A task is a block of tokens and a range; the kind's warps walk the tasks.
 struct HeadCut {
   int gpt_log2;
+  int rounds;
   int splits;
+  int blocks;     // CTAs of the kind
   int64_t tasks;
 };
 
+// CTAs [0, q.blocks) take the queries, the rest the keys.
 struct HeadParams {
   mfr_head_norm_args a;
-  HeadCut cut;       // forward: over the heads of both kinds; backward: the queries'
-  HeadCut key_cut;   // backward: the keys'
-  int q_blocks;      // backward: CTAs [0, q_blocks) take the queries, the rest the keys
-  int blocks;        // backward: CTAs, each leaving a row of partial weight gradients
+  HeadCut q, k;
 };
 
 // inv_freq / (2 pi) as a fraction of a turn times 2^64, modulo 2^64.
@@ -89,28 +89,45 @@ __device__ __forceinline__ void fill_turns(const mfr_head_norm_args& a, uint64_t
   __syncthreads();
 }
 
-// Sines and cosines of a lane's pairs at a position, times rotary_scale; (0, 1) for unrotated pairs.
-__device__ __forceinline__ void turns(const mfr_head_norm_args& a, const uint64_t* table, const LaneMap& m, int64_t pos,
-                                      float2 (&cs)[4], float2 (&sn)[4]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float c = 1.0f, s = 0.0f;
-    if (i < m.pairs) {
-      const uint64_t u = table[m.pair0 + i] * static_cast<uint64_t>(pos);
-      // the nearest 2^-32 turn, as a half turn in [-1, 1)
-      const float h = static_cast<float>(static_cast<int32_t>((u + 0x80000000ULL) >> 32)) * 4.656612873077393e-10f;
-      sincospif(h, &s, &c);
-      c *= a.rotary_scale;
-      s *= a.rotary_scale;
-    }
-    (i % 2 ? cs[i / 2].y : cs[i / 2].x) = c;
-    (i % 2 ? sn[i / 2].y : sn[i / 2].x) = s;
-  }
-}
-
 __device__ __forceinline__ int64_t position_of(const mfr_head_norm_args& a, int64_t t) {
   return (a.flags & MFR_FLAG_POSITIONS_64) ? static_cast<const int64_t*>(a.positions)[t]
                                            : static_cast<const int32_t*>(a.positions)[t];
+}
+
+// The cosines and sines of a warp's tokens: entry [(token, j, p)] holds pairs 8p + 2j and 8p + 2j + 1 of the token.
+template <int G>
+using TurnCache = float4[32 / G][4][G];
+
+// Fills a warp's cache: 1 and 0 for unrotated pairs, times rotary_scale else.  `pos`: the position of the lane's
+// group's token (gpt groups a token).
+template <int G>
+__device__ __forceinline__ void fill_cache(const mfr_head_norm_args& a, const uint64_t* table, int64_t pos, int gpt_log2, int lane,
+                                           TurnCache<G>& cache) {
+  const int entries = ((32 / G) >> gpt_log2) * 4 * G;
+  __syncwarp();  // the last task's turns are done with
+#pragma unroll 1
+  for (int first = 0; first < entries; first += 32) {
+    const int i = first + lane, token = i / (4 * G), j = i / G % 4, p = i % G;
+    const int64_t at = __shfl_sync(kAll, pos, ((token << gpt_log2) * G) & 31);
+    if (i >= entries) break;  // (the last iteration)
+    float c[2], s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      c[k] = 1.0f;
+      s[k] = 0.0f;
+      const int pair = 8 * p + 2 * j + k;
+      if (pair < a.rot / 2) {
+        const uint64_t u = table[pair] * static_cast<uint64_t>(at);
+        // the nearest 2^-32 turn, as a half turn in [-1, 1)
+        const float h = static_cast<float>(static_cast<int32_t>((u + 0x80000000ULL) >> 32)) * 4.656612873077393e-10f;
+        sincospif(h, &s[k], &c[k]);
+        c[k] *= a.rotary_scale;
+        s[k] *= a.rotary_scale;
+      }
+    }
+    cache[token][j][p] = make_float4(c[0], c[1], s[0], s[1]);
+  }
+  __syncwarp();
 }
 
 // A lane's 16 elements of a head as they lie in memory, and as its pairs' first and second elements.
@@ -181,16 +198,21 @@ __device__ __forceinline__ void fill_weight(const mfr_head_norm_args& a, const v
   for (int j = 0; j < 4; ++j) table[j][lane] = make_float4(v.a[j].x, v.a[j].y, v.b[j].x, v.b[j].y);
 }
 
-__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
-
-// Turns a lane's pairs by the angle, or back.
-template <bool BACK>
-__device__ __forceinline__ void turn_pairs(Pairs& v, const float2 (&cs)[4], const float2 (&sn)[4]) {
+// Turns a lane's pairs by the angle, or back; `turn`: the token's cache at the lane, G entries apart.
+template <bool BACK, int G>
+__device__ __forceinline__ void turn_pairs(Pairs& v, const float4* turn) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 a = v.a[j], b = v.b[j];
-    v.a[j] = __ffma2_rn(b, BACK ? sn[j] : neg2(sn[j]), __fmul2_rn(a, cs[j]));
-    v.b[j] = __ffma2_rn(a, BACK ? neg2(sn[j]) : sn[j], __fmul2_rn(b, cs[j]));
+    const float4 t = turn[j * G];
+    const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = v.a[j], b = v.b[j];
+    const float2 ac = __fmul2_rn(a, c), bc = __fmul2_rn(b, c);
+    if constexpr (BACK) {
+      v.a[j] = __ffma2_rn(b, s, ac);
+      v.b[j] = make_float2(__fmaf_rn(-a.x, s.x, bc.x), __fmaf_rn(-a.y, s.y, bc.y));
+    } else {
+      v.a[j] = make_float2(__fmaf_rn(-b.x, s.x, ac.x), __fmaf_rn(-b.y, s.y, ac.y));
+      v.b[j] = __ffma2_rn(a, s, bc);
+    }
   }
 }
 
@@ -204,28 +226,81 @@ __device__ __forceinline__ float group_sum(float v) {
 // 1 / sqrt(sum / D + eps): the norm's statistic in FP32, within 2 ulp of the root.
 __device__ __forceinline__ float rstd_of(float sum, float inv_d, float eps) { return rsqrtf(__fmaf_rn(sum, inv_d, eps)); }
 
-constexpr int kUnroll = 2;  // heads of a group in flight
+#ifndef HEADS_KB
+#define HEADS_KB 4
+#endif
 
-// Rounds [r0, r1) of one kind of one token: each group's head of the round.
+// A warp's place in its kind's tasks: the token and the rounds of the current one.
+struct Place {
+  int64_t t;
+  int64_t pos;  // -1 behind the last token
+  int r0, r1;
+};
+template <int G>
+__device__ __forceinline__ Place place_of(const mfr_head_norm_args& a, const HeadCut& cut, int64_t task, int group) {
+  Place q;
+  int split = 0;
+  int64_t block = task;
+  if (cut.splits > 1) {
+    block = task / cut.splits;
+    split = static_cast<int>(task - block * cut.splits);
+  }
+  q.t = block * ((32 / G) >> cut.gpt_log2) + (group >> cut.gpt_log2);
+  q.r0 = cut.splits > 1 ? static_cast<int>(static_cast<int64_t>(cut.rounds) * split / cut.splits) : 0;
+  q.r1 = cut.splits > 1 ? static_cast<int>(static_cast<int64_t>(cut.rounds) * (split + 1) / cut.splits) : cut.rounds;
+  q.pos = task < cut.tasks && q.t < a.T ? position_of(a, q.t) : -1;
+  return q;
+}
+
+// The lane's vectors of its group's head in round r of a place.
+__device__ __forceinline__ int64_t head_at(const mfr_heads& h, const Place& q, int r, int gpt_log2, int sub) {
+  return 2 * (q.t * h.token_stride + ((static_cast<int64_t>(r) << gpt_log2) + sub) * h.head_stride);
+}
+
+// Forward.  The next round's vectors (of the next task after a task's last round) are in flight while one is worked on.
 template <typename A, int G, int STYLE>
-__device__ __forceinline__ void norm_heads(const HeadParams& p, const mfr_heads& in, const mfr_heads& out, const WeightTable& weight, int heads,
-                                           int64_t t, bool read, bool zero, const LaneMap& m, int lane, int sub, int r0, int r1,
-                                           const float2 (&cs)[4], const float2 (&sn)[4]) {
-  if (r0 >= r1) return;
+__global__ void __launch_bounds__(kHeadThreads, HEADS_KB) head_norm_kernel(const __grid_constant__ HeadParams p) {
+  __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
+  __shared__ WeightTable weight;
+  __shared__ TurnCache<G> caches[kHeadWarps];
   const mfr_head_norm_args& a = p.a;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
+  const bool on = lane % G < a.D / 16;
+  const LaneMap m = lane_map(lane % G, a.rot, STYLE);
+  const bool keys = static_cast<int>(blockIdx.x) >= p.q.blocks;
+  const HeadCut& cut = keys ? p.k : p.q;
+  const int heads = keys ? a.k_heads : a.q_heads;
+  const mfr_heads& in = keys ? a.k : a.q;
+  const mfr_heads& out = keys ? a.k_out : a.q_out;
+  const int gl = cut.gpt_log2, sub = group & ((1 << gl) - 1);
+  const float4* turn = &caches[wid][group >> gl][0][lane % G];
   const float inv_d = 1.0f / static_cast<float>(a.D);
-  int h = (r0 << p.cut.gpt_log2) + sub;
-  const int gpt = 1 << p.cut.gpt_log2;
-  const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * (t * in.token_stride + h * in.head_stride);
-  uint8_t* dst = static_cast<uint8_t*>(out.data) + 2 * (t * out.token_stride + h * out.head_stride);
-  const int64_t src_step = 2 * in.head_stride << p.cut.gpt_log2, dst_step = 2 * out.head_stride << p.cut.gpt_log2;
-  for (int r = r0; r < r1; r += kUnroll) {
-    Raw raw[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) raw[i] = load_raw(src + i * src_step, m, read && r + i < r1 && h + i * gpt < heads);
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      Pairs v = unpack_pairs_of<A, STYLE>(raw[i]);
+  const int64_t step = static_cast<int64_t>(cut.blocks) * kHeadWarps;
+  int64_t task = static_cast<int64_t>(blockIdx.x - (keys ? p.q.blocks : 0)) * kHeadWarps + wid;
+  pdl_launch_dependents();
+  pdl_wait();
+  Place q = place_of<G>(a, cut, task, group);
+  const uint8_t* src = static_cast<const uint8_t*>(in.data);
+  uint8_t* dst = static_cast<uint8_t*>(out.data);
+  auto live = [&](const Place& z, int r) { return on && z.pos >= 0 && (r << gl) + sub < heads; };
+  Raw raw = load_raw(src + head_at(in, q, q.r0, gl, sub), m, live(q, q.r0));
+  fill_weight<A, STYLE>(a, keys ? a.k_weight : a.q_weight, 0, weight);
+  fill_turns(a, table);
+  const int64_t src_step = 2 * in.head_stride << gl, dst_step = 2 * out.head_stride << gl;
+  while (task < cut.tasks) {
+    task += step;
+    const Place next = place_of<G>(a, cut, task, group);
+    fill_cache<G>(a, table, q.pos, gl, lane, caches[wid]);
+    const uint8_t* sp = src + head_at(in, q, q.r0, gl, sub);
+    uint8_t* dp = dst + head_at(out, q, q.r0, gl, sub);
+    for (int r = q.r0; r < q.r1; ++r) {  // the same trip count for the whole warp
+      Pairs v = unpack_pairs_of<A, STYLE>(raw);
+      sp += src_step;
+      if (r + 1 == q.r1) {
+        raw = load_raw(src + head_at(in, next, next.r0, gl, sub), m, live(next, next.r0));
+      } else {
+        raw = load_raw(sp, m, live(q, r + 1));
+      }
       float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -236,117 +311,87 @@ __device__ __forceinline__ void norm_heads(const HeadParams& p, const mfr_heads&
       const float2 rr = make_float2(rs, rs);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 w = weight[j][lane];
+        const float4 w = weight[j][lane % G];
         v.a[j] = __fmul2_rn(__fmul2_rn(v.a[j], rr), make_float2(w.x, w.y));
         v.b[j] = __fmul2_rn(__fmul2_rn(v.b[j], rr), make_float2(w.z, w.w));
       }
-      turn_pairs<false>(v, cs, sn);
-      const bool live = r + i < r1 && h + i * gpt < heads;
-      if (read && live) store_pairs<A, STYLE>(dst + i * dst_step, m, v);
-      if (zero && live) {
-        *reinterpret_cast<uint4*>(dst + i * dst_step + 2 * m.off_a) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dst + i * dst_step + 2 * m.off_b) = make_uint4(0, 0, 0, 0);
+      turn_pairs<false, G>(v, turn);
+      if (live(q, r)) {
+        store_pairs<A, STYLE>(dp, m, v);
+      } else if ((a.flags & MFR_FLAG_ZERO_PADDING) && on && q.t < a.T && (r << gl) + sub < heads) {
+        *reinterpret_cast<uint4*>(dp + 2 * m.off_a) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dp + 2 * m.off_b) = make_uint4(0, 0, 0, 0);
       }
+      dp += dst_step;
     }
-    src += kUnroll * src_step;
-    dst += kUnroll * dst_step;
-    h += kUnroll * gpt;
+    q = next;
   }
 }
 
-template <typename A, int G, int STYLE>
-__global__ void __launch_bounds__(kHeadThreads, 3) head_norm_kernel(const __grid_constant__ HeadParams p) {
-  __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
-  __shared__ WeightTable weights[2];
-  const mfr_head_norm_args& a = p.a;
-  const int lane = threadIdx.x & 31, group = lane / G;
-  const bool on = lane % G < a.D / 16;
-  const LaneMap m = lane_map(lane % G, a.rot, STYLE);
-  pdl_launch_dependents();
-  pdl_wait();
-  fill_weight<A, STYLE>(a, a.q_weight, 0, weights[0]);
-  fill_weight<A, STYLE>(a, a.k_weight, 32, weights[1]);
-  fill_turns(a, table);
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5);
-  if (task >= p.cut.tasks) return;
-  const int split = static_cast<int>(task % p.cut.splits);
-  const int64_t t = (task / p.cut.splits) * ((32 / G) >> p.cut.gpt_log2) + (group >> p.cut.gpt_log2);
-  const int sub = group & ((1 << p.cut.gpt_log2) - 1);
-  const int64_t pos = t < a.T ? position_of(a, t) : -1;
-  const bool read = on && pos >= 0;
-  const bool zero = on && t < a.T && pos < 0 && (a.flags & MFR_FLAG_ZERO_PADDING);
-  float2 cs[4], sn[4];
-  turns(a, table, m, read ? pos : 0, cs, sn);
-  const int gpt = 1 << p.cut.gpt_log2;
-  const int q_rounds = (a.q_heads + gpt - 1) >> p.cut.gpt_log2, rounds = q_rounds + ((a.k_heads + gpt - 1) >> p.cut.gpt_log2);
-  const int r0 = static_cast<int>(static_cast<int64_t>(rounds) * split / p.cut.splits);
-  const int r1 = static_cast<int>(static_cast<int64_t>(rounds) * (split + 1) / p.cut.splits);
-  norm_heads<A, G, STYLE>(p, a.q, a.q_out, weights[0], a.q_heads, t, read, zero, m, lane % G, sub, r0, min(r1, q_rounds), cs, sn);
-  norm_heads<A, G, STYLE>(p, a.k, a.k_out, weights[1], a.k_heads, t, read, zero, m, lane % G, sub, max(r0, q_rounds) - q_rounds, r1 - q_rounds, cs, sn);
-}
-
-// Gradient.  CTAs [0, q_blocks) take the queries, the rest the keys; a warp walks its tasks with its lanes' share
-// of the weight gradient in registers, the next round's vectors in flight, and the CTA leaves one row of partial
+// Gradient: as forward, with the lanes' share of the weight gradient in registers; each CTA leaves one row of partial
 // sums in the workspace.
 template <typename A, int G, int STYLE>
 __global__ void __launch_bounds__(kHeadThreads, 2) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ float part[];  // [kHeadWarps][D]
   __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
-  __shared__ WeightTable weights;
+  __shared__ WeightTable weight;
+  __shared__ TurnCache<G> caches[kHeadWarps];
   const mfr_head_norm_args& a = p.a;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
   const bool on = lane % G < a.D / 16;
   const LaneMap m = lane_map(lane % G, a.rot, STYLE);
-  const bool keys = static_cast<int>(blockIdx.x) >= p.q_blocks;
-  const int block = keys ? blockIdx.x - p.q_blocks : blockIdx.x;
-  const int blocks = keys ? gridDim.x - p.q_blocks : p.q_blocks;
-  const HeadCut& cut = keys ? p.key_cut : p.cut;
+  const bool keys = static_cast<int>(blockIdx.x) >= p.q.blocks;
+  const HeadCut& cut = keys ? p.k : p.q;
   const int heads = keys ? a.k_heads : a.q_heads;
   const mfr_heads& in = keys ? a.k : a.q;
   const mfr_heads& out = keys ? a.k_out : a.q_out;
   const mfr_heads& dout = keys ? a.d_k_out : a.d_q_out;
-  const bool want = (keys ? a.d_k_weight : a.d_q_weight) != nullptr;
-  const int gpt = 1 << cut.gpt_log2, sub = group & (gpt - 1);
-  const int rounds = (heads + gpt - 1) >> cut.gpt_log2;
+  const int gl = cut.gpt_log2, sub = group & ((1 << gl) - 1);
+  const float4* turn = &caches[wid][group >> gl][0][lane % G];
   const float inv_d = 1.0f / static_cast<float>(a.D);
+  const int64_t step = static_cast<int64_t>(cut.blocks) * kHeadWarps;
+  int64_t task = static_cast<int64_t>(blockIdx.x - (keys ? p.q.blocks : 0)) * kHeadWarps + wid;
   pdl_launch_dependents();
   pdl_wait();
-  fill_weight<A, STYLE>(a, keys ? a.k_weight : a.q_weight, 0, weights);
+  Place q = place_of<G>(a, cut, task, group);
+  const uint8_t* x_src = static_cast<const uint8_t*>(in.data);
+  const uint8_t* g_src = static_cast<const uint8_t*>(dout.data);
+  uint8_t* dst = static_cast<uint8_t*>(out.data);
+  auto live = [&](const Place& z, int r) { return on && z.pos >= 0 && (r << gl) + sub < heads; };
+  Raw xr = load_raw(x_src + head_at(in, q, q.r0, gl, sub), m, live(q, q.r0));
+  Raw gr = load_raw(g_src + head_at(dout, q, q.r0, gl, sub), m, live(q, q.r0));
+  fill_weight<A, STYLE>(a, keys ? a.k_weight : a.q_weight, 0, weight);
   fill_turns(a, table);
   Pairs dw;
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = make_float2(0.0f, 0.0f);
-  const int64_t x_step = 2 * in.head_stride << cut.gpt_log2, g_step = 2 * dout.head_stride << cut.gpt_log2;
-  const int64_t o_step = 2 * out.head_stride << cut.gpt_log2;
-  for (int64_t task = static_cast<int64_t>(block) * kHeadWarps + wid; task < cut.tasks; task += static_cast<int64_t>(blocks) * kHeadWarps) {
-    const int split = static_cast<int>(task % cut.splits);
-    const int64_t t = (task / cut.splits) * ((32 / G) >> cut.gpt_log2) + (group >> cut.gpt_log2);
-    const int64_t pos = t < a.T ? position_of(a, t) : -1;
-    const bool write = on && t < a.T, read = on && pos >= 0;
-    const int r0 = static_cast<int>(static_cast<int64_t>(rounds) * split / cut.splits);
-    const int r1 = static_cast<int>(static_cast<int64_t>(rounds) * (split + 1) / cut.splits);
-    int h = (r0 << cut.gpt_log2) + sub;
-    const uint8_t* xp = static_cast<const uint8_t*>(in.data) + 2 * (t * in.token_stride + h * in.head_stride);
-    const uint8_t* gp = static_cast<const uint8_t*>(dout.data) + 2 * (t * dout.token_stride + h * dout.head_stride);
-    uint8_t* op = static_cast<uint8_t*>(out.data) + 2 * (t * out.token_stride + h * out.head_stride);
-    Raw xr = load_raw(xp, m, read && h < heads), gr = load_raw(gp, m, read && h < heads);
-    float2 cs[4], sn[4];
-    turns(a, table, m, read ? pos : 0, cs, sn);
-    for (int r = r0; r < r1; ++r) {
+  const int64_t x_step = 2 * in.head_stride << gl, g_step = 2 * dout.head_stride << gl, o_step = 2 * out.head_stride << gl;
+  while (task < cut.tasks) {
+    task += step;
+    const Place next = place_of<G>(a, cut, task, group);
+    fill_cache<G>(a, table, q.pos, gl, lane, caches[wid]);
+    const uint8_t* xp = x_src + head_at(in, q, q.r0, gl, sub);
+    const uint8_t* gp = g_src + head_at(dout, q, q.r0, gl, sub);
+    uint8_t* op = dst + head_at(out, q, q.r0, gl, sub);
+    for (int r = q.r0; r < q.r1; ++r) {
       const Pairs x = unpack_pairs_of<A, STYLE>(xr);
       Pairs g = unpack_pairs_of<A, STYLE>(gr);
       xp += x_step;
       gp += g_step;
-      const bool next = read && r + 1 < r1 && h + gpt < heads;
-      xr = load_raw(xp, m, next);
-      gr = load_raw(gp, m, next);
-      turn_pairs<true>(g, cs, sn);
+      if (r + 1 == q.r1) {
+        xr = load_raw(x_src + head_at(in, next, next.r0, gl, sub), m, live(next, next.r0));
+        gr = load_raw(g_src + head_at(dout, next, next.r0, gl, sub), m, live(next, next.r0));
+      } else {
+        xr = load_raw(xp, m, live(q, r + 1));
+        gr = load_raw(gp, m, live(q, r + 1));
+      }
+      turn_pairs<true, G>(g, turn);
       // sums of x^2 and of (g w) x
       float2 sq = make_float2(0.0f, 0.0f), dot = make_float2(0.0f, 0.0f);
       Pairs gw;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 w = weights[j][lane % G];
+        const float4 w = weight[j][lane % G];
         gw.a[j] = __fmul2_rn(g.a[j], make_float2(w.x, w.y));
         gw.b[j] = __fmul2_rn(g.b[j], make_float2(w.z, w.w));
         sq = __ffma2_rn(x.a[j], x.a[j], sq);
@@ -366,18 +411,18 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_norm_grad_kernel(const _
         d.a[j] = __ffma2_rn(x.a[j], cc, __fmul2_rn(gw.a[j], rr));
         d.b[j] = __ffma2_rn(x.b[j], cc, __fmul2_rn(gw.b[j], rr));
       }
-      if (write && h < heads) {
-        if (!read) {
+      if (on && q.t < a.T && (r << gl) + sub < heads) {
+        if (q.pos < 0) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) d.a[j] = d.b[j] = make_float2(0.0f, 0.0f);
         }
         store_pairs<A, STYLE>(op, m, d);
       }
       op += o_step;
-      h += gpt;
     }
+    q = next;
   }
-  if (!want) return;
+  if ((keys ? a.d_k_weight : a.d_q_weight) == nullptr) return;
   // over the warp's groups (lanes G apart), then over the CTA's warps in order
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -429,7 +474,7 @@ __global__ void __launch_bounds__(kSumThreads) head_weight_grad_kernel(const __g
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int d = (blockIdx.x % parts) * 32 + lane;
-  const int64_t b0 = keys ? p.q_blocks : 0, b1 = keys ? p.blocks : p.q_blocks;
+  const int64_t b0 = keys ? p.q.blocks : 0, b1 = p.q.blocks + (keys ? p.k.blocks : 0);
   float s = 0.0f;
   if (d < a.D) {
 #pragma unroll 4
@@ -480,57 +525,51 @@ int groups_of(int D) {
 
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Cuts `heads` heads (of one kind, or the larger of two) of T tokens for `warps` warps: as many groups on a token
-// as it has heads for, and a token's rounds in more ranges when the tokens alone leave warps idle.
-HeadCut cut_heads(int T, int q_heads, int k_heads, int groups, int64_t warps) {
-  HeadCut c{0, 1, 0};
-  const int most = q_heads > k_heads ? q_heads : k_heads;
-  while ((2 << c.gpt_log2) <= groups && (2 << c.gpt_log2) <= most) ++c.gpt_log2;
-  const int64_t rounds = ceil_div64(q_heads, 1 << c.gpt_log2) + ceil_div64(k_heads, 1 << c.gpt_log2);
+// Cuts one kind's heads for at most `most` CTAs: as many groups on a token as it has heads for, and a token's rounds
+// in more ranges when the tokens alone leave warps idle.
+HeadCut cut_heads(int T, int heads, int groups, int64_t most) {
+  HeadCut c{};
+  if (heads == 0 || T == 0) return c;
+  while ((2 << c.gpt_log2) <= groups && (2 << c.gpt_log2) <= heads) ++c.gpt_log2;
+  c.rounds = static_cast<int>(ceil_div64(heads, 1 << c.gpt_log2));
   const int64_t blocks = ceil_div64(T, groups >> c.gpt_log2);
-  int64_t splits = blocks > 0 ? warps / blocks : 1;
-  if (splits > rounds) splits = rounds;
+  int64_t splits = most * kHeadWarps / blocks;
+  if (splits > c.rounds) splits = c.rounds;
   if (splits < 1) splits = 1;
   c.splits = static_cast<int>(splits);
   c.tasks = blocks * splits;
+  const int64_t want = ceil_div64(c.tasks, kHeadWarps);
+  c.blocks = static_cast<int>(want < most ? want : most);
   return c;
+}
+
+// Shares `blocks` CTAs between the kinds in proportion to their work: a token's rounds, and its turns (about one
+// round's work); at least one for each kind that has heads.
+HeadParams cut_kinds(const mfr_head_norm_args& a, int blocks) {
+  HeadParams p{a, {}, {}};
+  const int groups = groups_of(a.D);
+  const int64_t wq = a.q_heads > 0 ? ceil_div64(a.q_heads, groups) + 1 : 0, wk = a.k_heads > 0 ? ceil_div64(a.k_heads, groups) + 1 : 0;
+  int64_t q = blocks * wq / (wq + wk);
+  if (a.q_heads > 0 && q == 0) q = 1;
+  if (a.k_heads > 0 && q == blocks) q = blocks - 1;
+  p.q = cut_heads(a.T, a.q_heads, groups, q);
+  p.k = cut_heads(a.T, a.k_heads, groups, blocks - q);
+  return p;
 }
 
 }  // namespace
 
 cudaError_t launch_head_norm(const mfr_head_norm_args& a, cudaStream_t stream) {
-  HeadParams p{a, {}, {}, 0, 0};
-  p.cut = cut_heads(a.T, a.q_heads, a.k_heads, groups_of(a.D), 152 * 3 * kHeadWarps);
-  const int64_t blocks = ceil_div64(p.cut.tasks, kHeadWarps);
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, static_cast<int>(blocks), false, stream)
-                                 : launch_s<__half>(p, static_cast<int>(blocks), false, stream);
+  const HeadParams p = cut_kinds(a, 152 * HEADS_KB);
+  const int blocks = p.q.blocks + p.k.blocks;
+  return a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, blocks, false, stream) : launch_s<__half>(p, blocks, false, stream);
 }
 
 cudaError_t launch_head_norm_backward(const mfr_head_norm_args& a, cudaStream_t stream) {
-  HeadParams p{a, {}, {}, 0, 0};
+  const HeadParams p = cut_kinds(a, kHeadGradBlocks);
   cudaError_t e = cudaSuccess;
-  if (a.T > 0) {
-    const int groups = groups_of(a.D);
-    // CTAs in proportion to the kinds' work: a token's rounds, and its sines and cosines (about two rounds)
-    auto weight = [&](int heads) { return heads > 0 ? ceil_div64(heads, groups) + 2 : 0; };
-    const int64_t wq = weight(a.q_heads), wk = weight(a.k_heads);
-    int q = static_cast<int>(kHeadGradBlocks * wq / (wq + wk)), k = kHeadGradBlocks - q;
-    if (a.q_heads > 0 && q == 0) q = 1;
-    if (a.k_heads > 0 && k == 0) k = 1;
-    if (q + k > kHeadGradBlocks) (q > k ? q : k) -= 1;
-    auto plan = [&](int heads, int most, HeadCut* cut) {
-      if (heads == 0) return 0;
-      *cut = cut_heads(a.T, heads, 0, groups, static_cast<int64_t>(most) * kHeadWarps);
-      const int64_t want = ceil_div64(cut->tasks, kHeadWarps);
-      return static_cast<int>(want < most ? want : most);
-    };
-    q = plan(a.q_heads, q, &p.cut);
-    k = plan(a.k_heads, k, &p.key_cut);
-    p.q_blocks = q;
-    p.blocks = q + k;
-    e = a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, p.blocks, true, stream) : launch_s<__half>(p, p.blocks, true, stream);
-  }
+  const int blocks = p.q.blocks + p.k.blocks;
+  if (a.T > 0) e = a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, blocks, true, stream) : launch_s<__half>(p, blocks, true, stream);
   // (no tokens: no partial sums, and the weight gradients are zeros)
   if (e != cudaSuccess || (a.d_q_weight == nullptr && a.d_k_weight == nullptr)) return e;
   return launch_pdl<HeadParams>(head_weight_grad_kernel, dim3(2 * ((a.D + 31) / 32)), kSumThreads, 0, a.flags & MFR_FLAG_PDL, stream, p);
