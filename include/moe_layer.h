@@ -198,8 +198,8 @@ typedef struct {
  *     (a, b) -> (a cos - b sin, b cos + a sin) * rotary_scale;   the other elements pass
  *   out = round_act(...)                                       one rounding, after the rotation
  * The angle is reduced exactly (integer arithmetic modulo one turn), so that far positions lose nothing;
- * |inv_freq| < 2^20.  A token whose position is negative is padding: it is not read, and its output rows are
- * left as they were, or set to zero under MFR_FLAG_ZERO_PADDING.  An output may be its own input, with equal
+ * |inv_freq| < 2^20.  A token whose position is negative is padding: its values do not matter, and its output rows
+ * are left as they were, or set to zero under MFR_FLAG_ZERO_PADDING.  An output may be its own input, with equal
  * strides (in place); otherwise outputs overlap no input and not each other. */
 typedef struct {
   int32_t T;                 /* tokens, >= 0                                                            */

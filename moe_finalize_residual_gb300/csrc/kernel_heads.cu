@@ -14,31 +14,37 @@
 // a turn (24-bit significand times 1 / (2 pi) to 64 bits), so the product with the position, modulo 2^64, is
 // the fraction of the turn, with an error of position * 2^-64 turns.
 //
+// The work is cut into rounds: one head for each of a warp's groups.  A warp keeps the vectors of its next rounds in
+// flight by cp.async into slots of shared memory that each lane fills and reads by itself, so no warp waits for
+// another.
+//
 // Bound by HBM: forward reads and writes each element once; backward reads two and writes one.
+#include <algorithm>
+
 #include "layer_launch.h"
 
 namespace mfr {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kHeadThreads = 256;
-constexpr int kHeadWarps = kHeadThreads / 32;
 
-// How a launch cuts one kind's work (queries or keys).  A warp's groups take `1 << gpt_log2` heads of a token at a
-// time (a round) and the warp as many tokens as that leaves groups for; a token's rounds are cut into `splits`
-// ranges.  A task is a block of tokens and a range; the kind's warps walk the tasks.
+// How a launch cuts its work.  A warp's groups take `1 << gpt_log2` heads of a token at a time (a round: first the
+// queries', then the keys') and the warp as many tokens (a block) as that leaves groups for; `splits` warps share a
+// block's rounds.
 struct HeadCut {
   int gpt_log2;
-  int rounds;
+  int q_rounds, k_rounds;
   int splits;
-  int blocks;     // CTAs of the kind
-  int64_t tasks;
+  int cache_bytes;      // a warp's turn cache
+  int64_t blocks;       // of tokens
+  int64_t team_blocks;  // backward: blocks that a team of `splits` warps takes one after the other
+  int64_t warps;
+  int ctas;
 };
 
-// CTAs [0, q.blocks) take the queries, the rest the keys.
 struct HeadParams {
   mfr_head_norm_args a;
-  HeadCut q, k;
+  HeadCut cut;
 };
 
 // inv_freq / (2 pi) as a fraction of a turn times 2^64, modulo 2^64.
@@ -83,51 +89,19 @@ __device__ __forceinline__ LaneMap lane_map(int p, int rot, int style) {
   return m;
 }
 
-// Fills the CTA's table of turns (shared memory, rot / 2 entries).
-__device__ __forceinline__ void fill_turns(const mfr_head_norm_args& a, uint64_t* table) {
-  for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x) table[i] = turn_of(a.inv_freq[i]);
-  __syncthreads();
-}
-
 __device__ __forceinline__ int64_t position_of(const mfr_head_norm_args& a, int64_t t) {
   return (a.flags & MFR_FLAG_POSITIONS_64) ? static_cast<const int64_t*>(a.positions)[t]
                                            : static_cast<const int32_t*>(a.positions)[t];
 }
 
-// The cosines and sines of a warp's tokens: entry [(token, j, p)] holds pairs 8p + 2j and 8p + 2j + 1 of the token.
-template <int G>
-using TurnCache = float4[32 / G][4][G];
-
-// Fills a warp's cache: 1 and 0 for unrotated pairs, times rotary_scale else.  `pos`: the position of the lane's
-// group's token (gpt groups a token).
-template <int G>
-__device__ __forceinline__ void fill_cache(const mfr_head_norm_args& a, const uint64_t* table, int64_t pos, int gpt_log2, int lane,
-                                           TurnCache<G>& cache) {
-  const int entries = ((32 / G) >> gpt_log2) * 4 * G;
-  __syncwarp();  // the last task's turns are done with
-#pragma unroll 1
-  for (int first = 0; first < entries; first += 32) {
-    const int i = first + lane, token = i / (4 * G), j = i / G % 4, p = i % G;
-    const int64_t at = __shfl_sync(kAll, pos, ((token << gpt_log2) * G) & 31);
-    if (i >= entries) break;  // (the last iteration)
-    float c[2], s[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      c[k] = 1.0f;
-      s[k] = 0.0f;
-      const int pair = 8 * p + 2 * j + k;
-      if (pair < a.rot / 2) {
-        const uint64_t u = table[pair] * static_cast<uint64_t>(at);
-        // the nearest 2^-32 turn, as a half turn in [-1, 1)
-        const float h = static_cast<float>(static_cast<int32_t>((u + 0x80000000ULL) >> 32)) * 4.656612873077393e-10f;
-        sincospif(h, &s[k], &c[k]);
-        c[k] *= a.rotary_scale;
-        s[k] *= a.rotary_scale;
-      }
-    }
-    cache[token][j][p] = make_float4(c[0], c[1], s[0], s[1]);
-  }
-  __syncwarp();
+// The cosine and sine of an angle at a position, times `scale`.
+__device__ __forceinline__ float2 cos_sin(uint64_t turn, int64_t pos, float scale) {
+  const uint64_t u = turn * static_cast<uint64_t>(pos);
+  // the nearest 2^-32 turn, as a half turn in [-1, 1)
+  const float h = static_cast<float>(static_cast<int32_t>((u + 0x80000000ULL) >> 32)) * 4.656612873077393e-10f;
+  float s, c;
+  sincospif(h, &s, &c);
+  return make_float2(c * scale, s * scale);
 }
 
 // A lane's 16 elements of a head as they lie in memory, and as its pairs' first and second elements.
@@ -138,12 +112,7 @@ struct Pairs {
   float2 a[4], b[4];
 };
 
-__device__ __forceinline__ Raw load_raw(const uint8_t* p, const LaneMap& m, bool on) {
-  Raw r;
-  r.a = on ? ldg16(p + 2 * m.off_a) : make_uint4(0, 0, 0, 0);
-  r.b = on ? ldg16(p + 2 * m.off_b) : make_uint4(0, 0, 0, 0);
-  return r;
-}
+__device__ __forceinline__ Raw load_raw(const uint8_t* p, const LaneMap& m) { return {ldg16(p + 2 * m.off_a), ldg16(p + 2 * m.off_b)}; }
 
 template <typename A, int STYLE>
 __device__ __forceinline__ Pairs unpack_pairs_of(const Raw& r) {
@@ -164,7 +133,7 @@ __device__ __forceinline__ Pairs unpack_pairs_of(const Raw& r) {
 }
 
 template <typename A, int STYLE>
-__device__ __forceinline__ void store_pairs(uint8_t* p, const LaneMap& m, const Pairs& v) {
+__device__ __forceinline__ void store_pairs(uint8_t* p, int second, const Pairs& v) {
   uint32_t w[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -176,44 +145,53 @@ __device__ __forceinline__ void store_pairs(uint8_t* p, const LaneMap& m, const 
       w[2 * j + 1] = Act<A>::pack(v.a[j].y, v.b[j].y);
     }
   }
-  *reinterpret_cast<uint4*>(p + 2 * m.off_a) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(p + 2 * m.off_b) = make_uint4(w[4], w[5], w[6], w[7]);
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(p + second) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// A kind's weight (ones without one) as each lane's pairs, in shared memory: [4][lanes of a head] vectors of (a, b)
-// pairs, read without bank conflicts.  Threads first .. first + D / 16 - 1 of the CTA fill it.
-using WeightTable = float4[4][MFR_MAX_HEAD_DIM / 16];
+
+// What a warp's tokens turn by, in shared memory: for lane p of a head and its pairs 2j and 2j + 1 two vectors that fold
+// the weight in, so that the rotation of the normed head is  a' = a A1 + b A2,  b' = b B1 + a B2:
+//   [kind][token][j][0][p] = A1 = c w_a, A2 = -s w_b      [..][1][p] = B1 = c w_b, B2 = s w_a      (two pairs each)
+template <int G>
+using TurnCache = float4 (*)[4][2][G];
+
+// A weight's elements of a pair (ones without a weight).
 template <typename A, int STYLE>
-__device__ __forceinline__ void fill_weight(const mfr_head_norm_args& a, const void* w, int first, WeightTable& table) {
-  const int lane = static_cast<int>(threadIdx.x) - first;
-  if (lane < 0 || lane >= a.D / 16) return;
-  Pairs v;
-  if (w != nullptr) {
-    v = unpack_pairs_of<A, STYLE>(load_raw(static_cast<const uint8_t*>(w), lane_map(lane, a.rot, STYLE), true));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v.a[j] = v.b[j] = make_float2(1.0f, 1.0f);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) table[j][lane] = make_float4(v.a[j].x, v.a[j].y, v.b[j].x, v.b[j].y);
+__device__ __forceinline__ float2 weight_pair(const void* w, int p, int k, const LaneMap& m) {
+  if (w == nullptr) return make_float2(1.0f, 1.0f);
+  // pair k of lane p: elements off_a + k and off_b + k, or off_a + 2k and off_a + 2k + 1
+  const int e0 = STYLE == MFR_ROTARY_HALF ? m.off_a + k : m.off_a + 2 * k, e1 = STYLE == MFR_ROTARY_HALF ? m.off_b + k : e0 + 1;
+  const A* v = static_cast<const A*>(w);
+  return make_float2(static_cast<float>(v[e0]), static_cast<float>(v[e1]));
 }
 
-// Turns a lane's pairs by the angle, or back; `turn`: the token's cache at the lane, G entries apart.
-template <bool BACK, int G>
-__device__ __forceinline__ void turn_pairs(Pairs& v, const float4* turn) {
+// Fills a warp's cache for its block of tokens; `pos`: the position of the lane's group's token.
+template <typename A, int G, int STYLE>
+__device__ __forceinline__ void fill_cache(const mfr_head_norm_args& a, int64_t pos, int gpt_log2, int lane, TurnCache<G> cache) {
+  const int tokens = (32 / G) >> gpt_log2, entries = tokens * 4 * G;
+#pragma unroll 1
+  for (int first = 0; first < entries; first += 32) {
+    const int i = first + lane, token = i / (4 * G), j = i / G % 4, p = i % G;
+    const int64_t at = __shfl_sync(kAll, pos, ((token << gpt_log2) * G) & 31);
+    if (i >= entries || p >= a.D / 16) continue;  // (the same trip count for all lanes)
+    const LaneMap m = lane_map(p, a.rot, STYLE);
+    float2 t[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 t = turn[j * G];
-    const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = v.a[j], b = v.b[j];
-    const float2 ac = __fmul2_rn(a, c), bc = __fmul2_rn(b, c);
-    if constexpr (BACK) {
-      v.a[j] = __ffma2_rn(b, s, ac);
-      v.b[j] = make_float2(__fmaf_rn(-a.x, s.x, bc.x), __fmaf_rn(-a.y, s.y, bc.y));
-    } else {
-      v.a[j] = make_float2(__fmaf_rn(-b.x, s.x, ac.x), __fmaf_rn(-b.y, s.y, ac.y));
-      v.b[j] = __ffma2_rn(a, s, bc);
+    for (int k = 0; k < 2; ++k) {
+      const int pair = 8 * p + 2 * j + k;
+      t[k] = pair < a.rot / 2 ? cos_sin(turn_of(a.inv_freq[pair]), at, a.rotary_scale) : make_float2(1.0f, 0.0f);
+    }
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const void* weight = kind ? a.k_weight : a.q_weight;
+      const float2 w0 = weight_pair<A, STYLE>(weight, p, 2 * j, m), w1 = weight_pair<A, STYLE>(weight, p, 2 * j + 1, m);
+      auto entry = cache[kind * tokens + token][j];
+      entry[0][p] = make_float4(t[0].x * w0.x, t[1].x * w1.x, -t[0].y * w0.y, -t[1].y * w1.y);
+      entry[1][p] = make_float4(t[0].x * w0.y, t[1].x * w1.y, t[0].y * w0.x, t[1].y * w1.x);
     }
   }
+  __syncwarp();
 }
 
 template <int G>
@@ -226,204 +204,197 @@ __device__ __forceinline__ float group_sum(float v) {
 // 1 / sqrt(sum / D + eps): the norm's statistic in FP32, within 2 ulp of the root.
 __device__ __forceinline__ float rstd_of(float sum, float inv_d, float eps) { return rsqrtf(__fmaf_rn(sum, inv_d, eps)); }
 
-#ifndef HEADS_KB
-#define HEADS_KB 4
-#endif
-
-// A warp's place in its kind's tasks: the token and the rounds of the current one.
-struct Place {
-  int64_t t;
-  int64_t pos;  // -1 behind the last token
-  int r0, r1;
+// A lane's way through the rounds of a block's queries and then keys: its first vector of its group's head.
+struct Walk {
+  uint8_t* at;
+  uint8_t* keys;  // where the keys begin
+  int64_t step, key_step;
+  __device__ __forceinline__ void start(const mfr_heads& q, const mfr_heads& k, const HeadCut& cut, int64_t t, int sub, int offset, int r) {
+    step = 2 * q.head_stride << cut.gpt_log2;
+    key_step = 2 * k.head_stride << cut.gpt_log2;
+    keys = static_cast<uint8_t*>(k.data) + 2 * (t * k.token_stride + sub * k.head_stride + offset);
+    at = static_cast<uint8_t*>(q.data) + 2 * (t * q.token_stride + sub * q.head_stride + offset) + r * step;
+    if (r >= cut.q_rounds) {
+      at = keys + (r - cut.q_rounds) * key_step;
+      step = key_step;
+    }
+  }
+  // to round r + 1
+  __device__ __forceinline__ void next(const HeadCut& cut, int r) {
+    at += step;
+    if (r + 1 == cut.q_rounds) {
+      at = keys;
+      step = key_step;
+    }
+  }
 };
-template <int G>
-__device__ __forceinline__ Place place_of(const mfr_head_norm_args& a, const HeadCut& cut, int64_t task, int group) {
-  Place q;
-  int split = 0;
-  int64_t block = task;
+
+// Slots of a warp's rounds in flight: N vectors a lane and round, each lane its own.
+template <int S, int N>
+constexpr int kSlotBytes = S * N * 32 * 16;
+
+#ifndef FS
+#define FS 4
+#endif
+#ifndef FT
+#define FT 64
+#endif
+#ifndef FC
+#define FC 16
+#endif
+constexpr int kFwdSlots = FS;
+constexpr int kFwdThreads = FT;
+constexpr int kFwdCtas = FC;  // CTAs an SM holds, by registers
+
+// Forward: a warp takes its rounds of one block of tokens.  The CTAs are small and come and go, which evens out the
+// SMs' load; a warp requests its first vectors, its position, frequencies and weights all at once.
+template <typename A, int G, int STYLE>
+__global__ void __launch_bounds__(kFwdThreads, kFwdCtas) head_norm_kernel(const __grid_constant__ HeadParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const mfr_head_norm_args& a = p.a;
+  const HeadCut& cut = p.cut;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
+  const bool lane_on = lane % G < a.D / 16;  // the other lanes double the first one's vectors and count nothing
+  const LaneMap m = lane_map(lane_on ? lane % G : 0, a.rot, STYLE);
+  const int second = 2 * (m.off_b - m.off_a);
+  const int gl = cut.gpt_log2, tokens = (32 / G) >> gl, sub = group & ((1 << gl) - 1);
+  uint8_t* mine = smem + wid * (kSlotBytes<kFwdSlots, 2> + cut.cache_bytes);
+  auto cache = reinterpret_cast<TurnCache<G>>(mine + kSlotBytes<kFwdSlots, 2>);
+  const uint32_t slot = smem_addr(mine) + lane * 16;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kFwdThreads / 32) + wid;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp >= cut.warps) return;
+  int64_t block = warp;
+  int r0 = 0, r1 = cut.q_rounds + cut.k_rounds;
   if (cut.splits > 1) {
-    block = task / cut.splits;
-    split = static_cast<int>(task - block * cut.splits);
+    block = warp / cut.splits;
+    const int split = static_cast<int>(warp - block * cut.splits), all = r1;
+    r0 = all * split / cut.splits;
+    r1 = all * (split + 1) / cut.splits;
   }
-  q.t = block * ((32 / G) >> cut.gpt_log2) + (group >> cut.gpt_log2);
-  q.r0 = cut.splits > 1 ? static_cast<int>(static_cast<int64_t>(cut.rounds) * split / cut.splits) : 0;
-  q.r1 = cut.splits > 1 ? static_cast<int>(static_cast<int64_t>(cut.rounds) * (split + 1) / cut.splits) : cut.rounds;
-  q.pos = task < cut.tasks && q.t < a.T ? position_of(a, q.t) : -1;
-  return q;
-}
-
-// The lane's vectors of its group's head in round r of a place.
-__device__ __forceinline__ int64_t head_at(const mfr_heads& h, const Place& q, int r, int gpt_log2, int sub) {
-  return 2 * (q.t * h.token_stride + ((static_cast<int64_t>(r) << gpt_log2) + sub) * h.head_stride);
-}
-
-// Forward.  The next round's vectors (of the next task after a task's last round) are in flight while one is worked on.
-template <typename A, int G, int STYLE>
-__global__ void __launch_bounds__(kHeadThreads, HEADS_KB) head_norm_kernel(const __grid_constant__ HeadParams p) {
-  __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
-  __shared__ WeightTable weight;
-  __shared__ TurnCache<G> caches[kHeadWarps];
-  const mfr_head_norm_args& a = p.a;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
-  const bool on = lane % G < a.D / 16;
-  const LaneMap m = lane_map(lane % G, a.rot, STYLE);
-  const bool keys = static_cast<int>(blockIdx.x) >= p.q.blocks;
-  const HeadCut& cut = keys ? p.k : p.q;
-  const int heads = keys ? a.k_heads : a.q_heads;
-  const mfr_heads& in = keys ? a.k : a.q;
-  const mfr_heads& out = keys ? a.k_out : a.q_out;
-  const int gl = cut.gpt_log2, sub = group & ((1 << gl) - 1);
-  const float4* turn = &caches[wid][group >> gl][0][lane % G];
-  const float inv_d = 1.0f / static_cast<float>(a.D);
-  const int64_t step = static_cast<int64_t>(cut.blocks) * kHeadWarps;
-  int64_t task = static_cast<int64_t>(blockIdx.x - (keys ? p.q.blocks : 0)) * kHeadWarps + wid;
-  pdl_launch_dependents();
-  pdl_wait();
-  Place q = place_of<G>(a, cut, task, group);
-  const uint8_t* src = static_cast<const uint8_t*>(in.data);
-  uint8_t* dst = static_cast<uint8_t*>(out.data);
-  auto live = [&](const Place& z, int r) { return on && z.pos >= 0 && (r << gl) + sub < heads; };
-  Raw raw = load_raw(src + head_at(in, q, q.r0, gl, sub), m, live(q, q.r0));
-  fill_weight<A, STYLE>(a, keys ? a.k_weight : a.q_weight, 0, weight);
-  fill_turns(a, table);
-  const int64_t src_step = 2 * in.head_stride << gl, dst_step = 2 * out.head_stride << gl;
-  while (task < cut.tasks) {
-    task += step;
-    const Place next = place_of<G>(a, cut, task, group);
-    fill_cache<G>(a, table, q.pos, gl, lane, caches[wid]);
-    const uint8_t* sp = src + head_at(in, q, q.r0, gl, sub);
-    uint8_t* dp = dst + head_at(out, q, q.r0, gl, sub);
-    for (int r = q.r0; r < q.r1; ++r) {  // the same trip count for the whole warp
-      Pairs v = unpack_pairs_of<A, STYLE>(raw);
-      sp += src_step;
-      if (r + 1 == q.r1) {
-        raw = load_raw(src + head_at(in, next, next.r0, gl, sub), m, live(next, next.r0));
-      } else {
-        raw = load_raw(sp, m, live(q, r + 1));
-      }
-      float2 sq = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sq = __ffma2_rn(v.a[j], v.a[j], sq);
-        sq = __ffma2_rn(v.b[j], v.b[j], sq);
-      }
-      const float rs = rstd_of(group_sum<G>(sq.x + sq.y), inv_d, a.eps);
-      const float2 rr = make_float2(rs, rs);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 w = weight[j][lane % G];
-        v.a[j] = __fmul2_rn(__fmul2_rn(v.a[j], rr), make_float2(w.x, w.y));
-        v.b[j] = __fmul2_rn(__fmul2_rn(v.b[j], rr), make_float2(w.z, w.w));
-      }
-      turn_pairs<false, G>(v, turn);
-      if (live(q, r)) {
-        store_pairs<A, STYLE>(dp, m, v);
-      } else if ((a.flags & MFR_FLAG_ZERO_PADDING) && on && q.t < a.T && (r << gl) + sub < heads) {
-        *reinterpret_cast<uint4*>(dp + 2 * m.off_a) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dp + 2 * m.off_b) = make_uint4(0, 0, 0, 0);
-      }
-      dp += dst_step;
+  const int64_t t = block * tokens + (group >> gl);
+  const bool in = t < a.T;
+  // the rounds that the lane's group has heads for, of each kind
+  const int q_last = (a.q_heads - sub + (1 << gl) - 1) >> gl, k_last = cut.q_rounds + ((a.k_heads - sub + (1 << gl) - 1) >> gl);
+  Walk src, dst;
+  src.start(a.q, a.k, cut, t, sub, m.off_a, r0);
+  auto request = [&](int r, int to_slot) {
+    if (r < r1) {
+      const bool take = in && r < (r < cut.q_rounds ? q_last : k_last);
+      const uint32_t to = slot + to_slot * (2 * 32 * 16);
+      cp_async16_if(to, src.at, take);
+      cp_async16_if(to + 32 * 16, src.at + second, take);
+      src.next(cut, r);
     }
-    q = next;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kFwdSlots - 1; ++i) request(r0 + i, i);
+  const int64_t pos = in ? position_of(a, t) : -1;
+  dst.start(a.q_out, a.k_out, cut, t, sub, m.off_a, r0);
+  fill_cache<A, G, STYLE>(a, pos, gl, lane, cache);
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  const bool write = lane_on && in && (pos >= 0 || (a.flags & MFR_FLAG_ZERO_PADDING));
+  int here = 0;  // the slot of the current round
+  for (int r = r0; r < r1; ++r) {  // the same trip count for the whole warp
+    const float4* turn = &cache[(r < cut.q_rounds ? 0 : tokens) + (group >> gl)][0][0][lane % G];
+    cp_async_wait_group<kFwdSlots - 2>();
+    const uint32_t from = slot + here * (2 * 32 * 16);
+    const Raw raw{lds16(from), lds16(from + 32 * 16)};
+    request(r + kFwdSlots - 1, here == 0 ? kFwdSlots - 1 : here - 1);
+    here = here + 1 == kFwdSlots ? 0 : here + 1;
+    const Pairs x = unpack_pairs_of<A, STYLE>(raw);
+    float2 sq = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sq = __ffma2_rn(x.a[j], x.a[j], sq);
+      sq = __ffma2_rn(x.b[j], x.b[j], sq);
+    }
+    const float rs = rstd_of(group_sum<G>(lane_on ? sq.x + sq.y : 0.0f), inv_d, a.eps);
+    const float2 rr = make_float2(rs, rs);
+    Pairs v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 ta = turn[2 * j * G], tb = turn[(2 * j + 1) * G];
+      const float2 xa = __fmul2_rn(x.a[j], rr), xb = __fmul2_rn(x.b[j], rr);
+      v.a[j] = __ffma2_rn(xb, make_float2(ta.z, ta.w), __fmul2_rn(xa, make_float2(ta.x, ta.y)));
+      v.b[j] = __ffma2_rn(xa, make_float2(tb.z, tb.w), __fmul2_rn(xb, make_float2(tb.x, tb.y)));
+    }
+    if (write && r < (r < cut.q_rounds ? q_last : k_last)) {
+      if (pos >= 0) {
+        store_pairs<A, STYLE>(dst.at, second, v);
+      } else {
+        *reinterpret_cast<uint4*>(dst.at) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst.at + second) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    dst.next(cut, r);
   }
 }
 
-// Gradient: as forward, with the lanes' share of the weight gradient in registers; each CTA leaves one row of partial
-// sums in the workspace.
-template <typename A, int G, int STYLE>
-__global__ void __launch_bounds__(kHeadThreads, 2) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
-  extern __shared__ float part[];  // [kHeadWarps][D]
-  __shared__ uint64_t table[MFR_MAX_HEAD_DIM / 2];
-  __shared__ WeightTable weight;
-  __shared__ TurnCache<G> caches[kHeadWarps];
-  const mfr_head_norm_args& a = p.a;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
-  const bool on = lane % G < a.D / 16;
-  const LaneMap m = lane_map(lane % G, a.rot, STYLE);
-  const bool keys = static_cast<int>(blockIdx.x) >= p.q.blocks;
-  const HeadCut& cut = keys ? p.k : p.q;
-  const int heads = keys ? a.k_heads : a.q_heads;
-  const mfr_heads& in = keys ? a.k : a.q;
-  const mfr_heads& out = keys ? a.k_out : a.q_out;
-  const mfr_heads& dout = keys ? a.d_k_out : a.d_q_out;
-  const int gl = cut.gpt_log2, sub = group & ((1 << gl) - 1);
-  const float4* turn = &caches[wid][group >> gl][0][lane % G];
-  const float inv_d = 1.0f / static_cast<float>(a.D);
-  const int64_t step = static_cast<int64_t>(cut.blocks) * kHeadWarps;
-  int64_t task = static_cast<int64_t>(blockIdx.x - (keys ? p.q.blocks : 0)) * kHeadWarps + wid;
-  pdl_launch_dependents();
-  pdl_wait();
-  Place q = place_of<G>(a, cut, task, group);
-  const uint8_t* x_src = static_cast<const uint8_t*>(in.data);
-  const uint8_t* g_src = static_cast<const uint8_t*>(dout.data);
-  uint8_t* dst = static_cast<uint8_t*>(out.data);
-  auto live = [&](const Place& z, int r) { return on && z.pos >= 0 && (r << gl) + sub < heads; };
-  Raw xr = load_raw(x_src + head_at(in, q, q.r0, gl, sub), m, live(q, q.r0));
-  Raw gr = load_raw(g_src + head_at(dout, q, q.r0, gl, sub), m, live(q, q.r0));
-  fill_weight<A, STYLE>(a, keys ? a.k_weight : a.q_weight, 0, weight);
-  fill_turns(a, table);
-  Pairs dw;
+
+#ifndef BS
+#define BS 3
+#endif
+constexpr int kBwdSlots = BS;
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
+
+// A kind's weight as each lane's pairs, in shared memory: [4][lanes of a head] vectors of (a, b) pairs.
+using WeightTable = float4[4][MFR_MAX_HEAD_DIM / 16];
+template <typename A, int STYLE>
+__device__ __forceinline__ void fill_weight(const mfr_head_norm_args& a, const void* w, int first, WeightTable& table) {
+  const int lane = static_cast<int>(threadIdx.x) - first;
+  if (lane < 0 || lane >= a.D / 16) return;
+  Pairs v;
+  if (w != nullptr) {
+    v = unpack_pairs_of<A, STYLE>(load_raw(static_cast<const uint8_t*>(w), lane_map(lane, a.rot, STYLE)));
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = make_float2(0.0f, 0.0f);
-  const int64_t x_step = 2 * in.head_stride << gl, g_step = 2 * dout.head_stride << gl, o_step = 2 * out.head_stride << gl;
-  while (task < cut.tasks) {
-    task += step;
-    const Place next = place_of<G>(a, cut, task, group);
-    fill_cache<G>(a, table, q.pos, gl, lane, caches[wid]);
-    const uint8_t* xp = x_src + head_at(in, q, q.r0, gl, sub);
-    const uint8_t* gp = g_src + head_at(dout, q, q.r0, gl, sub);
-    uint8_t* op = dst + head_at(out, q, q.r0, gl, sub);
-    for (int r = q.r0; r < q.r1; ++r) {
-      const Pairs x = unpack_pairs_of<A, STYLE>(xr);
-      Pairs g = unpack_pairs_of<A, STYLE>(gr);
-      xp += x_step;
-      gp += g_step;
-      if (r + 1 == q.r1) {
-        xr = load_raw(x_src + head_at(in, next, next.r0, gl, sub), m, live(next, next.r0));
-        gr = load_raw(g_src + head_at(dout, next, next.r0, gl, sub), m, live(next, next.r0));
-      } else {
-        xr = load_raw(xp, m, live(q, r + 1));
-        gr = load_raw(gp, m, live(q, r + 1));
-      }
-      turn_pairs<true, G>(g, turn);
-      // sums of x^2 and of (g w) x
-      float2 sq = make_float2(0.0f, 0.0f), dot = make_float2(0.0f, 0.0f);
-      Pairs gw;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 w = weight[j][lane % G];
-        gw.a[j] = __fmul2_rn(g.a[j], make_float2(w.x, w.y));
-        gw.b[j] = __fmul2_rn(g.b[j], make_float2(w.z, w.w));
-        sq = __ffma2_rn(x.a[j], x.a[j], sq);
-        sq = __ffma2_rn(x.b[j], x.b[j], sq);
-        dot = __ffma2_rn(gw.a[j], x.a[j], dot);
-        dot = __ffma2_rn(gw.b[j], x.b[j], dot);
-      }
-      const float rs = rstd_of(group_sum<G>(sq.x + sq.y), inv_d, a.eps);
-      const float c = group_sum<G>(dot.x + dot.y) * inv_d * rs * rs * rs;
-      const float2 rr = make_float2(rs, rs), cc = make_float2(-c, -c);
-      Pairs d;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // (a padding token's x and g are zeros)
-        dw.a[j] = __ffma2_rn(g.a[j], __fmul2_rn(x.a[j], rr), dw.a[j]);
-        dw.b[j] = __ffma2_rn(g.b[j], __fmul2_rn(x.b[j], rr), dw.b[j]);
-        d.a[j] = __ffma2_rn(x.a[j], cc, __fmul2_rn(gw.a[j], rr));
-        d.b[j] = __ffma2_rn(x.b[j], cc, __fmul2_rn(gw.b[j], rr));
-      }
-      if (on && q.t < a.T && (r << gl) + sub < heads) {
-        if (q.pos < 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d.a[j] = d.b[j] = make_float2(0.0f, 0.0f);
-        }
-        store_pairs<A, STYLE>(op, m, d);
-      }
-      op += o_step;
-    }
-    q = next;
+    for (int j = 0; j < 4; ++j) v.a[j] = v.b[j] = make_float2(1.0f, 1.0f);
   }
-  if ((keys ? a.d_k_weight : a.d_q_weight) == nullptr) return;
-  // over the warp's groups (lanes G apart), then over the CTA's warps in order
+#pragma unroll
+  for (int j = 0; j < 4; ++j) table[j][lane] = make_float4(v.a[j].x, v.a[j].y, v.b[j].x, v.b[j].y);
+}
+
+// What a warp's tokens turn by: [token][j][p], the cosines and the sines of pairs 2j and 2j + 1 of lane p.
+template <int G>
+__device__ __forceinline__ void fill_turns(const mfr_head_norm_args& a, int64_t pos, int gpt_log2, int lane, float4 (*cache)[4][G]) {
+  const int entries = ((32 / G) >> gpt_log2) * 4 * G;
+  __syncwarp();  // the last block's turns are done with
+#pragma unroll 1
+  for (int first = 0; first < entries; first += 32) {
+    const int i = first + lane, token = i / (4 * G), j = i / G % 4, p = i % G;
+    const int64_t at = __shfl_sync(kAll, pos, ((token << gpt_log2) * G) & 31);
+    if (i >= entries) continue;
+    float2 t[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int pair = 8 * p + 2 * j + k;
+      t[k] = pair < a.rot / 2 ? cos_sin(turn_of(a.inv_freq[pair]), at, a.rotary_scale) : make_float2(1.0f, 0.0f);
+    }
+    cache[token][j][p] = make_float4(t[0].x, t[1].x, t[0].y, t[1].y);
+  }
+  __syncwarp();
+}
+
+// Turns a lane's pairs back; `turn`: the token's turns at the lane.
+template <int G>
+__device__ __forceinline__ void turn_back(Pairs& v, const float4* turn) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 t = turn[j * G];
+    const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = v.a[j], b = v.b[j];
+    const float2 bc = __fmul2_rn(b, c);
+    v.a[j] = __ffma2_rn(b, s, __fmul2_rn(a, c));
+    v.b[j] = make_float2(__fmaf_rn(-a.x, s.x, bc.x), __fmaf_rn(-a.y, s.y, bc.y));
+  }
+}
+
+// Adds a lane's share of a weight gradient over the warp's groups (lanes G apart) and writes it to the warp's row.
+template <int G, int STYLE>
+__device__ __forceinline__ void write_sums(Pairs dw, const LaneMap& m, bool write, float* row) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -433,11 +404,7 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_norm_grad_kernel(const _
       dw.b[j].x += __shfl_xor_sync(kAll, dw.b[j].x, o);
       dw.b[j].y += __shfl_xor_sync(kAll, dw.b[j].y, o);
     }
-  }
-  if (group == 0 && on) {
-    float* row = part + wid * a.D;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    if (write) {
       if constexpr (STYLE == MFR_ROTARY_HALF) {
         row[m.off_a + 2 * j] = dw.a[j].x;
         row[m.off_a + 2 * j + 1] = dw.a[j].y;
@@ -451,56 +418,214 @@ __global__ void __launch_bounds__(kHeadThreads, 2) head_norm_grad_kernel(const _
       }
     }
   }
+}
+
+// A warp's shared memory in the gradient: its slots (later its sums), its turns, and each lane's share of the keys'
+// weight gradient (the queries' is in registers: they are the larger part).
+constexpr int kKeySumBytes = 4 * 32 * 16;
+__host__ __device__ constexpr int bwd_warp_bytes(int cache_bytes) { return kSlotBytes<kBwdSlots, 4> + cache_bytes + kKeySumBytes; }
+
+// Gradient: a warp takes its rounds of some neighbouring blocks, one after the other.
+template <typename A, int G, int STYLE>
+__global__ void __launch_bounds__(kBwdThreads, 2) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ WeightTable weights[2];
+  const mfr_head_norm_args& a = p.a;
+  const HeadCut& cut = p.cut;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane / G;
+  const bool lane_on = lane % G < a.D / 16;
+  const LaneMap m = lane_map(lane_on ? lane % G : 0, a.rot, STYLE);
+  const int second = 2 * (m.off_b - m.off_a);
+  const int gl = cut.gpt_log2, tokens = (32 / G) >> gl, sub = group & ((1 << gl) - 1);
+  uint8_t* mine = smem + wid * bwd_warp_bytes(cut.cache_bytes);
+  auto cache = reinterpret_cast<float4(*)[4][G]>(mine + kSlotBytes<kBwdSlots, 4>);
+  float4* key_sums = reinterpret_cast<float4*>(mine + kSlotBytes<kBwdSlots, 4> + cut.cache_bytes) + lane;  // [4][32]
+  const float4* turn = &cache[group >> gl][0][lane % G];
+  const uint32_t slot = smem_addr(mine) + lane * 16;
+  // the warp's blocks [block, block_end) and its rounds of each
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kBwdWarps + wid;
+  const int all = cut.q_rounds + cut.k_rounds;
+  const int64_t team = cut.splits > 1 ? warp / cut.splits : warp;
+  const int split = static_cast<int>(warp - team * cut.splits);
+  const int r0 = all * split / cut.splits, r1 = all * (split + 1) / cut.splits;
+  int64_t block = team * cut.team_blocks;
+  const int64_t block_end = block + cut.team_blocks < cut.blocks ? block + cut.team_blocks : cut.blocks;
+  const int q_last = (a.q_heads - sub + (1 << gl) - 1) >> gl, k_last = cut.q_rounds + ((a.k_heads - sub + (1 << gl) - 1) >> gl);
+  pdl_launch_dependents();
+  pdl_wait();
+  auto token = [&](int64_t b) { return b * tokens + (group >> gl); };
+  auto position = [&](int64_t b) { return b < block_end && token(b) < a.T ? position_of(a, token(b)) : -1; };
+  Walk xs, gs, dst;
+  int64_t next_block = block;
+  int next_r = r0;
+  bool next_in = false;
+  auto request = [&](int to_slot) {  // the next round, if there is one
+    if (next_block < block_end) {
+      if (next_r == r0) {
+        next_in = token(next_block) < a.T;
+        xs.start(a.q, a.k, cut, token(next_block), sub, m.off_a, r0);
+        gs.start(a.d_q_out, a.d_k_out, cut, token(next_block), sub, m.off_a, r0);
+      }
+      const bool take = next_in && next_r < (next_r < cut.q_rounds ? q_last : k_last);
+      const uint32_t to = slot + to_slot * (4 * 32 * 16);
+      cp_async16_if(to, xs.at, take);
+      cp_async16_if(to + 32 * 16, xs.at + second, take);
+      cp_async16_if(to + 2 * 32 * 16, gs.at, take);
+      cp_async16_if(to + 3 * 32 * 16, gs.at + second, take);
+      xs.next(cut, next_r);
+      gs.next(cut, next_r);
+      if (++next_r == r1) {
+        next_r = r0;
+        ++next_block;
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kBwdSlots - 1; ++i) request(i);
+  int64_t pos_next = position(block);
+  fill_weight<A, STYLE>(a, a.q_weight, 0, weights[0]);
+  fill_weight<A, STYLE>(a, a.k_weight, 32, weights[1]);
+  Pairs dw;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    dw.a[j] = dw.b[j] = make_float2(0.0f, 0.0f);
+    key_sums[32 * j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
   __syncthreads();
-  for (int d = threadIdx.x; d < a.D; d += kHeadThreads) {
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  int here = 0;  // the slot of the current round
+  for (; block < block_end; ++block) {
+    const int64_t pos = pos_next;
+    pos_next = position(block + 1);
+    const bool write = lane_on && token(block) < a.T;
+    dst.start(a.q_out, a.k_out, cut, token(block), sub, m.off_a, r0);
+    fill_turns<G>(a, pos, gl, lane, cache);
+    for (int r = r0; r < r1; ++r) {
+      const bool key = r >= cut.q_rounds;
+      cp_async_wait_group<kBwdSlots - 2>();
+      const uint32_t from = slot + here * (4 * 32 * 16);
+      const Raw xr{lds16(from), lds16(from + 32 * 16)}, gr{lds16(from + 2 * 32 * 16), lds16(from + 3 * 32 * 16)};
+      request(here == 0 ? kBwdSlots - 1 : here - 1);
+      here = here + 1 == kBwdSlots ? 0 : here + 1;
+      const Pairs x = unpack_pairs_of<A, STYLE>(xr);
+      Pairs g = unpack_pairs_of<A, STYLE>(gr);
+      turn_back<G>(g, turn);
+      // sums of x^2 and of (g w) x
+      float2 sq = make_float2(0.0f, 0.0f), dot = make_float2(0.0f, 0.0f);
+      Pairs gw;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = weights[key][j][lane % G];
+        gw.a[j] = __fmul2_rn(g.a[j], make_float2(w.x, w.y));
+        gw.b[j] = __fmul2_rn(g.b[j], make_float2(w.z, w.w));
+        sq = __ffma2_rn(x.a[j], x.a[j], sq);
+        sq = __ffma2_rn(x.b[j], x.b[j], sq);
+        dot = __ffma2_rn(gw.a[j], x.a[j], dot);
+        dot = __ffma2_rn(gw.b[j], x.b[j], dot);
+      }
+      const float rs = rstd_of(group_sum<G>(lane_on ? sq.x + sq.y : 0.0f), inv_d, a.eps);
+      const float c = group_sum<G>(lane_on ? dot.x + dot.y : 0.0f) * inv_d * rs * rs * rs;
+      const float2 rr = make_float2(rs, rs), cc = make_float2(-c, -c);
+      if (write && r < (key ? k_last : q_last)) {
+        Pairs d;
+        if (pos >= 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 xa = __fmul2_rn(x.a[j], rr), xb = __fmul2_rn(x.b[j], rr);
+            if (!key) {
+              dw.a[j] = __ffma2_rn(g.a[j], xa, dw.a[j]);
+              dw.b[j] = __ffma2_rn(g.b[j], xb, dw.b[j]);
+            } else {
+              const float4 s = key_sums[32 * j];
+              const float2 sa = __ffma2_rn(g.a[j], xa, make_float2(s.x, s.y)), sb = __ffma2_rn(g.b[j], xb, make_float2(s.z, s.w));
+              key_sums[32 * j] = make_float4(sa.x, sa.y, sb.x, sb.y);
+            }
+            d.a[j] = __ffma2_rn(x.a[j], cc, __fmul2_rn(gw.a[j], rr));
+            d.b[j] = __ffma2_rn(x.b[j], cc, __fmul2_rn(gw.b[j], rr));
+          }
+        } else {  // a padding token, whatever it holds
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d.a[j] = d.b[j] = make_float2(0.0f, 0.0f);
+        }
+        store_pairs<A, STYLE>(dst.at, second, d);
+      }
+      dst.next(cut, r);
+    }
+  }
+  if (a.d_q_weight == nullptr && a.d_k_weight == nullptr) return;
+  // over the warp's groups, then over the CTA's warps in order
+  cp_async_wait_all();
+  __syncwarp();
+  float* row = reinterpret_cast<float*>(mine);  // [2][D], in place of the slots
+  write_sums<G, STYLE>(dw, m, lane_on && group == 0, row);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 s = key_sums[32 * j];
+    dw.a[j] = make_float2(s.x, s.y);
+    dw.b[j] = make_float2(s.z, s.w);
+  }
+  write_sums<G, STYLE>(dw, m, lane_on && group == 0, row + a.D);
+  __syncthreads();
+  for (int d = threadIdx.x; d < 2 * a.D; d += kBwdThreads) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kHeadWarps; ++i) s += part[i * a.D + d];
-    static_cast<float*>(a.workspace)[static_cast<int64_t>(blockIdx.x) * a.D + d] = s;
+    for (int i = 0; i < kBwdWarps; ++i) s += reinterpret_cast<const float*>(smem + i * bwd_warp_bytes(cut.cache_bytes))[d];
+    static_cast<float*>(a.workspace)[static_cast<int64_t>(blockIdx.x) * 2 * a.D + d] = s;
   }
 }
 
-// Adds the partial weight gradients: CTA (kind, 32 elements), 32 rows at a time, then over the rows' warps
-// in order.
+// Adds the CTAs' partial weight gradients: a CTA takes 8 columns of the [2][D] rows, a warp 4 rows at a time; the sums
+// meet by a butterfly over the lanes of a column and then over the warps in order.
 constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) head_weight_grad_kernel(const __grid_constant__ HeadParams p) {
-  __shared__ float part[32][33];
+  __shared__ float part[kSumThreads / 32][8];
   const mfr_head_norm_args& a = p.a;
   pdl_launch_dependents();
   pdl_wait();
-  const int parts = (a.D + 31) / 32;
-  const bool keys = static_cast<int>(blockIdx.x) >= parts;
-  float* out = keys ? a.d_k_weight : a.d_q_weight;
-  if (out == nullptr) return;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int d = (blockIdx.x % parts) * 32 + lane;
-  const int64_t b0 = keys ? p.q.blocks : 0, b1 = p.q.blocks + (keys ? p.k.blocks : 0);
+  const int d = blockIdx.x * 8 + (lane & 7);
+  float* out = d < a.D ? a.d_q_weight : a.d_k_weight;  // (D is a multiple of 16: a CTA's columns are of one kind)
+  if (out == nullptr) return;
+  const float* rows = static_cast<const float*>(a.workspace) + d;
   float s = 0.0f;
-  if (d < a.D) {
-#pragma unroll 4
-    for (int64_t b = b0 + wid; b < b1; b += 32) s += static_cast<const float*>(a.workspace)[b * a.D + d];
-  }
-  part[wid][lane] = s;
+#pragma unroll 8
+  for (int64_t r = wid * 4 + (lane >> 3); r < p.cut.ctas; r += kSumThreads / 8) s += rows[r * 2 * a.D];
+  s += __shfl_xor_sync(kAll, s, 8);
+  s += __shfl_xor_sync(kAll, s, 16);
+  if (lane < 8) part[wid][lane] = s;
   __syncthreads();
-  const float v = warp_sum(part[lane][wid]);
-  if (lane == 0 && (blockIdx.x % parts) * 32 + wid < a.D) out[(blockIdx.x % parts) * 32 + wid] = v;
+  if (threadIdx.x < 8) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumThreads / 32; ++i) v += part[i][threadIdx.x];
+    out[d - (d < a.D ? 0 : a.D) - (lane & 7) + threadIdx.x] = v;
+  }
 }
 
 template <typename A, int G, int STYLE>
-cudaError_t launch_forward(const HeadParams& p, int blocks, cudaStream_t stream) {
-  return launch_pdl<HeadParams>(head_norm_kernel<A, G, STYLE>, dim3(blocks), kHeadThreads, 0, p.a.flags & MFR_FLAG_PDL, stream, p);
+cudaError_t launch_forward(const HeadParams& p, cudaStream_t stream) {
+  const int smem = kFwdThreads / 32 * (kSlotBytes<kFwdSlots, 2> + p.cut.cache_bytes);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<A, G, STYLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl<HeadParams>(head_norm_kernel<A, G, STYLE>, dim3(p.cut.ctas), kFwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
 }
 template <typename A, int G, int STYLE>
-cudaError_t launch_backward(const HeadParams& p, int blocks, cudaStream_t stream) {
-  return launch_pdl<HeadParams>(head_norm_grad_kernel<A, G, STYLE>, dim3(blocks), kHeadThreads, kHeadWarps * p.a.D * 4,
-                                p.a.flags & MFR_FLAG_PDL, stream, p);
+cudaError_t launch_backward(const HeadParams& p, cudaStream_t stream) {
+  static_assert(kSlotBytes<kBwdSlots, 4> >= 2 * MFR_MAX_HEAD_DIM * 4, "a warp's sums fit in its slots");
+  const int smem = kBwdWarps * bwd_warp_bytes(p.cut.cache_bytes);
+  const cudaError_t e = cudaFuncSetAttribute(head_norm_grad_kernel<A, G, STYLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl<HeadParams>(head_norm_grad_kernel<A, G, STYLE>, dim3(p.cut.ctas), kBwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
 }
 
 template <typename A, int STYLE>
-cudaError_t launch_g(const HeadParams& p, int blocks, bool backward, cudaStream_t stream) {
+cudaError_t launch_g(const HeadParams& p, bool backward, cudaStream_t stream) {
   const int lanes = p.a.D / 16;
 #define MFR_HEADS(G) \
-  if (lanes <= G) return backward ? launch_backward<A, G, STYLE>(p, blocks, stream) : launch_forward<A, G, STYLE>(p, blocks, stream)
+  if (lanes <= G) return backward ? launch_backward<A, G, STYLE>(p, stream) : launch_forward<A, G, STYLE>(p, stream)
   MFR_HEADS(1);
   MFR_HEADS(2);
   MFR_HEADS(4);
@@ -512,67 +637,54 @@ cudaError_t launch_g(const HeadParams& p, int blocks, bool backward, cudaStream_
 }
 
 template <typename A>
-cudaError_t launch_s(const HeadParams& p, int blocks, bool backward, cudaStream_t stream) {
-  return p.a.style == MFR_ROTARY_HALF ? launch_g<A, MFR_ROTARY_HALF>(p, blocks, backward, stream)
-                                      : launch_g<A, MFR_ROTARY_INTERLEAVED>(p, blocks, backward, stream);
-}
-
-int groups_of(int D) {
-  int g = 1;
-  while (g < D / 16) g *= 2;
-  return 32 / g;
+cudaError_t launch_s(const HeadParams& p, bool backward, cudaStream_t stream) {
+  return p.a.style == MFR_ROTARY_HALF ? launch_g<A, MFR_ROTARY_HALF>(p, backward, stream)
+                                      : launch_g<A, MFR_ROTARY_INTERLEAVED>(p, backward, stream);
 }
 
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Cuts one kind's heads for at most `most` CTAs: as many groups on a token as it has heads for, and a token's rounds
-// in more ranges when the tokens alone leave warps idle.
-HeadCut cut_heads(int T, int heads, int groups, int64_t most) {
+// Cuts the work: as many groups on a token as its larger kind has heads for; `warps` warps fill the GPU, and a block's
+// rounds are shared between so many warps that there are that many; `most`: warps at most (0: one for each block).
+HeadCut cut_heads(int T, int q_heads, int k_heads, int D, int cta_warps, int64_t warps, int64_t most, int entry_bytes) {
   HeadCut c{};
-  if (heads == 0 || T == 0) return c;
+  int G = 1;
+  while (G < D / 16) G *= 2;
+  const int groups = 32 / G, heads = std::max(q_heads, k_heads);
   while ((2 << c.gpt_log2) <= groups && (2 << c.gpt_log2) <= heads) ++c.gpt_log2;
-  c.rounds = static_cast<int>(ceil_div64(heads, 1 << c.gpt_log2));
-  const int64_t blocks = ceil_div64(T, groups >> c.gpt_log2);
-  int64_t splits = most * kHeadWarps / blocks;
-  if (splits > c.rounds) splits = c.rounds;
-  if (splits < 1) splits = 1;
-  c.splits = static_cast<int>(splits);
-  c.tasks = blocks * splits;
-  const int64_t want = ceil_div64(c.tasks, kHeadWarps);
-  c.blocks = static_cast<int>(want < most ? want : most);
+  c.q_rounds = static_cast<int>(ceil_div64(q_heads, 1 << c.gpt_log2));
+  c.k_rounds = static_cast<int>(ceil_div64(k_heads, 1 << c.gpt_log2));
+  const int tokens = groups >> c.gpt_log2;
+  c.cache_bytes = tokens * 4 * G * entry_bytes;
+  c.blocks = ceil_div64(T, tokens);
+  c.splits = static_cast<int>(std::min<int64_t>(c.q_rounds + c.k_rounds, std::max<int64_t>(1, c.blocks > 0 ? warps / c.blocks : 1)));
+  c.team_blocks = most > 0 ? std::max<int64_t>(1, ceil_div64(c.blocks, most)) : 1;
+  c.warps = ceil_div64(c.blocks, c.team_blocks) * c.splits;
+  c.ctas = static_cast<int>(ceil_div64(c.warps, cta_warps));
   return c;
 }
 
-// Shares `blocks` CTAs between the kinds in proportion to their work: a token's rounds, and its turns (about one
-// round's work); at least one for each kind that has heads.
-HeadParams cut_kinds(const mfr_head_norm_args& a, int blocks) {
-  HeadParams p{a, {}, {}};
-  const int groups = groups_of(a.D);
-  const int64_t wq = a.q_heads > 0 ? ceil_div64(a.q_heads, groups) + 1 : 0, wk = a.k_heads > 0 ? ceil_div64(a.k_heads, groups) + 1 : 0;
-  int64_t q = blocks * wq / (wq + wk);
-  if (a.q_heads > 0 && q == 0) q = 1;
-  if (a.k_heads > 0 && q == blocks) q = blocks - 1;
-  p.q = cut_heads(a.T, a.q_heads, groups, q);
-  p.k = cut_heads(a.T, a.k_heads, groups, blocks - q);
-  return p;
+HeadCut cut_backward(int T, int q_heads, int k_heads, int D) {
+  return cut_heads(T, q_heads, k_heads, D, kBwdWarps, 152 * 2 * kBwdWarps, kHeadGradBlocks * kBwdWarps, 16);
 }
 
 }  // namespace
 
+int head_grad_rows(int T, int q_heads, int k_heads, int D) { return cut_backward(T, q_heads, k_heads, D).ctas; }
+
 cudaError_t launch_head_norm(const mfr_head_norm_args& a, cudaStream_t stream) {
-  const HeadParams p = cut_kinds(a, 152 * HEADS_KB);
-  const int blocks = p.q.blocks + p.k.blocks;
-  return a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, blocks, false, stream) : launch_s<__half>(p, blocks, false, stream);
+  constexpr int kWarps = kFwdThreads / 32;
+  const HeadParams p{a, cut_heads(a.T, a.q_heads, a.k_heads, a.D, kWarps, 152 * kFwdCtas * kWarps, 0, 64)};
+  return a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, false, stream) : launch_s<__half>(p, false, stream);
 }
 
 cudaError_t launch_head_norm_backward(const mfr_head_norm_args& a, cudaStream_t stream) {
-  const HeadParams p = cut_kinds(a, kHeadGradBlocks);
+  const HeadParams p{a, cut_backward(a.T, a.q_heads, a.k_heads, a.D)};
   cudaError_t e = cudaSuccess;
-  const int blocks = p.q.blocks + p.k.blocks;
-  if (a.T > 0) e = a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, blocks, true, stream) : launch_s<__half>(p, blocks, true, stream);
+  if (a.T > 0) e = a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, true, stream) : launch_s<__half>(p, true, stream);
   // (no tokens: no partial sums, and the weight gradients are zeros)
   if (e != cudaSuccess || (a.d_q_weight == nullptr && a.d_k_weight == nullptr)) return e;
-  return launch_pdl<HeadParams>(head_weight_grad_kernel, dim3(2 * ((a.D + 31) / 32)), kSumThreads, 0, a.flags & MFR_FLAG_PDL, stream, p);
+  return launch_pdl<HeadParams>(head_weight_grad_kernel, dim3(2 * a.D / 8), kSumThreads, 0, a.flags & MFR_FLAG_PDL, stream, p);
 }
 
 }  // namespace mfr

@@ -1,5 +1,6 @@
 // C ABI of the operators around the finalize (moe_layer.h): argument validation (nothing is enqueued on
 // error), size queries and dispatch to the kernels.
+#include <algorithm>
 #include <climits>
 #include <cstdlib>
 
@@ -8,6 +9,8 @@
 
 namespace mfr {
 namespace {
+
+constexpr int kMaxHeads = 65536;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool any_dtype(int d) { return d == MFR_BF16 || d == MFR_FP16 || d == MFR_FP32; }
@@ -164,8 +167,8 @@ int check_head_norm(const mfr_head_norm_args* a, bool backward) {
   int st;
   if ((st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING | MFR_FLAG_POSITIONS_64)) != MFR_OK) return st;
   if (a->T < 0) return fail(MFR_ERR_INVALID_ARG, "T = %d < 0", a->T);
-  if (a->q_heads < 0 || a->k_heads < 0 || a->q_heads > 65536 || a->k_heads > 65536 || a->q_heads + a->k_heads == 0)
-    return fail(MFR_ERR_INVALID_ARG, "q_heads = %d, k_heads = %d: each in [0, 65536], not both 0", a->q_heads, a->k_heads);
+  if (a->q_heads < 0 || a->k_heads < 0 || a->q_heads > kMaxHeads || a->k_heads > kMaxHeads || a->q_heads + a->k_heads == 0)
+    return fail(MFR_ERR_INVALID_ARG, "q_heads = %d, k_heads = %d: each in [0, %d], not both 0", a->q_heads, a->k_heads, kMaxHeads);
   if (a->D < 16 || a->D > MFR_MAX_HEAD_DIM || a->D % 16 != 0)
     return fail(MFR_ERR_INVALID_ARG, "D = %d must be a multiple of 16 in [16, %d]", a->D, MFR_MAX_HEAD_DIM);
   if (a->style != MFR_ROTARY_HALF && a->style != MFR_ROTARY_INTERLEAVED)
@@ -254,9 +257,9 @@ int moe_head_norm_rotary(const mfr_head_norm_args* args, struct CUstream_st* str
 }
 
 int64_t moe_head_norm_rotary_workspace_bytes(int32_t T, int32_t q_heads, int32_t k_heads, int32_t D) {
-  if (T < 0 || q_heads < 0 || k_heads < 0 || D < 16 || D > MFR_MAX_HEAD_DIM || D % 16 != 0)
-    return fail(MFR_ERR_INVALID_ARG, "T, q_heads, k_heads >= 0 and D a multiple of 16 in [16, %d]", MFR_MAX_HEAD_DIM);
-  return static_cast<int64_t>(kHeadGradBlocks) * D * 4;  // a row of partial sums for each CTA
+  if (T < 0 || q_heads < 0 || k_heads < 0 || q_heads > kMaxHeads || k_heads > kMaxHeads || D < 16 || D > MFR_MAX_HEAD_DIM || D % 16 != 0)
+    return fail(MFR_ERR_INVALID_ARG, "T >= 0, q_heads and k_heads in [0, %d] and D a multiple of 16 in [16, %d]", kMaxHeads, MFR_MAX_HEAD_DIM);
+  return std::max(static_cast<int64_t>(head_grad_rows(T, q_heads, k_heads, D)) * 2 * D * 4, int64_t{16});
 }
 
 int moe_head_norm_rotary_backward(const mfr_head_norm_args* args, struct CUstream_st* stream) {

@@ -14,8 +14,8 @@ namespace mfr {
 constexpr int kRouteBlocks = 152;
 // Batches of at most this many tokens are routed and ordered by one CTA in one launch, with no workspace.
 constexpr int kRouteOneBlockTokens = 64;
-// CTAs of the head-norm gradient at most: two on each SM of a GB300, a row of partial weight gradients each.
-constexpr int kHeadGradBlocks = 152 * 2;
+// CTAs of the head-norm gradient at most (four times what a GB300 holds): a row of partial weight gradients each.
+constexpr int kHeadGradBlocks = 152 * 2 * 4;
 
 inline int route_blocks(int T) {
   if (T <= kRouteOneBlockTokens) return 1;
@@ -26,6 +26,8 @@ cudaError_t launch_route(const mfr_route_args& a, cudaStream_t stream);
 cudaError_t launch_route_backward(const mfr_route_backward_args& a, cudaStream_t stream);
 cudaError_t launch_dispatch(const mfr_dispatch_args& a, cudaStream_t stream);
 cudaError_t launch_routed_backward(const mfr_routed_backward_args& a, cudaStream_t stream);
+// Rows of partial weight gradients ([2][D] FP32 each) that the head-norm gradient leaves in its workspace.
+int head_grad_rows(int T, int q_heads, int k_heads, int D);
 cudaError_t launch_head_norm(const mfr_head_norm_args& a, cudaStream_t stream);
 cudaError_t launch_head_norm_backward(const mfr_head_norm_args& a, cudaStream_t stream);
 

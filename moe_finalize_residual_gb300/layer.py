@@ -458,8 +458,8 @@ def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     D is a multiple of 16 up to 512; tokens and heads may be strided (views of a packed projection), by multiples of
     8 elements.
 
-    ``positions`` is int32 or int64.  A negative position marks a padding token: it is not read, and its output
-    rows are left as they were (zeros in an allocated output).  ``q_out`` and ``k_out`` may be ``q`` and ``k``."""
+    ``positions`` is int32 or int64.  A negative position marks a padding token: its values do not matter, and its
+    output rows are left as they were (zeros in an allocated output).  ``q_out`` and ``k_out`` may be ``q`` and ``k``."""
     flags = _PDL if pdl else 0
     allocated = []
     index, act = q.get_device(), q.dtype
