@@ -29,17 +29,16 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 
 // How a launch cuts its work.  A warp's groups take `1 << gpt_log2` heads of a token at a time (a round: first the
-// queries', then the keys') and the warp as many tokens (a block) as that leaves groups for; `splits` warps share a
-// block's rounds.
+// queries', then the keys') and the warp as many tokens (a block) as that leaves groups for.  Forward, `splits` warps
+// share a block's rounds; backward, all `warps` share all blocks' rounds.
 struct HeadCut {
   int gpt_log2;
   int q_rounds, k_rounds;
   int splits;
   int cache_bytes;      // a warp's turn cache
   int64_t blocks;       // of tokens
-  int64_t team_blocks;  // backward: blocks that a team of `splits` warps takes one after the other
   int64_t warps;
-  int ctas;
+  int64_t ctas;
 };
 
 struct HeadParams {
@@ -233,18 +232,9 @@ struct Walk {
 template <int S, int N>
 constexpr int kSlotBytes = S * N * 32 * 16;
 
-#ifndef FS
-#define FS 4
-#endif
-#ifndef FT
-#define FT 64
-#endif
-#ifndef FC
-#define FC 16
-#endif
-constexpr int kFwdSlots = FS;
-constexpr int kFwdThreads = FT;
-constexpr int kFwdCtas = FC;  // CTAs an SM holds, by registers
+constexpr int kFwdSlots = 4;
+constexpr int kFwdThreads = 64;
+constexpr int kFwdCtas = 12;  // CTAs an SM holds, by registers
 
 // Forward: a warp takes its rounds of one block of tokens.  The CTAs are small and come and go, which evens out the
 // SMs' load; a warp requests its first vectors, its position, frequencies and weights all at once.
@@ -334,11 +324,9 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) head_norm_kernel(const 
 }
 
 
-#ifndef BS
-#define BS 3
-#endif
-constexpr int kBwdSlots = BS;
-constexpr int kBwdThreads = 256;
+constexpr int kBwdSlots = 3;
+constexpr int kBwdThreads = 192;
+constexpr int kBwdCtas = 2;  // CTAs an SM holds: 12 warps of 168 registers (16 of 128 spill: 63.3 against 60.1 us)
 constexpr int kBwdWarps = kBwdThreads / 32;
 
 // A kind's weight as each lane's pairs, in shared memory: [4][lanes of a head] vectors of (a, b) pairs.
@@ -425,9 +413,9 @@ __device__ __forceinline__ void write_sums(Pairs dw, const LaneMap& m, bool writ
 constexpr int kKeySumBytes = 4 * 32 * 16;
 __host__ __device__ constexpr int bwd_warp_bytes(int cache_bytes) { return kSlotBytes<kBwdSlots, 4> + cache_bytes + kKeySumBytes; }
 
-// Gradient: a warp takes its rounds of some neighbouring blocks, one after the other.
+// Gradient: the warps that the GPU holds share all rounds equally, each a contiguous range.
 template <typename A, int G, int STYLE>
-__global__ void __launch_bounds__(kBwdThreads, 2) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ WeightTable weights[2];
   const mfr_head_norm_args& a = p.a;
@@ -442,29 +430,34 @@ __global__ void __launch_bounds__(kBwdThreads, 2) head_norm_grad_kernel(const __
   float4* key_sums = reinterpret_cast<float4*>(mine + kSlotBytes<kBwdSlots, 4> + cut.cache_bytes) + lane;  // [4][32]
   const float4* turn = &cache[group >> gl][0][lane % G];
   const uint32_t slot = smem_addr(mine) + lane * 16;
-  // the warp's blocks [block, block_end) and its rounds of each
+  // the warp's rounds, an equal share of all blocks' rounds: from round r of a block on, `left` of them
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kBwdWarps + wid;
   const int all = cut.q_rounds + cut.k_rounds;
-  const int64_t team = cut.splits > 1 ? warp / cut.splits : warp;
-  const int split = static_cast<int>(warp - team * cut.splits);
-  const int r0 = all * split / cut.splits, r1 = all * (split + 1) / cut.splits;
-  int64_t block = team * cut.team_blocks;
-  const int64_t block_end = block + cut.team_blocks < cut.blocks ? block + cut.team_blocks : cut.blocks;
+  const int64_t total = cut.blocks * all;
+  int64_t left = 0, block = 0;
+  int r = 0;
+  if (warp < cut.warps) {
+    const int64_t first = total / cut.warps * warp + min(total % cut.warps, warp);
+    left = total / cut.warps + (warp < total % cut.warps ? 1 : 0);
+    block = first / all;
+    r = static_cast<int>(first - block * all);
+  }
   const int q_last = (a.q_heads - sub + (1 << gl) - 1) >> gl, k_last = cut.q_rounds + ((a.k_heads - sub + (1 << gl) - 1) >> gl);
   pdl_launch_dependents();
   pdl_wait();
   auto token = [&](int64_t b) { return b * tokens + (group >> gl); };
-  auto position = [&](int64_t b) { return b < block_end && token(b) < a.T ? position_of(a, token(b)) : -1; };
+  auto position = [&](int64_t b) { return token(b) < a.T ? position_of(a, token(b)) : -1; };
   Walk xs, gs, dst;
-  int64_t next_block = block;
-  int next_r = r0;
-  bool next_in = false;
+  int64_t next_block = block, next_left = left;
+  int next_r = r;
+  bool next_in = false, next_new = true;
   auto request = [&](int to_slot) {  // the next round, if there is one
-    if (next_block < block_end) {
-      if (next_r == r0) {
+    if (next_left > 0) {
+      if (next_new) {
         next_in = token(next_block) < a.T;
-        xs.start(a.q, a.k, cut, token(next_block), sub, m.off_a, r0);
-        gs.start(a.d_q_out, a.d_k_out, cut, token(next_block), sub, m.off_a, r0);
+        xs.start(a.q, a.k, cut, token(next_block), sub, m.off_a, next_r);
+        gs.start(a.d_q_out, a.d_k_out, cut, token(next_block), sub, m.off_a, next_r);
+        next_new = false;
       }
       const bool take = next_in && next_r < (next_r < cut.q_rounds ? q_last : k_last);
       const uint32_t to = slot + to_slot * (4 * 32 * 16);
@@ -474,9 +467,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) head_norm_grad_kernel(const __
       cp_async16_if(to + 3 * 32 * 16, gs.at + second, take);
       xs.next(cut, next_r);
       gs.next(cut, next_r);
-      if (++next_r == r1) {
-        next_r = r0;
+      --next_left;
+      if (++next_r == all) {
+        next_r = 0;
         ++next_block;
+        next_new = true;
       }
     }
     cp_async_commit();
@@ -495,13 +490,13 @@ __global__ void __launch_bounds__(kBwdThreads, 2) head_norm_grad_kernel(const __
   __syncthreads();
   const float inv_d = 1.0f / static_cast<float>(a.D);
   int here = 0;  // the slot of the current round
-  for (; block < block_end; ++block) {
+  for (; left > 0; ++block, r = 0) {
     const int64_t pos = pos_next;
     pos_next = position(block + 1);
     const bool write = lane_on && token(block) < a.T;
-    dst.start(a.q_out, a.k_out, cut, token(block), sub, m.off_a, r0);
+    dst.start(a.q_out, a.k_out, cut, token(block), sub, m.off_a, r);
     fill_turns<G>(a, pos, gl, lane, cache);
-    for (int r = r0; r < r1; ++r) {
+    for (; r < all && left > 0; ++r, --left) {
       const bool key = r >= cut.q_rounds;
       cp_async_wait_group<kBwdSlots - 2>();
       const uint32_t from = slot + here * (4 * 32 * 16);
@@ -610,7 +605,7 @@ cudaError_t launch_forward(const HeadParams& p, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<A, G, STYLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl<HeadParams>(head_norm_kernel<A, G, STYLE>, dim3(p.cut.ctas), kFwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
+  return launch_pdl<HeadParams>(head_norm_kernel<A, G, STYLE>, dim3(static_cast<unsigned>(p.cut.ctas)), kFwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
 }
 template <typename A, int G, int STYLE>
 cudaError_t launch_backward(const HeadParams& p, cudaStream_t stream) {
@@ -618,7 +613,7 @@ cudaError_t launch_backward(const HeadParams& p, cudaStream_t stream) {
   const int smem = kBwdWarps * bwd_warp_bytes(p.cut.cache_bytes);
   const cudaError_t e = cudaFuncSetAttribute(head_norm_grad_kernel<A, G, STYLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl<HeadParams>(head_norm_grad_kernel<A, G, STYLE>, dim3(p.cut.ctas), kBwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
+  return launch_pdl<HeadParams>(head_norm_grad_kernel<A, G, STYLE>, dim3(static_cast<unsigned>(p.cut.ctas)), kBwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
 }
 
 template <typename A, int STYLE>
@@ -644,9 +639,8 @@ cudaError_t launch_s(const HeadParams& p, bool backward, cudaStream_t stream) {
 
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Cuts the work: as many groups on a token as its larger kind has heads for; `warps` warps fill the GPU, and a block's
-// rounds are shared between so many warps that there are that many; `most`: warps at most (0: one for each block).
-HeadCut cut_heads(int T, int q_heads, int k_heads, int D, int cta_warps, int64_t warps, int64_t most, int entry_bytes) {
+// Cuts the work: as many groups on a token as its larger kind has heads for.  `entry_bytes`: of a turn cache.
+HeadCut cut_heads(int T, int q_heads, int k_heads, int D, int entry_bytes) {
   HeadCut c{};
   int G = 1;
   while (G < D / 16) G *= 2;
@@ -657,24 +651,36 @@ HeadCut cut_heads(int T, int q_heads, int k_heads, int D, int cta_warps, int64_t
   const int tokens = groups >> c.gpt_log2;
   c.cache_bytes = tokens * 4 * G * entry_bytes;
   c.blocks = ceil_div64(T, tokens);
-  c.splits = static_cast<int>(std::min<int64_t>(c.q_rounds + c.k_rounds, std::max<int64_t>(1, c.blocks > 0 ? warps / c.blocks : 1)));
-  c.team_blocks = most > 0 ? std::max<int64_t>(1, ceil_div64(c.blocks, most)) : 1;
-  c.warps = ceil_div64(c.blocks, c.team_blocks) * c.splits;
-  c.ctas = static_cast<int>(ceil_div64(c.warps, cta_warps));
   return c;
 }
 
+// Forward: a warp for each block, or as many as a block has rounds for when the blocks alone leave warps idle.
+HeadCut cut_forward(int T, int q_heads, int k_heads, int D) {
+  HeadCut c = cut_heads(T, q_heads, k_heads, D, 64);
+  const int64_t fill = 152 * kFwdCtas * (kFwdThreads / 32);
+  c.splits = static_cast<int>(std::min<int64_t>(c.q_rounds + c.k_rounds, std::max<int64_t>(1, fill / c.blocks)));
+  c.warps = c.blocks * c.splits;
+  c.ctas = ceil_div64(c.warps, kFwdThreads / 32);
+  return c;
+}
+
+// Backward: the warps that the GPU holds, or one for each round.
 HeadCut cut_backward(int T, int q_heads, int k_heads, int D) {
-  return cut_heads(T, q_heads, k_heads, D, kBwdWarps, 152 * 2 * kBwdWarps, kHeadGradBlocks * kBwdWarps, 16);
+  HeadCut c = cut_heads(T, q_heads, k_heads, D, 16);
+  c.warps = std::min<int64_t>(static_cast<int64_t>(kHeadGradBlocks) * kBwdWarps, c.blocks * (c.q_rounds + c.k_rounds));
+  c.ctas = ceil_div64(c.warps, kBwdWarps);
+  return c;
 }
 
 }  // namespace
 
-int head_grad_rows(int T, int q_heads, int k_heads, int D) { return cut_backward(T, q_heads, k_heads, D).ctas; }
+int head_grad_rows(int T, int q_heads, int k_heads, int D) {
+  return static_cast<int>(cut_backward(T, q_heads, k_heads, D).ctas);
+}
 
 cudaError_t launch_head_norm(const mfr_head_norm_args& a, cudaStream_t stream) {
-  constexpr int kWarps = kFwdThreads / 32;
-  const HeadParams p{a, cut_heads(a.T, a.q_heads, a.k_heads, a.D, kWarps, 152 * kFwdCtas * kWarps, 0, 64)};
+  const HeadParams p{a, cut_forward(a.T, a.q_heads, a.k_heads, a.D)};
+  if (p.cut.ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   return a.act_dtype == MFR_BF16 ? launch_s<__nv_bfloat16>(p, false, stream) : launch_s<__half>(p, false, stream);
 }
 

@@ -14,8 +14,8 @@ namespace mfr {
 constexpr int kRouteBlocks = 152;
 // Batches of at most this many tokens are routed and ordered by one CTA in one launch, with no workspace.
 constexpr int kRouteOneBlockTokens = 64;
-// CTAs of the head-norm gradient at most (four times what a GB300 holds): a row of partial weight gradients each.
-constexpr int kHeadGradBlocks = 152 * 2 * 4;
+// CTAs of the head-norm gradient at most: two on each SM of a GB300, a row of partial weight gradients each.
+constexpr int kHeadGradBlocks = 152 * 2;
 
 inline int route_blocks(int T) {
   if (T <= kRouteOneBlockTokens) return 1;
