@@ -12,9 +12,9 @@
 //
 // The expert order is a stable counting sort.  A CTA takes a contiguous chunk of tokens and marks each
 // route in a bitmap [expert][token of the segment]: a route's rank among its expert's routes is the number
-// of marks below its own, so the marks may be set in any order (atomicOr) with the same result.  The chunks'
-// counts meet in a second kernel (order_kernel), which adds those of the chunks before its own; a batch of
-// one chunk does both in one launch.
+// of marks below its own, so the marks may be set in any order (atomicOr) with the same result.  Small batches
+// run as one cluster whose CTAs read each other's counts from shared memory, in one launch; larger ones leave
+// the chunks' counts in the workspace, and a second kernel (order_kernel) adds those of the chunks before its own.
 #include "layer_launch.h"
 
 namespace mfr {
@@ -42,6 +42,8 @@ struct RouteParams {
   mfr_route_args a;
   int group_size;   // experts of a group
   int width_log2;   // a group is 2^width_log2 whole lanes, aligned; -1: it is not
+  int clustered;    // the whole batch runs as one cluster
+  int chunk, extra; // chunk b holds `chunk` tokens, and one more for b < extra
 };
 
 // A float as an unsigned integer of the same order (no NaN, no -0).
@@ -128,6 +130,31 @@ __device__ __forceinline__ void load_logits(const L* row, int e0, int E, float x
         v = static_cast<float>(p[j]);
     }
     x[j] = clean(v);
+  }
+}
+
+// NV consecutive floats of a lane in shared memory, in vectors (a lane's share is 4 NV bytes, aligned to that).
+template <int NV>
+__device__ __forceinline__ void store_lane(float* base, int lane, const float (&v)[NV]) {
+  if constexpr (NV >= 4) {
+#pragma unroll
+    for (int j = 0; j < NV; j += 4) reinterpret_cast<float4*>(base + lane * NV)[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) base[lane * NV + j] = v[j];
+  }
+}
+template <int NV>
+__device__ __forceinline__ void load_lane(const float* base, int lane, float (&v)[NV]) {
+  if constexpr (NV >= 4) {
+#pragma unroll
+    for (int j = 0; j < NV; j += 4) {
+      const float4 f = reinterpret_cast<const float4*>(base + lane * NV)[j / 4];
+      v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = base[lane * NV + j];
   }
 }
 
@@ -344,16 +371,17 @@ __device__ __noinline__ void decide_candidates(const mfr_route_args& a, const L*
 }
 
 // Chooses and weighs the experts of one token whose logits are x.  Each lane gets up to two of them: the
-// expert id[i] at place[i] of the token's list, or id -1.  `bias`: the experts' biases in shared memory.
-template <typename L, int NV>
+// expert id[i] at place[i] of the token's list, or id -1; `taken` in all.  `bias`: the experts' biases in shared memory.  GENERAL:
+// there are biases or groups; without them the logits decide and no score is needed for the choice.
+template <typename L, int NV, bool GENERAL>
 __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, float (&x)[NV], int lane, const float* bias,
-                                            const Scratch& sc, int (&id)[2], int (&place)[2]) {
+                                            const Scratch& sc, int (&id)[2], int (&place)[2], int& taken) {
   const mfr_route_args& a = p.a;
   const L* row = static_cast<const L*>(a.logits) + t * a.logits_stride;
   const int e0 = lane * NV;
   const bool softmax = a.score == MFR_SCORE_SOFTMAX;
-  const bool top2 = a.num_groups > 1 && a.group_score == MFR_GROUP_TOP2;
-  const bool biased = a.bias != nullptr;
+  const bool top2 = GENERAL && a.num_groups > 1 && a.group_score == MFR_GROUP_TOP2;
+  const bool biased = GENERAL && a.bias != nullptr;
   float (&c)[NV] = x;  // the logits become the choice scores
 
   float top = -kInf, inv = 0.0f;  // the largest logit, and 1 / the softmax's sum
@@ -388,12 +416,14 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
     }
   }
   if (biased) {
+    float b[NV];
+    load_lane<NV>(bias, lane, b);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) c[j] = x[j] > -kInf ? clean(s[j] + bias[e0 + j]) : -kInf;
+    for (int j = 0; j < NV; ++j) c[j] = x[j] > -kInf ? clean(s[j] + b[j]) : -kInf;
   }
 
   bool close = false;  // a decision lies within the error bound and too many experts with it: all in FP64
-  if (a.num_groups > 1) {
+  if (GENERAL && a.num_groups > 1) {
     const bool sums = top2 && !biased;  // groups compare sums of scores, experts compare logits
     float mine = -kInf, second = -kInf; // lane g: group g's score, and its second best value
     if (p.width_log2 >= 0) {
@@ -414,8 +444,10 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       second = __shfl_sync(kAll, b2, from);
       if (lane >= a.num_groups) mine = -kInf;
     } else {
+      float v[NV];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) sc.scores[e0 + j] = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
+      for (int j = 0; j < NV; ++j) v[j] = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
+      store_lane<NV>(sc.scores, lane, v);
       __syncwarp();
       if (lane < a.num_groups) {
         float b1 = -kInf;
@@ -443,8 +475,10 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       const float tol = (top2 ? 4.0f : 2.0f) * err + 2.4e-7f * (fabsf(worst) + fabsf(best_out));
       if (best_out > -kInf && !(worst - best_out > tol)) {
         if (p.width_log2 >= 0) {
+          float v[NV];
 #pragma unroll
-          for (int j = 0; j < NV; ++j) sc.scores[e0 + j] = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
+          for (int j = 0; j < NV; ++j) v[j] = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
+          store_lane<NV>(sc.scores, lane, v);
           __syncwarp();
         }
         kept = decide_groups(p, row, lane, sc, top, mine, second, in, worst, best_out, tol);
@@ -472,38 +506,71 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
   id[0] = id[1] = -1;
   place[0] = lane;
   place[1] = lane + 32;
-  int n = kList + 1;  // candidates
-  if (!close && a.K < 32) {
-    // The K + 1 best of the lanes' best bound the K + 1 best experts from below: every expert from there on is a
-    // candidate (about 10 of 256 for K = 8), and the candidates are ranked by counting.
+  int n = kList + 1;                // candidates
+  float z[2] = {-kInf, -kInf};      // their scores: without a bias, their logits
+  bool reload = biased;
+  if (!close && a.K < kList) {
+    // Every expert from some score on is a candidate, and the candidates are ranked by counting.  The K + 1 best of
+    // the lanes' best bound the K + 1 best experts from below (about 10 candidates of 256 for K = 8).
     float best = c[0];
 #pragma unroll
     for (int j = 1; j < NV; ++j) best = fmaxf(best, c[j]);
     uint32_t key = ordered(best);
     const uint32_t first = __reduce_max_sync(kAll, key);
     uint32_t tau = first;
+    if (a.K < 32) {
 #pragma unroll 4
-    for (int k = 0; k < a.K; ++k) {
-      if (key == tau) key = 0;
-      tau = __reduce_max_sync(kAll, key);
+      for (int k = 0; k < a.K; ++k) {
+        if (key == tau) key = 0;
+        tau = __reduce_max_sync(kAll, key);
+      }
+    } else {
+      tau = 0;
     }
     const float most = unordered(first);
     // fewer lanes than that have any: all experts that can be taken are candidates
-    const float least = tau > ordered(-kInf) ? unordered(tau) : -3.402823466e38f;
+    float least = tau > ordered(-kInf) ? unordered(tau) : -3.402823466e38f;
     unsigned mask = 0;
+    auto select = [&]() {
+      mask = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) mask |= c[j] >= least ? 1u << j : 0u;
-    int before = __popc(mask);
+      for (int j = 0; j < NV; ++j) mask |= c[j] >= least ? 1u << j : 0u;
+      return __popc(mask);
+    };
+    // the candidates up to and with the lane's own
+    auto scan = [&](int own) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kAll, before, o);
-      if (lane >= o) before += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, own, o);
+        if (lane >= o) own += v;
+      }
+      return own;
+    };
+    int before = select();
+    n = __reduce_add_sync(kAll, before);
+    before = scan(before);
+    if (n > kList) {
+      // The lanes say little when there are few of them: close in on a score that leaves a list's worth.
+      uint32_t lo = ordered(least), hi = first;  // too many from lo on
+      least = most;
+      n = __reduce_add_sync(kAll, select());
+      while (n <= a.K && hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        least = unordered(mid);
+        n = __reduce_add_sync(kAll, select());
+        if (n > kList) {
+          lo = mid;
+          n = 0;
+        } else if (n <= a.K) {
+          hi = mid;
+        }
+      }
+      before = scan(select());
+      if (n <= a.K) n = kList + 1;  // more equal scores than the list holds
     }
-    n = __shfl_sync(kAll, before, 31);
     if (n <= kList) {
       // by expert index, so that among equal scores the earlier candidate is the lower expert
-#pragma unroll
-      for (int j = 0; j < NV; ++j) sc.scores[e0 + j] = c[j];
+      store_lane<NV>(sc.scores, lane, c);
       int i = before - __popc(mask);
       while (mask) {
         const int j = __ffs(mask) - 1;
@@ -515,7 +582,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       if (lane < 4 && n + lane < kList) sc.value[n + lane] = -kInf;  // the list in fours
       __syncwarp();
       int rank[2] = {0, 0};
-      float v[2];
+      float (&v)[2] = z;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int me = lane + 32 * h;
@@ -540,7 +607,9 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
 #pragma unroll
         for (int h = 0; h < 2; ++h)  // (an infinite score is near to every other)
           if (lane + 32 * h < n && rank[h] < a.K && rank[h] + 1 < n) tie |= !(v[h] - sc.scores[rank[h] + 1] > near);
-        if (__any_sync(kAll, tie)) decide_candidates(a, row, lane, sc, top, n, rank[0], rank[1]);
+        if (__any_sync(kAll, tie)) {
+            decide_candidates(a, row, lane, sc, top, n, rank[0], rank[1]);
+        }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -553,7 +622,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
     }
   }
   if (!close && n > kList) {
-    // Many equal scores, or K of 32 and more: one expert after the other.
+    // Many equal scores, or K of the list's length: one expert after the other.
     float last = kInf;
     const int rounds = biased ? a.K + 1 : a.K;  // one more, to see how near the first one left out is
     for (int k = 0; k < rounds && !close; ++k) {
@@ -568,7 +637,9 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       const float v = warp_max(best);
       if (!(v > -kInf)) break;
       if (biased) {
-        if (k > 0 && !(last - v > 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(v)))) close = true;
+        if (k > 0 && !(last - v > 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(v)))) {
+            close = true;
+        }
         if (k == a.K) break;
         last = v;
       }
@@ -582,18 +653,22 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       if (lane == (k & 31)) (k < 32 ? id[0] : id[1]) = chosen;
     }
     n = kList;  // both places of a lane may be taken
+    reload = true;
   }
-  if (close) {
+  if (GENERAL && close) {
     slow_choice<L, NV>(a, row, lane, id[0], id[1]);
     n = kList;
+    reload = true;
   }
 
   // The weights, from the chosen logits, in FP32.  Halves: experts in a lane's second place are rare.
   const bool two = n > 32;
-  float w[2] = {0.0f, 0.0f}, z[2] = {-kInf, -kInf};
-  if (id[0] >= 0) z[0] = clean(static_cast<float>(row[id[0]]));
-  if (two && id[1] >= 0) z[1] = clean(static_cast<float>(row[id[1]]));
-  const int taken = __popc(__ballot_sync(kAll, id[0] >= 0)) + (two ? __popc(__ballot_sync(kAll, id[1] >= 0)) : 0);
+  float w[2] = {0.0f, 0.0f};
+  if (reload && id[0] >= 0) z[0] = clean(static_cast<float>(row[id[0]]));
+  if (reload && two && id[1] >= 0) z[1] = clean(static_cast<float>(row[id[1]]));
+  if (id[0] < 0) z[0] = -kInf;
+  if (id[1] < 0) z[1] = -kInf;
+  taken = __popc(__ballot_sync(kAll, id[0] >= 0)) + (two ? __popc(__ballot_sync(kAll, id[1] >= 0)) : 0);
   if (a.renormalize) {
     // softmax: over the chosen logits.  sigmoid: over the logarithms of the chosen scores, so that small scores
     // keep their ratios; directly while FP32 holds them in full.
@@ -611,7 +686,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
     if (id[0] >= 0) w[0] = weigh(z[0]);
     if (two && id[1] >= 0) w[1] = weigh(z[1]);
     const float sum = warp_sum(w[0] + w[1]);
-    const float over = sum > 0.0f ? __fdiv_rn(a.scale, sum) : 0.0f;
+    const float over = sum > 0.0f ? a.scale * fast_rcp(sum) : 0.0f;
     w[0] *= over;
     w[1] *= over;
   } else {
@@ -641,16 +716,19 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
 // The expert order
 // ---------------------------------------------------------------------------------------------------
 
-// Finishes the order of one chunk: `before[e]` routes of expert e lie in earlier chunks, `total[e]` in all;
-// perm_idx holds each route's rank within the chunk.  off: E + 1 ints of shared memory.
-__device__ __forceinline__ void finish_order(const mfr_route_args& a, int64_t r0, int64_t r1, const int* before,
-                                             const int* total, int* off, int* warp_sums) {
+// Finishes the order of chunk `b` of `chunks`, which holds `routes` routes from r0 on: `before[e]` routes of expert e lie
+// in earlier chunks, `total[e]` in all; route(i, rank) gives route i's expert (-1: none) and its rank within the chunk.
+// off: E + 1 ints, warp_sums: 32 ints of shared memory.
+template <typename F>
+__device__ __forceinline__ void finish_order(const mfr_route_args& a, int b, int chunks, int64_t r0, int64_t routes, const int* before,
+                                             const int* total, int* off, int* warp_sums, F route) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
   // exclusive sum over the experts of their padded rows: 32 experts a warp, then the warps' sums
-  const int chunks = (a.E + 31) / 32;  // at most 32
-  for (int i = warp; i < chunks; i += nwarps) {
+  const int parts = (a.E + 31) / 32;  // at most 32
+  for (int i = warp; i < parts; i += nwarps) {
     const int e = i * 32 + lane;
-    const int rows = e < a.E ? static_cast<int>((static_cast<int64_t>(total[e]) + a.row_align - 1) / a.row_align * a.row_align) : 0;
+    int rows = e < a.E ? total[e] : 0;
+    if (a.row_align > 1) rows = static_cast<int>((static_cast<unsigned>(rows) + a.row_align - 1) / a.row_align * a.row_align);
     int sum = rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -662,186 +740,285 @@ __device__ __forceinline__ void finish_order(const mfr_route_args& a, int64_t r0
   }
   __syncthreads();
   if (warp == 0) {
-    const int v = lane < chunks ? warp_sums[lane] : 0;
+    const int v = lane < parts ? warp_sums[lane] : 0;
     int sum = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(kAll, sum, o);
       if (lane >= o) sum += u;
     }
+    __syncwarp();
     warp_sums[lane] = sum - v;
     if (lane == 31) off[a.E] = sum;
   }
   __syncthreads();
-  for (int e = tid; e < a.E; e += blockDim.x) off[e] += warp_sums[e >> 5];
-  __syncthreads();
-  for (int64_t r = r0 + tid; r < r1; r += blockDim.x) {
-    const int e = a.expert_ids[r];
+  auto start = [&](int e) { return e < a.E ? off[e] + warp_sums[e >> 5] : off[e]; };
+  for (int64_t i = tid; i < routes; i += blockDim.x) {
+    int rank = 0;
+    const int e = route(i, rank);
     int row = -1;
     if (e >= 0) {
-      row = off[e] + before[e] + a.perm_idx[r];
-      a.row_route[row] = static_cast<int>(r);
+      row = start(e) + before[e] + rank;
+      a.row_route[row] = static_cast<int>(r0 + i);
     }
-    a.perm_idx[r] = row;
+    a.perm_idx[r0 + i] = row;
   }
-  if (blockIdx.x == 0) {
-    for (int e = tid; e < a.E; e += blockDim.x) {
-      a.expert_offsets[e] = off[e];
-      a.expert_counts[e] = total[e];
+  if (b == 0) {
+    for (int e = tid; e <= a.E; e += blockDim.x) {
+      a.expert_offsets[e] = start(e);
+      if (e < a.E) a.expert_counts[e] = total[e];
     }
-    if (tid == 0) a.expert_offsets[a.E] = off[a.E];
   }
   // rows of no route: the padding behind each expert's routes, and everything behind the last expert
   if (a.row_align > 1)
-    for (int e = blockIdx.x * nwarps + warp; e < a.E; e += gridDim.x * nwarps)
-      for (int row = off[e] + total[e] + lane; row < off[e + 1]; row += 32) a.row_route[row] = -1;
-  for (int64_t row = off[a.E] + static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; row < a.num_rows;
-       row += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    for (int e = b * nwarps + warp; e < a.E; e += chunks * nwarps)
+      for (int row = start(e) + total[e] + lane; row < start(e + 1); row += 32) a.row_route[row] = -1;
+  for (int64_t row = off[a.E] + static_cast<int64_t>(b) * blockDim.x + tid; row < a.num_rows; row += static_cast<int64_t>(chunks) * blockDim.x)
     a.row_route[row] = -1;
 }
 
-// The chunk of tokens of one CTA.
-__device__ __forceinline__ void chunk_of(int T, int64_t& t0, int64_t& t1) {
-  t0 = static_cast<int64_t>(T) * blockIdx.x / gridDim.x;
-  t1 = static_cast<int64_t>(T) * (blockIdx.x + 1) / gridDim.x;
+// The tokens [t0, t1) of chunk b.
+__device__ __forceinline__ void chunk_of(const RouteParams& p, int b, int64_t& t0, int64_t& t1) {
+  t0 = static_cast<int64_t>(p.chunk) * b + min(b, p.extra);
+  t1 = t0 + p.chunk + (b < p.extra ? 1 : 0);
 }
 
-template <int NV>
-constexpr int route_threads() { return NV <= 8 ? 1024 : 512; }
-
-// Shared memory: each warp's scratch, the biases, and for the order the bitmap, the running counts, the offsets and the
-// scan's warp sums.
-template <int NV>
-int route_smem(int E, bool order) {
-  const int scratch = route_threads<NV>() / 32 * kScratchBytes<NV> + 32 * NV * 4;
-  return order ? scratch + E * kSegWords * 4 + E * 4 + (E + 1) * 4 + 32 * 4 : scratch;
+// Cluster barrier with release and acquire of shared memory, and a load from a peer's shared memory.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ int load_peer(const int* local, uint32_t rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
-template <typename L, int NV>
-__global__ void __launch_bounds__(route_threads<NV>(), 1) route_kernel(const __grid_constant__ RouteParams p) {
+template <int NV, bool GENERAL>
+constexpr int kRouteThreads = NV <= 8 ? 1024 : 512;
+
+// Shared memory: each warp's scratch, the biases, and for the order the bitmap, the counts (of the chunk, of the chunks
+// before it, of all), the offsets, the scan's warp sums and a segment's experts.
+constexpr uint16_t kNoExpert = 0xffff;
+struct OrderSmem {
+  uint32_t* bits;   // [E][kSegWords]
+  int *count, *before, *total, *off, *warp_sums;
+  uint16_t* chosen; // [kSegTokens][K]
+};
+__host__ __device__ inline int order_smem_bytes(int E, int K) {
+  return E * kSegWords * 4 + 3 * E * 4 + (E + 1) * 4 + 32 * 4 + kSegTokens * K * 2;
+}
+__device__ __forceinline__ OrderSmem order_smem(uint8_t* base, int E) {
+  OrderSmem o;
+  o.bits = reinterpret_cast<uint32_t*>(base);
+  o.count = reinterpret_cast<int*>(o.bits + E * kSegWords);
+  o.before = o.count + E;
+  o.total = o.before + E;
+  o.warp_sums = o.total + E;
+  o.off = o.warp_sums + 32;
+  o.chosen = reinterpret_cast<uint16_t*>(o.off + E + 1);
+  return o;
+}
+
+template <typename L, int NV, bool GENERAL>
+__global__ void __launch_bounds__(kRouteThreads<NV, GENERAL>, 1) route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const mfr_route_args& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, nwarps = blockDim.x >> 5;
+  const int warp = __shfl_sync(kAll, tid >> 5, 0);  // so that the compiler knows it to be the same for the warp
   const Scratch scratch = scratch_of<NV>(smem + warp * kScratchBytes<NV>);
   float* bias = reinterpret_cast<float*>(smem + nwarps * kScratchBytes<NV>);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(bias + 32 * NV);
-  int* count = reinterpret_cast<int*>(bits + a.E * kSegWords);
-  int* off = count + a.E;
-  int* warp_sums = off + a.E + 1;
+  const OrderSmem o = order_smem(reinterpret_cast<uint8_t*>(bias + (GENERAL ? 32 * NV : 0)), a.E);
   const bool order = a.expert_offsets != nullptr;
   int64_t t0, t1;
-  chunk_of(a.T, t0, t1);
+  chunk_of(p, blockIdx.x, t0, t1);
   if (order) {
-    for (int i = tid; i < a.E * kSegWords; i += blockDim.x) bits[i] = 0;
-    for (int i = tid; i < a.E; i += blockDim.x) count[i] = 0;
+    for (int i = tid; i < a.E * kSegWords; i += blockDim.x) o.bits[i] = 0;
+    for (int i = tid; i < a.E; i += blockDim.x) o.count[i] = 0;
   }
   pdl_launch_dependents();
   pdl_wait();
-  for (int e = tid; e < 32 * NV; e += blockDim.x) bias[e] = a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
-  __syncthreads();
+  if (GENERAL)
+    for (int e = tid; e < 32 * NV; e += blockDim.x) bias[e] = a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
+  if (GENERAL || order) __syncthreads();
+  // the rank of route i (token i / K of the segment) of expert e among the segment's routes of that expert
+  auto rank_of = [&](int i, int e) {
+    const int token = i / a.K;
+    const uint32_t* bits = o.bits + e * kSegWords;
+    int rank = __popc(bits[token >> 5] & ((1u << (token & 31)) - 1));
+    for (int w = 0; w < (token >> 5); ++w) rank += __popc(bits[w]);
+    return rank;
+  };
   for (int64_t seg = t0; seg < t1; seg += kSegTokens) {
     const int64_t end = seg + kSegTokens < t1 ? seg + kSegTokens : t1;
     for (int64_t t = seg + warp; t < end; t += nwarps) {
-      int id[2], place[2];
+      int id[2], place[2], taken;
       float x[NV];
       load_logits<L, NV>(static_cast<const L*>(a.logits) + t * a.logits_stride, lane * NV, a.E, x);
-      route_token<L, NV>(p, t, x, lane, bias, scratch, id, place);
+      route_token<L, NV, GENERAL>(p, t, x, lane, bias, scratch, id, place, taken);
       if (order) {
         const int i = static_cast<int>(t - seg);
-        if (id[0] >= 0) atomicOr(&bits[id[0] * kSegWords + (i >> 5)], 1u << (i & 31));
-        if (id[1] >= 0) atomicOr(&bits[id[1] * kSegWords + (i >> 5)], 1u << (i & 31));
+        uint16_t* mine = o.chosen + i * a.K;
+        for (int k = taken + lane; k < a.K; k += 32) mine[k] = kNoExpert;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (id[h] >= 0) {
+            mine[place[h]] = static_cast<uint16_t>(id[h]);
+            atomicOr(&o.bits[id[h] * kSegWords + (i >> 5)], 1u << (i & 31));
+          }
+        }
       }
     }
     if (!order) continue;
     __syncthreads();
-    const int routes = static_cast<int>(end - seg) * a.K;
-    for (int r = tid; r < routes; r += blockDim.x) {
-      const int e = a.expert_ids[seg * a.K + r];
-      int rank = -1;
-      if (e >= 0) {
-        const int i = r / a.K;
-        rank = count[e] + __popc(bits[e * kSegWords + (i >> 5)] & ((1u << (i & 31)) - 1));
-        for (int w = 0; w < (i >> 5); ++w) rank += __popc(bits[e * kSegWords + w]);
+    if (!p.clustered) {
+      const int routes = static_cast<int>(end - seg) * a.K;
+      for (int i = tid; i < routes; i += blockDim.x) {
+        const int e = o.chosen[i];
+        a.perm_idx[seg * a.K + i] = e == kNoExpert ? -1 : o.count[e] + rank_of(i, e);
       }
-      a.perm_idx[seg * a.K + r] = rank;
+      __syncthreads();
     }
-    __syncthreads();
     for (int e = tid; e < a.E; e += blockDim.x) {
       int n = 0;
 #pragma unroll
       for (int w = 0; w < kSegWords; ++w) {
-        n += __popc(bits[e * kSegWords + w]);
-        bits[e * kSegWords + w] = 0;
+        n += __popc(o.bits[e * kSegWords + w]);
+        if (!p.clustered) o.bits[e * kSegWords + w] = 0;
       }
-      count[e] += n;
+      o.count[e] += n;
     }
     __syncthreads();
   }
   if (!order) return;
-  if (gridDim.x > 1) {
-    for (int e = tid; e < a.E; e += blockDim.x) static_cast<int*>(a.workspace)[blockIdx.x * a.E + e] = count[e];
-  } else {
-    // one chunk: nothing lies before it (the bitmap is all zeros again and serves as `before`)
-    finish_order(a, t0 * a.K, t1 * a.K, reinterpret_cast<const int*>(bits), count, off, warp_sums);
+  if (!p.clustered) {
+    for (int e = tid; e < a.E; e += blockDim.x) static_cast<int*>(a.workspace)[static_cast<int64_t>(blockIdx.x) * a.E + e] = o.count[e];
+    return;
   }
+  // one cluster holds the whole batch, a segment a CTA
+  const int chunks = gridDim.x, b = blockIdx.x;
+  if (chunks > 1) cluster_barrier();
+  for (int e = tid; e < a.E; e += blockDim.x) {
+    int before = 0, total = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int v = chunks > 1 ? load_peer(o.count + e, c) : o.count[e];
+      total += v;
+      if (c < b) before += v;
+    }
+    o.before[e] = before;
+    o.total[e] = total;
+  }
+  if (chunks > 1) {
+    cluster_barrier();  // (no CTA leaves while a peer reads its counts)
+  } else {
+    __syncthreads();
+  }
+  finish_order(a, b, chunks, t0 * a.K, (t1 - t0) * a.K, o.before, o.total, o.off, o.warp_sums, [&](int64_t i, int& rank) {
+    const int e = o.chosen[i];
+    if (e == kNoExpert) return -1;
+    rank = rank_of(static_cast<int>(i), e);
+    return e;
+  });
 }
 
 constexpr int kOrderThreads = 1024;
+constexpr int kOrderParts = 4096;  // partial counts of an expert, times the experts, at most
 
 // Adds the chunks' counts and finishes the order of chunk blockIdx.x.
 __global__ void __launch_bounds__(kOrderThreads, 1) order_kernel(const __grid_constant__ RouteParams p) {
-  const mfr_route_args& a = p.a;
   __shared__ int before[MFR_MAX_EXPERTS], total[MFR_MAX_EXPERTS], off[MFR_MAX_EXPERTS + 1], warp_sums[32];
+  __shared__ int4 part_before[kOrderParts / 4], part_total[kOrderParts / 4];
+  const mfr_route_args& a = p.a;
+  const int tid = threadIdx.x, b = blockIdx.x, chunks = gridDim.x;
+  int64_t t0, t1;
+  chunk_of(p, b, t0, t1);
+  const int64_t r0 = t0 * a.K, routes = (t1 - t0) * a.K;
+  // columns of the count matrix, four at a time when its rows allow; the threads split the rows too
+  const int wide = a.E % 4 == 0 ? 4 : 1, cols = a.E / wide;
+  const int parts = min(kOrderThreads / cols, 32), part = tid / cols, c = tid - part * cols;
+  const int* column = static_cast<const int*>(a.workspace) + c * wide;
   pdl_launch_dependents();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) before[e] = total[e] = 0;
-  __syncthreads();
   pdl_wait();
-  // columns of the count matrix: the threads split its rows too, and meet by integer adds (any order)
-  const int* ws = static_cast<const int*>(a.workspace);
-  const int parts = kOrderThreads / a.E;  // E <= 1024
-  const int part = threadIdx.x / a.E, e = threadIdx.x % a.E;
+  // this thread's first route, on its way while the counts are added
+  const int e_first = tid < routes ? a.expert_ids[r0 + tid] : -1, rank_first = tid < routes ? a.perm_idx[r0 + tid] : 0;
   if (part < parts) {
-    int b = 0, n = 0;
-#pragma unroll 8
-    for (int i = part; i < static_cast<int>(gridDim.x); i += parts) {
-      const int v = ws[i * a.E + e];
-      n += v;
-      if (i < static_cast<int>(blockIdx.x)) b += v;
+    if (wide == 4) {
+      int4 n = make_int4(0, 0, 0, 0), m = n;
+#pragma unroll 10
+      for (int i = part; i < chunks; i += parts) {
+        const int4 v = *reinterpret_cast<const int4*>(column + i * a.E);
+        n.x += v.x, n.y += v.y, n.z += v.z, n.w += v.w;
+        if (i < b) m.x += v.x, m.y += v.y, m.z += v.z, m.w += v.w;
+      }
+      part_total[part * cols + c] = n;
+      part_before[part * cols + c] = m;
+    } else {
+      int n = 0, m = 0;
+#pragma unroll 10
+      for (int i = part; i < chunks; i += parts) {
+        const int v = column[i * a.E];
+        n += v;
+        if (i < b) m += v;
+      }
+      reinterpret_cast<int*>(part_total)[part * a.E + c] = n;
+      reinterpret_cast<int*>(part_before)[part * a.E + c] = m;
     }
-    atomicAdd(&before[e], b);
-    atomicAdd(&total[e], n);
   }
   __syncthreads();
-  int64_t t0, t1;
-  chunk_of(a.T, t0, t1);
-  finish_order(a, t0 * a.K, t1 * a.K, before, total, off, warp_sums);
+  for (int e = tid; e < a.E; e += kOrderThreads) {
+    int n = 0, m = 0;
+    for (int i = 0; i < parts; ++i) {
+      n += reinterpret_cast<const int*>(part_total)[i * a.E + e];
+      m += reinterpret_cast<const int*>(part_before)[i * a.E + e];
+    }
+    total[e] = n;
+    before[e] = m;
+  }
+  __syncthreads();
+  finish_order(a, b, chunks, r0, routes, before, total, off, warp_sums, [&](int64_t i, int& rank) {
+    if (i == tid) {
+      rank = rank_first;
+      return e_first;
+    }
+    rank = a.perm_idx[r0 + i];
+    return a.expert_ids[r0 + i];
+  });
+}
+
+template <typename L, int NV, bool GENERAL>
+cudaError_t launch_route_nv(const mfr_route_args& a, cudaStream_t stream) {
+  const bool order = a.expert_offsets != nullptr, pdl = a.flags & MFR_FLAG_PDL;
+  constexpr int kThreads = kRouteThreads<NV, GENERAL>;
+  const int fixed = kThreads / 32 * kScratchBytes<NV> + (GENERAL ? 32 * NV * 4 : 0);
+  const int smem = fixed + (order ? order_smem_bytes(a.E, a.K) : 0);
+  auto kern = route_kernel<L, NV, GENERAL>;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + order_smem_bytes(NV * 32, MFR_MAX_TOP_K));
+  if (e != cudaSuccess) return e;
+  const int chunks = route_chunks(a.T, a.E, order);
+  RouteParams p{a, a.E / a.num_groups, -1, order && chunks <= kRouteCluster, a.T / chunks, a.T % chunks};
+  for (int w = 0; w <= 5; ++w)
+    if (p.group_size == NV << w) p.width_log2 = w;
+  e = launch_pdl<RouteParams>(kern, dim3(chunks), kThreads, smem, pdl, stream, p, p.clustered ? chunks : 1);
+  if (e != cudaSuccess || !order || p.clustered) return e;
+  return launch_pdl<RouteParams>(order_kernel, dim3(chunks), kOrderThreads, 0, pdl, stream, p);
 }
 
 template <typename L, int NV>
-cudaError_t launch_route_nv(const mfr_route_args& a, cudaStream_t stream) {
-  const bool order = a.expert_offsets != nullptr, pdl = a.flags & MFR_FLAG_PDL;
-  const int smem = route_smem<NV>(a.E, order);
-  auto kern = route_kernel<L, NV>;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, route_smem<NV>(NV * 32, true));
-  if (e != cudaSuccess) return e;
-  const int blocks = route_blocks(a.T);
-  RouteParams p{a, a.E / a.num_groups, -1};
-  for (int w = 0; w <= 5; ++w)
-    if (p.group_size == NV << w) p.width_log2 = w;
-  e = launch_pdl<RouteParams>(kern, dim3(blocks), route_threads<NV>(), smem, pdl, stream, p);
-  if (e != cudaSuccess || !order || blocks == 1) return e;
-  return launch_pdl<RouteParams>(order_kernel, dim3(blocks), kOrderThreads, 0, pdl, stream, p);
+cudaError_t launch_route_g(const mfr_route_args& a, cudaStream_t stream) {
+  return a.bias != nullptr || a.num_groups > 1 ? launch_route_nv<L, NV, true>(a, stream) : launch_route_nv<L, NV, false>(a, stream);
 }
 
 template <typename L>
 cudaError_t launch_route_t(const mfr_route_args& a, cudaStream_t stream) {
-  if (a.E <= 32) return launch_route_nv<L, 1>(a, stream);
-  if (a.E <= 64) return launch_route_nv<L, 2>(a, stream);
-  if (a.E <= 128) return launch_route_nv<L, 4>(a, stream);
-  if (a.E <= 256) return launch_route_nv<L, 8>(a, stream);
-  if (a.E <= 512) return launch_route_nv<L, 16>(a, stream);
-  return launch_route_nv<L, 32>(a, stream);
+  if (a.E <= 32) return launch_route_g<L, 1>(a, stream);
+  if (a.E <= 64) return launch_route_g<L, 2>(a, stream);
+  if (a.E <= 128) return launch_route_g<L, 4>(a, stream);
+  if (a.E <= 256) return launch_route_g<L, 8>(a, stream);
+  if (a.E <= 512) return launch_route_g<L, 16>(a, stream);
+  return launch_route_g<L, 32>(a, stream);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -850,116 +1027,178 @@ cudaError_t launch_route_t(const mfr_route_args& a, cudaStream_t stream) {
 
 constexpr int kGradThreads = 256;
 
-// One warp a token: the chosen experts' gradients go into the warp's row of shared memory, which is then
-// written out whole, with the other experts' share (softmax without renormalisation) or zeros.
+// Writes a lane's NV values of a row, in vectors when all of them exist and the address allows.
+template <typename L, int NV>
+__device__ __forceinline__ void store_logits(L* row, int e0, int E, const float (&v)[NV]) {
+  constexpr int kBytes = NV * static_cast<int>(sizeof(L));
+  constexpr int kVec = kBytes >= 16 ? 16 : kBytes;
+  L* p = row + e0;
+  if constexpr (kVec >= 4) {
+    if (e0 + NV <= E && (reinterpret_cast<uintptr_t>(p) & (kVec - 1)) == 0) {
+      uint32_t raw[kBytes / 4];
+#pragma unroll
+      for (int i = 0; i < kBytes / 4; ++i) {
+        if constexpr (sizeof(L) == 4)
+          raw[i] = __float_as_uint(v[i]);
+        else
+          raw[i] = Act<L>::pack(v[2 * i], v[2 * i + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBytes / kVec; ++i) {
+        if constexpr (kVec == 16)
+          reinterpret_cast<uint4*>(p)[i] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+        else if constexpr (kVec == 8)
+          reinterpret_cast<uint2*>(p)[i] = make_uint2(raw[2 * i], raw[2 * i + 1]);
+        else
+          reinterpret_cast<uint32_t*>(p)[i] = raw[i];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (e0 + j < E) {
+      if constexpr (sizeof(L) == 4)
+        p[j] = v[j];
+      else if constexpr (std::is_same<L, __nv_bfloat16>::value)
+        p[j] = __float2bfloat16_rn(v[j]);
+      else
+        p[j] = __float2half_rn(v[j]);
+    }
+  }
+}
+
+// One warp a token.  The chosen experts' gradients meet their experts' lanes through a row of shared memory, all zeros
+// between tokens; the other experts get their share (softmax without renormalisation) or zeros.
 //   softmax            dx_e = s_e (ds_e - sum_k ds_k s_k)       ds_k = scale * dw_k, 0 for experts not chosen
 //   softmax, renorm    dx_k = p_k (ds_k - sum_j ds_j p_j)       p = softmax over the chosen logits
 //   sigmoid            dx_k = ds_k s_k (1 - s_k)
 //   sigmoid, renorm    dx_k = p_k (1 - s_k) (ds_k - sum_j ds_j p_j)   p = s / sum s
-template <typename L>
+// Bound by HBM: the logits are read (softmax without renormalisation; else only the chosen ones) and the gradient
+// written once.
+template <typename L, int NV>
 __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_constant__ mfr_route_backward_args a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = kGradThreads / 32;
-  float* buf = reinterpret_cast<float*>(smem) + warp * a.E;
-  for (int e = lane; e < a.E; e += 32) buf[e] = 0.0f;
+  __shared__ __align__(16) float rows[kGradThreads / 32][32 * NV];
+  const int lane = threadIdx.x & 31, nwarps = kGradThreads / 32, e0 = lane * NV;
+  const int warp = __shfl_sync(kAll, static_cast<int>(threadIdx.x >> 5), 0);  // known to be the same for the warp
+  float* buf = rows[warp];
+  for (int e = lane; e < 32 * NV; e += 32) buf[e] = 0.0f;
   __syncwarp();
   pdl_launch_dependents();
   pdl_wait();
-  const bool softmax = a.score == MFR_SCORE_SOFTMAX, dense = softmax && !a.renormalize;
+  const bool softmax = a.score == MFR_SCORE_SOFTMAX, dense = softmax && !a.renormalize, two = a.K > 32;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * nwarps + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * nwarps) {
     const L* row = static_cast<const L*>(a.logits) + t * a.logits_stride;
-    L* out = static_cast<L*>(a.d_logits) + t * a.d_logits_stride;
-    int id[2];
-    float x[2], d[2], g[2];
+    float v[NV];  // the logits, then the gradient
+    if (dense) load_logits<L, NV>(row, e0, a.E, v);
+    int id[2] = {-1, -1};
+    float x[2], d[2], g[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = lane + 32 * i;
-      id[i] = k < a.K ? a.expert_ids[t * a.K + k] : -1;
+      if ((i == 0 || two) && k < a.K) id[i] = a.expert_ids[t * a.K + k];
       if (id[i] >= a.E) id[i] = -1;
       x[i] = id[i] >= 0 ? clean(static_cast<float>(row[id[i]])) : -kInf;
       d[i] = id[i] >= 0 ? load_any(a.d_scale, t * a.K + k, a.scale_dtype) * a.scale : 0.0f;
     }
-    float top = -kInf, inv = 0.0f, inner = 0.0f;
-    if (dense) {
-      for (int e = lane; e < a.E; e += 32) top = fmaxf(top, clean(static_cast<float>(row[e])));
-      top = warp_max(top);
-      float sum = 0.0f;
-      for (int e = lane; e < a.E; e += 32) {
-        const float v = clean(static_cast<float>(row[e]));
-        if (v > -kInf) sum += v == top ? 1.0f : expf(v - top);
-      }
-      sum = warp_sum(sum);
-      inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-    }
+    float inner = 0.0f;
     if (softmax) {
-      if (!dense) top = warp_max(fmaxf(x[0], x[1]));
-      float p[2];
+      float top, inv;
+      if (dense) {
+        float m = v[0], sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) p[i] = !(x[i] > -kInf) ? 0.0f : x[i] == top ? 1.0f : expf(x[i] - top);
+        for (int j = 1; j < NV; ++j) m = fmaxf(m, v[j]);
+        top = warp_max(m);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          v[j] = !(v[j] > -kInf) ? 0.0f : v[j] == top ? 1.0f : fast_exp2((v[j] - top) * kLog2e);
+          sum += v[j];
+        }
+        sum = warp_sum(sum);
+        inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+      } else {
+        top = warp_max(fmaxf(x[0], x[1]));
+      }
+      float p[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if ((i == 0 || two) && x[i] > -kInf) p[i] = x[i] == top ? 1.0f : expf(x[i] - top);
       if (!dense) {
         const float sum = warp_sum(p[0] + p[1]);
         inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) p[i] *= inv;
+      p[0] *= inv;
+      p[1] *= inv;
       inner = warp_sum(d[0] * p[0] + d[1] * p[1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) g[i] = dense ? p[i] * d[i] : p[i] * (d[i] - inner);
+      inner *= inv;
     } else {
-      float q[2], l[2];  // 1 - s, and the weight p (or s)
+      float q[2], l[2] = {0.0f, 0.0f};  // 1 - s, and the weight p (or s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) q[i] = __fdiv_rn(1.0f, 1.0f + expf(x[i]));
       if (a.renormalize) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) l[i] = x[i] > -kInf ? fminf(x[i], 0.0f) - log1pf(expf(-fabsf(x[i]))) : -kInf;
-        const float m = warp_max(fmaxf(l[0], l[1]) + 0.0f);
+        const float m = warp_max(fmaxf(l[0], l[1]));
 #pragma unroll
         for (int i = 0; i < 2; ++i) l[i] = !(l[i] > -kInf) ? 0.0f : l[i] == m ? 1.0f : expf(l[i] - m);
         const float sum = warp_sum(l[0] + l[1]);
-        inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
         l[0] *= inv;
         l[1] *= inv;
         inner = warp_sum(d[0] * l[0] + d[1] * l[1]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) l[i] = __fdiv_rn(1.0f, 1.0f + expf(-x[i]));
+        for (int i = 0; i < 2; ++i)
+          if (id[i] >= 0) l[i] = __fdiv_rn(1.0f, 1.0f + expf(-x[i]));
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) g[i] = l[i] * q[i] * (d[i] - inner);
     }
-    // place by place, so that an expert named twice gets both, in order
-    for (int k = 0; k < a.K; ++k) {
-      if (lane == (k & 31)) {
-        const int i = k >> 5;
-        const int e = i ? id[1] : id[0];
-        if (e >= 0) buf[e] += i ? g[1] : g[0];
+    // Distinct experts at once; an expert named twice gets its gradients place by place.
+    const unsigned same = __match_any_sync(kAll, id[0]);  // (every lane takes part)
+    const bool twice = id[0] >= 0 && (same & (kAll >> (31 - lane))) != 1u << lane;
+    if (two || __any_sync(kAll, twice)) {
+      for (int k = 0; k < a.K; ++k) {
+        if (lane == (k & 31)) {
+          const int e = k < 32 ? id[0] : id[1];
+          if (e >= 0) buf[e] += k < 32 ? g[0] : g[1];
+        }
+        __syncwarp();
       }
-      __syncwarp();
+    } else if (id[0] >= 0) {
+      buf[id[0]] = g[0];
     }
-    for (int e = lane; e < a.E; e += 32) {
-      float v = buf[e];
-      if (dense) {
-        const float z = clean(static_cast<float>(row[e]));
-        if (z > -kInf) v -= (z == top ? 1.0f : expf(z - top)) * inv * inner;
-      }
-      buf[e] = 0.0f;
-      if constexpr (sizeof(L) == 4)
-        out[e] = v;
-      else if constexpr (std::is_same<L, __nv_bfloat16>::value)
-        out[e] = __float2bfloat16_rn(v);
-      else
-        out[e] = __float2half_rn(v);
-    }
+    __syncwarp();
+    float b[NV];
+    load_lane<NV>(buf, lane, b);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = dense ? b[j] - v[j] * inner : b[j];
+    __syncwarp();
+    if (id[0] >= 0) buf[id[0]] = 0.0f;
+    if (id[1] >= 0) buf[id[1]] = 0.0f;
+    store_logits<L, NV>(static_cast<L*>(a.d_logits) + t * a.d_logits_stride, e0, a.E, v);
     __syncwarp();
   }
 }
 
-template <typename L>
-cudaError_t launch_route_backward_t(const mfr_route_backward_args& a, cudaStream_t stream) {
+template <typename L, int NV>
+cudaError_t launch_route_backward_nv(const mfr_route_backward_args& a, cudaStream_t stream) {
   const int per = kGradThreads / 32;
   const int64_t want = (static_cast<int64_t>(a.T) + per - 1) / per;
   const int blocks = static_cast<int>(want < 152 * 8 ? want : 152 * 8);
-  return launch_pdl<mfr_route_backward_args>(route_grad_kernel<L>, dim3(blocks), kGradThreads, per * a.E * 4, a.flags & MFR_FLAG_PDL, stream, a);
+  return launch_pdl<mfr_route_backward_args>(route_grad_kernel<L, NV>, dim3(blocks), kGradThreads, 0, a.flags & MFR_FLAG_PDL, stream, a);
+}
+
+template <typename L>
+cudaError_t launch_route_backward_t(const mfr_route_backward_args& a, cudaStream_t stream) {
+  if (a.E <= 32) return launch_route_backward_nv<L, 1>(a, stream);
+  if (a.E <= 64) return launch_route_backward_nv<L, 2>(a, stream);
+  if (a.E <= 128) return launch_route_backward_nv<L, 4>(a, stream);
+  if (a.E <= 256) return launch_route_backward_nv<L, 8>(a, stream);
+  if (a.E <= 512) return launch_route_backward_nv<L, 16>(a, stream);
+  return launch_route_backward_nv<L, 32>(a, stream);
 }
 
 }  // namespace

@@ -226,8 +226,8 @@ int64_t moe_route_max_rows(int32_t T, int32_t K, int32_t E, int32_t row_align) {
 int64_t moe_route_workspace_bytes(int32_t T, int32_t K, int32_t E) {
   int st;
   if ((st = check_routes(T, K)) != MFR_OK || (st = check_experts(E, K)) != MFR_OK) return st;
-  const int blocks = route_blocks(T);
-  return blocks > 1 ? (static_cast<int64_t>(blocks) * E * 4 + 15) / 16 * 16 : 0;  // the chunks' counts of each expert
+  const int chunks = route_chunks(T, E, true);
+  return chunks > kRouteCluster ? (static_cast<int64_t>(chunks) * E * 4 + 15) / 16 * 16 : 0;  // the chunks' counts of each expert
 }
 
 int moe_route_backward(const mfr_route_backward_args* args, struct CUstream_st* stream) {
