@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import struct
 from typing import Optional, Tuple
 
@@ -197,6 +198,9 @@ def moe_route_workspace_bytes(T: int, K: int, E: int) -> int:
     return _size(_lib.moe_route_workspace_bytes(T, K, E))
 
 
+_route_space = functools.lru_cache(maxsize=1024)(lambda T, K, E: moe_route_workspace_bytes(T, K, E))
+
+
 def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
               num_groups: int = 1, topk_groups: int = 1, group_score: str = "max", renormalize: bool = True,
               scale: float = 1.0, scale_dtype: torch.dtype = torch.float32, row_align: int = 1, order: bool = True,
@@ -261,7 +265,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
         if workspace is not None:
             space = workspace.numel()
         else:
-            space = moe_route_workspace_bytes(T, top_k, E)
+            space = _route_space(T, top_k, E)
             if space:
                 workspace = torch.empty(space, dtype=torch.uint8, device=logits.device)
                 allocated.append(workspace)
@@ -436,10 +440,11 @@ def _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act):
             and _good_heads(k, index, (T, k.shape[1], D), act)):
         _check_heads("q", q, q.device, None, (torch.bfloat16, torch.float16))
         _check_heads("k", k, q.device, (T, k.shape[1], D), act)
-    if q_weight is not None and not _good(q_weight, index, (D,), act):
-        _check_tensor("q_weight", q_weight, q.device, (D,), act)
-    if k_weight is not None and not _good(k_weight, index, (D,), act):
-        _check_tensor("k_weight", k_weight, q.device, (D,), act)
+    shape = (D,)
+    if q_weight is not None and not _good(q_weight, index, shape, act):
+        _check_tensor("q_weight", q_weight, q.device, shape, act)
+    if k_weight is not None and not _good(k_weight, index, shape, act):
+        _check_tensor("k_weight", k_weight, q.device, shape, act)
     if not (positions.dtype is torch.int32 and _good(positions, index, (T,), torch.int32)):
         _check_tensor("positions", positions, q.device, (T,), (torch.int32, torch.int64))
     if not _good(inv_freq, index, (inv_freq.numel(),), torch.float32):
@@ -492,6 +497,9 @@ def head_norm_rotary_workspace_bytes(T: int, q_heads: int, k_heads: int, D: int)
     return _size(_lib.moe_head_norm_rotary_workspace_bytes(T, q_heads, k_heads, D))
 
 
+_head_space = functools.lru_cache(maxsize=1024)(lambda *sizes: head_norm_rotary_workspace_bytes(*sizes))
+
+
 def head_norm_rotary_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
                               q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
                               positions: torch.Tensor, inv_freq: torch.Tensor, *, eps: float = 1e-6,
@@ -533,7 +541,7 @@ def head_norm_rotary_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: t
                 _check_tensor("workspace", workspace, dev, None, torch.uint8)
             space = workspace.numel()
         else:
-            space = head_norm_rotary_workspace_bytes(T, hq, hk, D)
+            space = _head_space(T, hq, hk, D)
             workspace = torch.empty(space, dtype=torch.uint8, device=dev)
             allocated.append(workspace)
     if check:
