@@ -601,17 +601,14 @@ __global__ void __launch_bounds__(kSumThreads) head_weight_grad_kernel(const __g
 template <typename A, int G, int STYLE>
 cudaError_t launch_forward(const HeadParams& p, cudaStream_t stream) {
   const int smem = kFwdThreads / 32 * (kSlotBytes<kFwdSlots, 2> + p.cut.cache_bytes);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<A, G, STYLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  static_assert(kFwdThreads / 32 * (kSlotBytes<kFwdSlots, 2> + 32 * 256) <= 48 * 1024, "32 lanes' turns of both kinds fit without asking");
   return launch_pdl<HeadParams>(head_norm_kernel<A, G, STYLE>, dim3(static_cast<unsigned>(p.cut.ctas)), kFwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
 }
 template <typename A, int G, int STYLE>
 cudaError_t launch_backward(const HeadParams& p, cudaStream_t stream) {
   static_assert(kSlotBytes<kBwdSlots, 4> >= 2 * MFR_MAX_HEAD_DIM * 4, "a warp's sums fit in its slots");
   const int smem = kBwdWarps * bwd_warp_bytes(p.cut.cache_bytes);
-  const cudaError_t e = cudaFuncSetAttribute(head_norm_grad_kernel<A, G, STYLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<head_norm_grad_kernel<A, G, STYLE>>(kBwdWarps * bwd_warp_bytes(32 * 64));  // 32 lanes' turns
   if (e != cudaSuccess) return e;
   return launch_pdl<HeadParams>(head_norm_grad_kernel<A, G, STYLE>, dim3(static_cast<unsigned>(p.cut.ctas)), kBwdThreads, smem, p.a.flags & MFR_FLAG_PDL, stream, p);
 }

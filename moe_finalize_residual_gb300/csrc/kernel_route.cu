@@ -994,8 +994,7 @@ cudaError_t launch_route_nv(const mfr_route_args& a, cudaStream_t stream) {
   const int smem = fixed + (order ? order_smem_bytes(a.E, a.K) : 0);
   auto kern = route_kernel<L, NV, GENERAL>;
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + order_smem_bytes(NV * 32, MFR_MAX_TOP_K));
+  if (smem > 48 * 1024) e = allow_smem<route_kernel<L, NV, GENERAL>>(fixed + order_smem_bytes(NV * 32, MFR_MAX_TOP_K));
   if (e != cudaSuccess) return e;
   const int chunks = route_chunks(a.T, a.E, order);
   RouteParams p{a, a.E / a.num_groups, -1, order && chunks <= kRouteCluster, a.T / chunks, a.T % chunks};

@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "mfr_device.cuh"
 #include "moe_layer.h"
 
@@ -40,6 +42,21 @@ cudaError_t launch_routed_backward(const mfr_routed_backward_args& a, cudaStream
 int head_grad_rows(int T, int q_heads, int k_heads, int D);
 cudaError_t launch_head_norm(const mfr_head_norm_args& a, cudaStream_t stream);
 cudaError_t launch_head_norm_backward(const mfr_head_norm_args& a, cudaStream_t stream);
+
+// Lets Kern have up to `most` bytes of dynamic shared memory on the current device: once a device, since the runtime's
+// call costs as much as a small launch's preparation.
+template <auto Kern>
+cudaError_t allow_smem(int most) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch `kern` in clusters of `cluster` CTAs, with the programmatic-dependent-launch attribute iff `pdl`.  Every kernel
 // launched this way waits (pdl_wait) before it reads or writes anything.

@@ -97,10 +97,10 @@ def _args(mfr, call):
     """A valid argument block of a call, with fake pointers."""
     L = mfr.layer
     if call == "moe_route":
-        a = L._CRoute(T=100, E=64, K=8, logits_dtype=2, scale_dtype=2, score=0, num_groups=8, topk_groups=4,
+        a = L._CRoute(T=1000, E=64, K=8, logits_dtype=2, scale_dtype=2, score=0, num_groups=8, topk_groups=4,
                       group_score=1, renormalize=1, row_align=16, scale=1.0, logits=0x10000, logits_stride=64,
                       bias=0x20000, expert_ids=0x30000, expert_scale=0x40000, perm_idx=0x50000, row_route=0x60000,
-                      num_rows=2000, expert_offsets=0x70000, expert_counts=0x80000, workspace=0x90000,
+                      num_rows=10000, expert_offsets=0x70000, expert_counts=0x80000, workspace=0x90000,
                       workspace_bytes=1 << 20, flags=1)
     elif call == "moe_route_backward":
         a = L._CRouteBackward(T=100, E=64, K=8, logits_dtype=0, scale_dtype=2, score=1, renormalize=0, scale=1.0,
