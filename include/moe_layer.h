@@ -16,7 +16,8 @@
  * no allocation and no synchronization inside, a negative status before anything is enqueued on error
  * (message by moe_finalize_last_error), work enqueued on `stream`, MFR_FLAG_PDL to launch with programmatic
  * dependent launch (every kernel waits for its predecessor before reading or writing anything).  Two calls
- * that may run at the same time must not share a workspace.  All sums, products, softmax and norm
+ * that may run at the same time must not share a workspace.  Outputs overlap no input and not each other, unless
+ * a call says so.  All sums, products, softmax and norm
  * statistics are FP32 or wider; an output in a 16-bit type is rounded once, to nearest even.  Every result
  * is the same from run to run: no atomic changes the order of a sum.
  */
@@ -127,8 +128,8 @@ int moe_route_backward(const mfr_route_backward_args* args, struct CUstream_st* 
 /* ---------------------------------------------------------------------------------------------------- */
 
 /* rows[perm_idx[t, k]] = x[t] for every route whose perm_idx lies in [0, num_rows); no two routes may name
- * the same row.  With row_route, rows whose route is negative are set to zero; without it they are left as
- * they were.  Rows of any type, copied as bytes.  Its gradient to x is moe_finalize_fused in finalize-only
+ * the same row.  With row_route (perm_idx the other way round, as moe_route writes it), rows whose route is
+ * negative are set to zero; without it they are left as they were.  Rows of any type, copied as bytes.  Its gradient to x is moe_finalize_fused in finalize-only
  * mode over the gradient rows, with expert_scale NULL and a factor of 1. */
 typedef struct {
   int32_t T, K;              /* K in 1..MFR_MAX_TOP_K, T*K < 2^31                                        */
@@ -148,8 +149,8 @@ int moe_dispatch_rows(const mfr_dispatch_args* args, struct CUstream_st* stream)
  *   d_gemm2[perm[t,k]] = round_act((scale[t,k] * rsf) * d_out[t])
  *   d_scale[t,k]       = round(rsf * sum_h row[perm[t,k], h] * d_out[t, h])        0 for a skipped route
  * (the gradient of the shared row is d_out itself).  Routes outside [0, num_rows) are skipped; no two routes
- * may name the same row.  With row_route, rows of d_gemm2 whose route is negative are set to zero; without
- * it they are left as they were. */
+ * may name the same row.  With row_route (perm_idx the other way round), rows of d_gemm2 whose route is
+ * negative are set to zero; without it they are left as they were. */
 typedef struct {
   int32_t T, H, K;           /* as in mfr_args                                                          */
   int32_t act_dtype;         /* of gemm2_out, d_out, d_gemm2                                             */

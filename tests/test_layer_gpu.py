@@ -94,6 +94,9 @@ ROUTES = [  # T, E, K, score, renorm, logits, biased, G, Gk, top2, align
     (1000, 128, 1, "sigmoid", False, "bf16", True, 2, 1, True, 64),
     (2500, 96, 3, "softmax", True, "fp32", True, 3, 2, True, 1),  # groups of one lane and a third
     (20000, 16, 2, "softmax", True, "fp32", False, 1, 1, False, 8),  # more than one segment a chunk
+    (40, 64, 20, "sigmoid", True, "fp32", True, 8, 1, True, 16),  # fewer experts in the kept groups than places
+    (200, 512, 62, "sigmoid", True, "fp32", True, 4, 2, False, 1),  # nearly as many places as candidates are ranked
+    (90, 1024, 40, "softmax", False, "bf16", True, 1, 1, False, 1),
 ]
 
 
@@ -432,10 +435,11 @@ def _heads(T, Hq, Hk, D, rot, act, seed, packed):
     return q, k, w, pos, freq
 
 
-# The value before its rounding: the mean square (16 fused steps, 5 adds, a division) and the root, half of it each:
-# 12 u; three products; the angle 1.2e-7 (2^-32 turns and a rounding of the half turn: pi 2^-25) and the sine or cosine
-# 2 u; the rotation's two products and sum on both elements of the pair.
-H_REL = 12 * U + 3 * U + 1.2e-7 + 4 * U + 3 * U
+# The value before its rounding, relative to its pair's length: the mean square (two chains of 8 fused steps, their sum,
+# 5 adds, a fused step) 15 u, half of it in the root, and the root itself 4 u; the element times the root u; the turn: the
+# angle 1.2e-7 (2^-32 turns and a rounding of the half turn: pi 2^-25), the sine or cosine 2 u, times rotary_scale u, times
+# the weight u; the products and their sum 2 u, all of it on both elements: (7.5 + 4 + 1 + 4 + 2) u = 18.5 u, and 1.2e-7.
+H_REL = 22 * U + 1.2e-7
 
 
 def _pair_size(v, rot, style):
@@ -814,6 +818,57 @@ def test_calls_on_another_stream_than_the_current(mfr):
         torch.full((5000, 64), 1e9, device="cuda")  # would land in freed memory
         side.synchronize()
         assert torch.equal(got.perm_idx, want.perm_idx) and torch.equal(got.row_route, want.row_route)
+
+
+def test_two_calls_at_once(mfr):
+    """The same calls on two streams, each with workspaces of its own."""
+    L = [Layer(700, seed=s) for s in (1, 2)]
+    want = [[t.clone() for t in _flat(x.forward(mfr)) + list(x.step(mfr))] for x in L]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [None, None]
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = _flat(L[i].forward(mfr)) + list(L[i].step(mfr))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_offsets_past_32_bits(mfr):
+    """Rows, tokens and heads that lie more than 2^32 bytes apart."""
+    x = torch.randint(0, 255, (2, 1 << 20), generator=gen(0), dtype=torch.uint8).cuda()
+    perm = torch.tensor([[0, 4999], [4500, 2]], dtype=torch.int32, device="cuda")
+    rows = mfr.moe_dispatch(x, perm, 5000)
+    assert torch.equal(rows[[0, 4999]], x[[0, 0]]) and torch.equal(rows[[4500, 2]], x[[1, 1]]) and not rows[4998].any()
+    del rows
+    H, n = 8192, 300000
+    gemm2 = torch.zeros(n, H, dtype=torch.bfloat16, device="cuda")
+    d = torch.randn(2, H, generator=gen(1)).bfloat16().cuda()
+    perm = torch.tensor([[n - 1, 5], [n - 2, 280001]], dtype=torch.int32, device="cuda")
+    gemm2[n - 1], gemm2[280001] = 1, 2
+    d_rows, d_scale = mfr.moe_finalize_routed_backward(d, mfr.Partial(gemm2, perm))
+    assert torch.equal(d_rows[perm.long()], d[:, None].expand(2, 2, H)) and int((d_rows != 0).any(1).sum()) == 4
+    want = torch.tensor([[1.0, 0.0], [0.0, 2.0]], device="cuda").double() * d.double().sum(1, keepdim=True)
+    assert ((d_scale.double() - want).abs() <= (-(-H // 2048) * 8 + 14) * U * 2 * d.double().abs().sum(1, keepdim=True)).all()
+    del gemm2, d_rows
+    wide = torch.zeros(3, 1 << 30, dtype=torch.float16, device="cuda")
+    q = wide[:, 8:8 + 256].view(3, 2, 128)
+    q.copy_(torch.randn(3, 2, 128, generator=gen(2)))
+    pos, freq = torch.arange(3, device="cuda"), torch.rand(64, generator=gen(3)).cuda()
+    w = torch.ones(128, dtype=torch.float16, device="cuda")
+    a, _ = mfr.head_norm_rotary(q, q, w, w, pos, freq)
+    b, _ = mfr.head_norm_rotary(q.contiguous(), q.contiguous(), w, w, pos, freq)
+    assert torch.equal(a, b)
+    ga = mfr.head_norm_rotary_backward(q, q, q, q, w, w, pos, freq)
+    c = q.contiguous()
+    gb = mfr.head_norm_rotary_backward(c, c, c, c, w, w, pos, freq)
+    assert all(torch.equal(x, y) for x, y in zip(ga, gb))
+    logits = wide[:, 5:5 + 100]
+    logits.copy_(torch.randn(3, 100, generator=gen(4)))
+    a, b = mfr.moe_route(logits, 7), mfr.moe_route(logits.contiguous(), 7)
+    assert torch.equal(a.expert_ids, b.expert_ids) and torch.equal(a.perm_idx, b.perm_idx)
 
 
 @pytest.mark.parametrize("T", [7, 300])
