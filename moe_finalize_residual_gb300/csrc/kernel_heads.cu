@@ -18,7 +18,9 @@
 // flight by cp.async into slots of shared memory that each lane fills and reads by itself, so no warp waits for
 // another.
 //
-// Bound by HBM: forward reads and writes each element once; backward reads two and writes one.
+// Bound by HBM: forward reads and writes each element once; backward reads two and writes one.  Measured on GB300 (copy
+// bandwidth 6779 GB/s), 48 + 8 heads of 128, BF16, from a packed projection: forward of 16384 tokens, 470 MB, 71.4 us
+// (0.97 of the copy); gradient of 8192 tokens, 352 MB, 60 us (0.86), of which 3 us are the sum of the weight gradients.
 #include <algorithm>
 
 #include "layer_launch.h"
@@ -237,7 +239,8 @@ constexpr int kFwdThreads = 64;
 constexpr int kFwdCtas = 12;  // CTAs an SM holds, by registers
 
 // Forward: a warp takes its rounds of one block of tokens.  The CTAs are small and come and go, which evens out the
-// SMs' load; a warp requests its first vectors, its position, frequencies and weights all at once.
+// SMs' load; a warp requests its first vectors, its position, frequencies and weights all at once.  Persistent warps
+// with equal shares took 82 to 88 us for the 71.4 above: their streams lie far apart, or the last of them end late.
 template <typename A, int G, int STYLE>
 __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) head_norm_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -413,7 +416,8 @@ __device__ __forceinline__ void write_sums(Pairs dw, const LaneMap& m, bool writ
 constexpr int kKeySumBytes = 4 * 32 * 16;
 __host__ __device__ constexpr int bwd_warp_bytes(int cache_bytes) { return kSlotBytes<kBwdSlots, 4> + cache_bytes + kKeySumBytes; }
 
-// Gradient: the warps that the GPU holds share all rounds equally, each a contiguous range.
+// Gradient: the warps that the GPU holds share all rounds equally, each a contiguous range, so that few rows of partial
+// weight gradients are left to add (CTAs that come and go, as forward: 57 us, but 6.5 us more to add their rows).
 template <typename A, int G, int STYLE>
 __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) head_norm_grad_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(16) uint8_t smem[];

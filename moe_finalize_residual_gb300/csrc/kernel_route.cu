@@ -15,6 +15,12 @@
 // of marks below its own, so the marks may be set in any order (atomicOr) with the same result.  Small batches
 // run as one cluster whose CTAs read each other's counts from shared memory, in one launch; larger ones leave
 // the chunks' counts in the workspace, and a second kernel (order_kernel) adds those of the chunks before its own.
+//
+// Bound by instructions, not by HBM: a token of 256 experts takes about 465 warp instructions for a choice by logits
+// and about 950 with a bias, groups and 64-bit decisions, while its logits take 0.15 ns of HBM time.  Ranking the few
+// candidates by counting is what keeps it there: one expert after the other took 1835.  Measured on GB300, in a graph:
+// 16384 tokens of 256 experts, top-8, 9.9 us by logits and 20 us with bias and groups (the logits are 2.5 us at the copy
+// bandwidth), and 7 us more for the order; one token 2.5 us, 3.9 us with the order.
 #include "layer_launch.h"
 
 namespace mfr {
@@ -925,7 +931,9 @@ __global__ void __launch_bounds__(kRouteThreads<NV, GENERAL>, 1) route_kernel(co
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderParts = 4096;  // partial counts of an expert, times the experts, at most
 
-// Adds the chunks' counts and finishes the order of chunk blockIdx.x.
+// Adds the chunks' counts and finishes the order of chunk blockIdx.x.  Every CTA reads all counts (152 x 256 of them 156
+// KB, from L2) rather than wait for another launch to add them once: about 5.5 us, latency from the first load to the
+// last store.
 __global__ void __launch_bounds__(kOrderThreads, 1) order_kernel(const __grid_constant__ RouteParams p) {
   __shared__ int before[MFR_MAX_EXPERTS], total[MFR_MAX_EXPERTS], off[MFR_MAX_EXPERTS + 1], warp_sums[32];
   __shared__ int4 part_before[kOrderParts / 4], part_total[kOrderParts / 4];
@@ -1074,7 +1082,9 @@ __device__ __forceinline__ void store_logits(L* row, int e0, int E, const float 
 //   sigmoid            dx_k = ds_k s_k (1 - s_k)
 //   sigmoid, renorm    dx_k = p_k (1 - s_k) (ds_k - sum_j ds_j p_j)   p = s / sum s
 // Bound by HBM: the logits are read (softmax without renormalisation; else only the chosen ones) and the gradient
-// written once.
+// written once.  16384 tokens of 256 experts, FP32 softmax without renormalisation, 35 MB: 9.4 us in a graph (5.1 us at
+// the copy bandwidth; about 3 us are the launch and the first loads).  With scalar loads and the row read three times it
+// took 15.4 us.
 template <typename L, int NV>
 __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_constant__ mfr_route_backward_args a) {
   __shared__ __align__(16) float rows[kGradThreads / 32][32 * NV];

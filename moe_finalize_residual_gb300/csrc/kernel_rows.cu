@@ -2,8 +2,13 @@
 // of the finalize to those rows and to the expert scales.
 //
 // Both move whole 16-byte vectors and are bound by HBM: a token's row is read once (K rows are written
-// from it), every expert row once.  A CTA takes one token and up to KB of its routes, so that all its row
-// vectors are in flight together; rows that no route names are set to zero by the CTAs behind the tokens'.
+// from it), every expert row once.  A CTA takes one token (or a slice of its row) and, in the gradient, up to
+// KB of its routes, so that all its row vectors are in flight together; rows that no route names are set to
+// zero by the CTAs behind the tokens'.
+//
+// Measured on GB300 (copy bandwidth 6779 GB/s): dispatch of 4096 tokens of 7168 FP16 elements to 8 experts, a
+// quarter of the routes masked, 529 MB in 81 us (0.96 of the copy); the gradient of the same batch in BF16, 881 MB
+// in 132 us (0.98).
 #include "layer_launch.h"
 
 namespace mfr {
@@ -167,9 +172,12 @@ __global__ void __launch_bounds__(kBackThreads) routed_backward_kernel(const __g
 template <typename A>
 cudaError_t launch_routed_backward_t(const mfr_routed_backward_args& a, cudaStream_t stream) {
   RoutedBackwardParams p{a, {}};
-  // Few tokens: one route a CTA, so that the rows spread over the SMs; else up to 8 rows in flight a thread.
+  // Up to 8 routes a CTA, so that a thread has as many rows in flight and reads the token's gradient once, as long as
+  // that leaves three CTAs for each SM.  us at KB = 1 / 2 / 4 / 8: 8 tokens of H 7168, top-8, 3.2 / 3.5 / 4.1 / 5.6; 64
+  // tokens of H 3584, top-16, 4.6 / 4.3 / 4.7 / 6.6; 152 of them 7.9 / 6.5 / 5.7 / 6.1; 4096 tokens of H 7168, top-8,
+  // 191 / 149 / 134 / 133.
   int kb = 1;
-  while (kb < 8 && kb < a.K && static_cast<int64_t>(a.T) * ((a.K + 2 * kb - 1) / (2 * kb)) >= 2 * 152) kb *= 2;
+  while (kb < 8 && kb < a.K && static_cast<int64_t>(a.T) * ((a.K + 2 * kb - 1) / (2 * kb)) >= 3 * 152) kb *= 2;
   p.g.slices = (a.K + kb - 1) / kb;
   p.g.token_ctas = static_cast<int64_t>(a.T) * p.g.slices;
   p.g.zero_ctas = a.row_route != nullptr && a.d_gemm2 != nullptr ? (a.num_rows + kZeroRows - 1) / kZeroRows : 0;
@@ -191,7 +199,8 @@ cudaError_t launch_routed_backward_t(const mfr_routed_backward_args& a, cudaStre
 cudaError_t launch_dispatch(const mfr_dispatch_args& a, cudaStream_t stream) {
   DispatchParams p{a, {}, 0};
   const int nvec = static_cast<int>(a.row_bytes / 16);
-  // Whole rows a CTA for batches that fill the SMs, else slices of at least one warp's vectors.
+  // Whole rows a CTA for batches that fill the SMs four times, else slices of at least one warp's vectors.  With one
+  // CTA an SM in place of four: 300 tokens of 6144 BF16 elements, top-8, 10.0 us against 6.1; 16 tokens 1.9 either way.
   int64_t slices = a.T > 0 ? (4 * 152 + a.T - 1) / a.T : 1;
   const int most = (nvec + 31) / 32;
   if (slices > most) slices = most;
