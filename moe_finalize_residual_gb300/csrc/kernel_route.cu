@@ -16,11 +16,11 @@
 // run as one cluster whose CTAs read each other's counts from shared memory, in one launch; larger ones leave
 // the chunks' counts in the workspace, and a second kernel (order_kernel) adds those of the chunks before its own.
 //
-// Bound by instructions, not by HBM: a token of 256 experts takes about 465 warp instructions for a choice by logits
-// and about 950 with a bias, groups and 64-bit decisions, while its logits take 0.15 ns of HBM time.  Ranking the few
+// Bound by instructions, not by HBM: a token of 256 experts takes about 430 warp instructions for a choice by logits
+// and about 900 with a bias, groups and 64-bit decisions, while its logits take 0.15 ns of HBM time.  Ranking the few
 // candidates by counting is what keeps it there: one expert after the other took 1835.  Measured on GB300, in a graph:
-// 16384 tokens of 256 experts, top-8, 9.9 us by logits and 20 us with bias and groups (the logits are 2.5 us at the copy
-// bandwidth), and 7 us more for the order; one token 2.5 us, 3.9 us with the order.
+// 16384 tokens of 256 experts, top-8, 9.3 us by logits and 19.4 us with bias and groups (the logits are 2.5 us at the
+// copy bandwidth), and 7 us more for the order; one token 2.5 us, 3.8 us with the order.
 #include "layer_launch.h"
 
 namespace mfr {
@@ -202,9 +202,9 @@ __device__ __noinline__ double score_sum64(const mfr_route_args& a, const L* row
 }
 
 // Chooses the token's experts with every score in FP64 (local arrays: this path is rare).  Lane l gets the
-// ids of places l and l + 32.
+// ids of places l and l + 32.  (Out of line, and by value: what the hot path keeps in registers must not have an address.)
 template <typename L, int NV>
-__device__ __noinline__ void slow_choice(const mfr_route_args& a, const L* row, int lane, int& id0, int& id1) {
+__device__ __noinline__ int2 slow_choice(const mfr_route_args& a, const L* row, int lane) {
   constexpr int64_t kNone = INT64_MIN;
   int64_t c[NV];  // choice scores, as ordered integers
   double s[NV];
@@ -255,7 +255,7 @@ __device__ __noinline__ void slow_choice(const mfr_route_args& a, const L* row, 
     for (int j = 0; j < NV; ++j)
       if (e0 + j < a.E && !((kept >> ((e0 + j) / size)) & 1)) c[j] = kNone;
   }
-  id0 = id1 = -1;
+  int id0 = -1, id1 = -1;
   for (int k = 0; k < a.K; ++k) {
     int64_t best = kNone;
     int at = INT32_MAX;
@@ -277,6 +277,7 @@ __device__ __noinline__ void slow_choice(const mfr_route_args& a, const L* row, 
     if (at / NV == lane) c[at % NV] = kNone;
     if (lane == (k & 31)) (k < 32 ? id0 : id1) = at;
   }
+  return make_int2(id0, id1);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -307,9 +308,10 @@ __device__ __forceinline__ Scratch scratch_of(uint8_t* base) {
 // The groups whose scores lie within `tol` of the border between kept and dropped ones, decided again in FP64.
 // sc.scores holds the values that the groups compare, lane g group g's score and second best value; `in`: whether
 // it is kept.  Returns the groups kept, or 0 when too many values matter.
-template <typename L>
-__device__ __noinline__ unsigned decide_groups(const RouteParams& p, const L* row, int lane, const Scratch& sc, float top, float mine,
+template <typename L, int NV>
+__device__ __noinline__ unsigned decide_groups(const RouteParams& p, const L* row, int lane, uint8_t* scratch, float top, float mine,
                                                float second, bool in, float worst, float best_out, float tol) {
+  const Scratch sc = scratch_of<NV>(scratch);
   const mfr_route_args& a = p.a;
   const bool top2 = a.group_score == MFR_GROUP_TOP2, biased = a.bias != nullptr;
   const bool here = lane < a.num_groups && mine > -kInf;
@@ -358,9 +360,9 @@ __device__ __noinline__ unsigned decide_groups(const RouteParams& p, const L* ro
 }
 
 // The candidates' ranks again, in FP64.
-template <typename L>
-__device__ __noinline__ void decide_candidates(const mfr_route_args& a, const L* row, int lane, const Scratch& sc, float top, int n,
-                                               int& rank0, int& rank1) {
+template <typename L, int NV>
+__device__ __noinline__ int2 decide_candidates(const mfr_route_args& a, const L* row, int lane, uint8_t* scratch, float top, int n) {
+  const Scratch sc = scratch_of<NV>(scratch);
   const double inv = 1.0 / score_sum64(a, row, lane, top);
   for (int q = lane; q < n; q += 32) {
     const int e = sc.expert[q];
@@ -368,12 +370,13 @@ __device__ __noinline__ void decide_candidates(const mfr_route_args& a, const L*
   }
   __syncwarp();
   const int64_t v0 = lane < n ? sc.wide[lane] : 0, v1 = lane + 32 < n ? sc.wide[lane + 32] : 0;
-  rank0 = rank1 = 0;
+  int rank0 = 0, rank1 = 0;
   for (int q = 0; q < n; ++q) {
     const int64_t u = sc.wide[q];
     rank0 += (u > v0 || (u == v0 && q < lane)) ? 1 : 0;
     rank1 += (u > v1 || (u == v1 && q < lane + 32)) ? 1 : 0;
   }
+  return make_int2(rank0, rank1);
 }
 
 // Chooses and weighs the experts of one token whose logits are x.  Each lane gets up to two of them: the
@@ -381,7 +384,8 @@ __device__ __noinline__ void decide_candidates(const mfr_route_args& a, const L*
 // there are biases or groups; without them the logits decide and no score is needed for the choice.
 template <typename L, int NV, bool GENERAL>
 __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, float (&x)[NV], int lane, const float* bias,
-                                            const Scratch& sc, int (&id)[2], int (&place)[2], int& taken) {
+                                            uint8_t* scratch, int (&id)[2], int (&place)[2], int& taken) {
+  const Scratch sc = scratch_of<NV>(scratch);
   const mfr_route_args& a = p.a;
   const L* row = static_cast<const L*>(a.logits) + t * a.logits_stride;
   const int e0 = lane * NV;
@@ -431,72 +435,105 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
   bool close = false;  // a decision lies within the error bound and too many experts with it: all in FP64
   if (GENERAL && a.num_groups > 1) {
     const bool sums = top2 && !biased;  // groups compare sums of scores, experts compare logits
-    float mine = -kInf, second = -kInf; // lane g: group g's score, and its second best value
-    if (p.width_log2 >= 0) {
-      float b1 = -kInf, b2 = -kInf;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const float v = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
-      }
-      for (int o = (1 << p.width_log2) >> 1; o > 0; o >>= 1) {
-        const float v1 = __shfl_xor_sync(kAll, b1, o), v2 = __shfl_xor_sync(kAll, b2, o);
-        b2 = fmaxf(fminf(b1, v1), fmaxf(b2, v2));
-        b1 = fmaxf(b1, v1);
-      }
-      const int from = (lane << p.width_log2) & 31;
-      mine = __shfl_sync(kAll, group_score(b1, b2, top2), from);
-      second = __shfl_sync(kAll, b2, from);
-      if (lane >= a.num_groups) mine = -kInf;
-    } else {
+    // what the groups compare of the lane's experts, for the paths that read it from shared memory
+    auto share_values = [&]() {
       float v[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) v[j] = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
       store_lane<NV>(sc.scores, lane, v);
       __syncwarp();
+    };
+    float mine = -kInf, second = -kInf;  // a group's score and second best value: its lanes hold them, or lane g group g's
+    float worst = -kInf, best_out = -kInf;  // the kept group nearest to a dropped one, and that one
+    bool on = false;                        // the lane's group is kept, or group `lane` is
+    const int w = p.width_log2;
+    if (w >= 0) {
+      if (sums) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const float v = c[j] > -kInf ? s[j] : -kInf;
+          second = fmaxf(second, fminf(mine, v));
+          mine = fmaxf(mine, v);
+        }
+      } else if (top2) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          second = fmaxf(second, fminf(mine, c[j]));
+          mine = fmaxf(mine, c[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) mine = fmaxf(mine, c[j]);
+      }
+      for (int o = (1 << w) >> 1; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(kAll, mine, o);
+        if (top2) second = fmaxf(fminf(mine, m2), fmaxf(second, __shfl_xor_sync(kAll, second, o)));
+        mine = fmaxf(mine, m2);
+      }
+      if (top2) mine = group_score(mine, second, true);
+      // the best group again and again; among equal ones the lowest lane's
+      const uint32_t key = ordered(mine + 0.0f);
+      const uint32_t none = ordered(-kInf);
+      uint32_t last = none;
+      for (int i = 0; i < a.topk_groups; ++i) {
+        const uint32_t m = __reduce_max_sync(kAll, on ? 0 : key);
+        if (m <= none) break;
+        const int first = __ffs(__ballot_sync(kAll, !on && key == m)) - 1;
+        on = on || (lane >> w) == (first >> w);
+        last = m;
+      }
+      worst = unordered(last);
+      best_out = unordered(max(none, __reduce_max_sync(kAll, on ? 0 : key)));
+    } else {
+      share_values();
       if (lane < a.num_groups) {
-        float b1 = -kInf;
         for (int i = 0; i < p.group_size; ++i) {
           const float v = sc.scores[lane * p.group_size + i];
-          second = fmaxf(second, fminf(b1, v));
-          b1 = fmaxf(b1, v);
+          second = fmaxf(second, fminf(mine, v));
+          mine = fmaxf(mine, v);
         }
-        mine = group_score(b1, second, top2);
+        mine = group_score(mine, second, top2);
       }
       __syncwarp();
+      int rank = 0;
+      for (int g = 0; g < a.num_groups; ++g) {
+        const float v = __shfl_sync(kAll, mine, g);
+        rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
+      }
+      on = rank < a.topk_groups && mine > -kInf;
+      worst = -warp_max(on ? -mine : -kInf);
+      best_out = warp_max(on ? -kInf : mine);
     }
-    int rank = 0;
-#pragma unroll 4
-    for (int g = 0; g < a.num_groups; ++g) {
-      const float v = __shfl_sync(kAll, mine, g);
-      rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
-    }
-    const bool in = rank < a.topk_groups && mine > -kInf;
-    unsigned kept = __ballot_sync(kAll, in);
+    unsigned kept = 0;  // by group
+    bool by_group = w < 0;
     if (top2 || biased) {
-      // the kept group nearest to a dropped one
-      const float worst = -warp_max(in ? -mine : -kInf);
-      const float best_out = warp_max(in ? -kInf : mine);
       const float tol = (top2 ? 4.0f : 2.0f) * err + 2.4e-7f * (fabsf(worst) + fabsf(best_out));
-      if (best_out > -kInf && !(worst - best_out > tol)) {
-        if (p.width_log2 >= 0) {
-          float v[NV];
-#pragma unroll
-          for (int j = 0; j < NV; ++j) v[j] = sums ? (c[j] > -kInf ? s[j] : -kInf) : c[j];
-          store_lane<NV>(sc.scores, lane, v);
-          __syncwarp();
+      if (__any_sync(kAll, best_out > -kInf && !(worst - best_out > tol))) {  // (the same for all lanes)
+        if (w >= 0) {
+          // group g's to lane g
+          const int from = (lane << w) & 31;
+          mine = __shfl_sync(kAll, mine, from);
+          second = __shfl_sync(kAll, second, from);
+          on = __shfl_sync(kAll, on, from);
+          if (lane >= a.num_groups) {
+            mine = -kInf;
+            on = false;
+          }
+          share_values();
         }
-        kept = decide_groups(p, row, lane, sc, top, mine, second, in, worst, best_out, tol);
+        kept = decide_groups<L, NV>(p, row, lane, scratch, top, mine, second, on, worst, best_out, tol);
         close = kept == 0;
+        if (w >= 0) on = (kept >> (lane >> w)) & 1;
+        by_group = false;
       }
     }
-    if (p.width_log2 >= 0) {
-      if (!((kept >> (lane >> p.width_log2)) & 1)) {
+    if (w >= 0) {
+      if (!on) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) c[j] = -kInf;
       }
     } else {
+      if (by_group) kept = __ballot_sync(kAll, on);
       int g = e0 / p.group_size, left = p.group_size - e0 % p.group_size;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -525,7 +562,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
     const uint32_t first = __reduce_max_sync(kAll, key);
     uint32_t tau = first;
     if (a.K < 32) {
-#pragma unroll 4
+#pragma unroll 8
       for (int k = 0; k < a.K; ++k) {
         if (key == tau) key = 0;
         tau = __reduce_max_sync(kAll, key);
@@ -593,14 +630,23 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       for (int h = 0; h < 2; ++h) {
         const int me = lane + 32 * h;
         if (32 * h >= n) break;
-        v[h] = me < n ? sc.value[me] : -kInf;
+        v[h] = me < n ? sc.value[me] : kInf;
         for (int q = 0; q < n; q += 4) {
           const float4 u = *reinterpret_cast<const float4*>(sc.value + q);
-          rank[h] += (u.x > v[h] || (u.x == v[h] && q < me)) ? 1 : 0;
-          rank[h] += (u.y > v[h] || (u.y == v[h] && q + 1 < me)) ? 1 : 0;
-          rank[h] += (u.z > v[h] || (u.z == v[h] && q + 2 < me)) ? 1 : 0;
-          rank[h] += (u.w > v[h] || (u.w == v[h] && q + 3 < me)) ? 1 : 0;
+          rank[h] += u.x > v[h] ? 1 : 0;
+          rank[h] += u.y > v[h] ? 1 : 0;
+          rank[h] += u.z > v[h] ? 1 : 0;
+          rank[h] += u.w > v[h] ? 1 : 0;
         }
+      }
+      // without equal scores the ranks are 0 .. n - 1 (a lane behind the list has none above its infinity)
+      if (static_cast<int>(__reduce_add_sync(kAll, rank[0] + rank[1])) != n * (n - 1) / 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int me = lane + 32 * h;
+          for (int q = 0; q < me && me < n; ++q) rank[h] += sc.value[q] == v[h] ? 1 : 0;
+        }
+        __syncwarp();
       }
       if (biased) {
         // in order of rank: a chosen one within the error bound of the next is decided in FP64
@@ -614,7 +660,9 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
         for (int h = 0; h < 2; ++h)  // (an infinite score is near to every other)
           if (lane + 32 * h < n && rank[h] < a.K && rank[h] + 1 < n) tie |= !(v[h] - sc.scores[rank[h] + 1] > near);
         if (__any_sync(kAll, tie)) {
-            decide_candidates(a, row, lane, sc, top, n, rank[0], rank[1]);
+          const int2 ranks = decide_candidates<L, NV>(a, row, lane, scratch, top, n);
+          rank[0] = ranks.x;
+          rank[1] = ranks.y;
         }
       }
 #pragma unroll
@@ -662,7 +710,9 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
     reload = true;
   }
   if (GENERAL && close) {
-    slow_choice<L, NV>(a, row, lane, id[0], id[1]);
+    const int2 ids = slow_choice<L, NV>(a, row, lane);
+    id[0] = ids.x;
+    id[1] = ids.y;
     n = kList;
     reload = true;
   }
@@ -833,7 +883,7 @@ __global__ void __launch_bounds__(kRouteThreads<NV, GENERAL>, 1) route_kernel(co
   const mfr_route_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, nwarps = blockDim.x >> 5;
   const int warp = __shfl_sync(kAll, tid >> 5, 0);  // so that the compiler knows it to be the same for the warp
-  const Scratch scratch = scratch_of<NV>(smem + warp * kScratchBytes<NV>);
+  uint8_t* scratch = smem + warp * kScratchBytes<NV>;
   float* bias = reinterpret_cast<float*>(smem + nwarps * kScratchBytes<NV>);
   const OrderSmem o = order_smem(reinterpret_cast<uint8_t*>(bias + (GENERAL ? 32 * NV : 0)), a.E);
   const bool order = a.expert_offsets != nullptr;
