@@ -691,9 +691,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       const float v = warp_max(best);
       if (!(v > -kInf)) break;
       if (biased) {
-        if (k > 0 && !(last - v > 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(v)))) {
-            close = true;
-        }
+        if (k > 0 && !(last - v > 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(v)))) close = true;
         if (k == a.K) break;
         last = v;
       }
@@ -1132,88 +1130,117 @@ __device__ __forceinline__ void store_logits(L* row, int e0, int E, const float 
 //   sigmoid            dx_k = ds_k s_k (1 - s_k)
 //   sigmoid, renorm    dx_k = p_k (1 - s_k) (ds_k - sum_j ds_j p_j)   p = s / sum s
 // Bound by HBM: the logits are read (softmax without renormalisation; else only the chosen ones) and the gradient
-// written once.  16384 tokens of 256 experts, FP32 softmax without renormalisation, 35 MB: 9.4 us in a graph (5.1 us at
+// written once.  16384 tokens of 256 experts, FP32 softmax without renormalisation, 35 MB: 8.5 us in a graph (5.1 us at
 // the copy bandwidth; about 3 us are the launch and the first loads).  With scalar loads and the row read three times it
-// took 15.4 us.
+// took 15.4 us, without the next token's request 9.4.
 template <typename L, int NV>
 __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_constant__ mfr_route_backward_args a) {
   __shared__ __align__(16) float rows[kGradThreads / 32][32 * NV];
   const int lane = threadIdx.x & 31, nwarps = kGradThreads / 32, e0 = lane * NV;
   const int warp = __shfl_sync(kAll, static_cast<int>(threadIdx.x >> 5), 0);  // known to be the same for the warp
   float* buf = rows[warp];
-  for (int e = lane; e < 32 * NV; e += 32) buf[e] = 0.0f;
-  __syncwarp();
+  const bool softmax = a.score == MFR_SCORE_SOFTMAX, dense = softmax && !a.renormalize, two = a.K > 32;
+  if (!dense) {
+    for (int e = lane; e < 32 * NV; e += 32) buf[e] = 0.0f;  // zeros between tokens
+    __syncwarp();
+  }
   pdl_launch_dependents();
   pdl_wait();
-  const bool softmax = a.score == MFR_SCORE_SOFTMAX, dense = softmax && !a.renormalize, two = a.K > 32;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * nwarps + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * nwarps) {
-    const L* row = static_cast<const L*>(a.logits) + t * a.logits_stride;
-    float v[NV];  // the logits, then the gradient
-    if (dense) load_logits<L, NV>(row, e0, a.E, v);
-    int id[2] = {-1, -1};
-    float x[2], d[2], g[2] = {0.0f, 0.0f};
+  // What a token needs, requested while the one before it is worked on.
+  struct Token {
+    float v[NV];  // the logits (dense; with many experts a lane they are loaded when they are needed)
+    int id[2];
+    float d[2];
+  };
+  constexpr bool kAhead = NV <= 8;
+  auto load_row = [&](int64_t t, float (&v)[NV]) {
+    load_logits<L, NV>(static_cast<const L*>(a.logits) + t * a.logits_stride, e0, a.E, v);
+  };
+  auto load = [&](int64_t t, Token& z) {
+    if (dense && kAhead) load_row(t, z.v);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = lane + 32 * i;
-      if ((i == 0 || two) && k < a.K) id[i] = a.expert_ids[t * a.K + k];
-      if (id[i] >= a.E) id[i] = -1;
-      x[i] = id[i] >= 0 ? clean(static_cast<float>(row[id[i]])) : -kInf;
-      d[i] = id[i] >= 0 ? load_any(a.d_scale, t * a.K + k, a.scale_dtype) * a.scale : 0.0f;
+      const bool in = (i == 0 || two) && k < a.K;
+      z.id[i] = in ? a.expert_ids[t * a.K + k] : -1;
+      z.d[i] = in ? load_any(a.d_scale, t * a.K + k, a.scale_dtype) : 0.0f;
+      if (z.id[i] < 0 || z.id[i] >= a.E) {
+        z.id[i] = -1;
+        z.d[i] = 0.0f;
+      }
     }
-    float inner = 0.0f;
-    if (softmax) {
-      float top, inv;
-      if (dense) {
-        float m = v[0], sum = 0.0f;
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * nwarps + warp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * nwarps;
+  if (t >= a.T) return;
+  Token z;
+  load(t, z);
+  for (; t < a.T; t += step) {
+    const L* row = static_cast<const L*>(a.logits) + t * a.logits_stride;
+    if (dense && !kAhead) load_row(t, z.v);
+    Token next;
+    if (t + step < a.T) load(t + step, next);
+    float (&v)[NV] = z.v;
+    const int (&id)[2] = z.id;
+    float d[2] = {z.d[0] * a.scale, z.d[1] * a.scale}, g[2] = {0.0f, 0.0f}, inner = 0.0f;
+    if (dense) {
+      float m = v[0], sum = 0.0f;
 #pragma unroll
-        for (int j = 1; j < NV; ++j) m = fmaxf(m, v[j]);
-        top = warp_max(m);
+      for (int j = 1; j < NV; ++j) m = fmaxf(m, v[j]);
+      const float top = warp_max(m);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          v[j] = !(v[j] > -kInf) ? 0.0f : v[j] == top ? 1.0f : fast_exp2((v[j] - top) * kLog2e);
-          sum += v[j];
-        }
-        sum = warp_sum(sum);
-        inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-      } else {
-        top = warp_max(fmaxf(x[0], x[1]));
+      for (int j = 0; j < NV; ++j) {
+        v[j] = !(v[j] > -kInf) ? 0.0f : v[j] == top ? 1.0f : fast_exp2((v[j] - top) * kLog2e);
+        sum += v[j];
       }
-      float p[2] = {0.0f, 0.0f};
+      store_lane<NV>(buf, lane, v);
+      sum = warp_sum(sum);
+      const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if ((i == 0 || two) && x[i] > -kInf) p[i] = x[i] == top ? 1.0f : expf(x[i] - top);
-      if (!dense) {
-        const float sum = warp_sum(p[0] + p[1]);
-        inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        const float p = id[i] >= 0 ? buf[id[i]] * inv : 0.0f;
+        g[i] = p * d[i];
       }
-      p[0] *= inv;
-      p[1] *= inv;
-      inner = warp_sum(d[0] * p[0] + d[1] * p[1]);
+      inner = warp_sum(g[0] + g[1]) * inv;
+      // the share that every expert has
 #pragma unroll
-      for (int i = 0; i < 2; ++i) g[i] = dense ? p[i] * d[i] : p[i] * (d[i] - inner);
-      inner *= inv;
+      for (int j = 0; j < NV; ++j) v[j] *= -inner;
+      __syncwarp();
+      store_lane<NV>(buf, lane, v);
+      __syncwarp();
     } else {
-      float q[2], l[2] = {0.0f, 0.0f};  // 1 - s, and the weight p (or s)
+      float x[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) q[i] = __fdiv_rn(1.0f, 1.0f + expf(x[i]));
+      for (int i = 0; i < 2; ++i) x[i] = id[i] >= 0 ? clean(static_cast<float>(row[id[i]])) : -kInf;
+      // The weights p over the chosen experts (sigmoid without renormalisation: s), and 1 - s of the sigmoid.  Softmax from
+      // the logits, sigmoid from the logarithms of the scores.
+      float p[2] = {0.0f, 0.0f}, q[2] = {1.0f, 1.0f};
+      if (!softmax) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if ((i == 0 || two) && id[i] >= 0) {
+            q[i] = __fdiv_rn(1.0f, 1.0f + expf(x[i]));
+            if (a.renormalize)
+              x[i] = fminf(x[i], 0.0f) - log1pf(expf(-fabsf(x[i])));
+            else
+              p[i] = __fdiv_rn(1.0f, 1.0f + expf(-x[i]));
+          }
+        }
+      }
       if (a.renormalize) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) l[i] = x[i] > -kInf ? fminf(x[i], 0.0f) - log1pf(expf(-fabsf(x[i]))) : -kInf;
-        const float m = warp_max(fmaxf(l[0], l[1]));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) l[i] = !(l[i] > -kInf) ? 0.0f : l[i] == m ? 1.0f : expf(l[i] - m);
-        const float sum = warp_sum(l[0] + l[1]);
-        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        l[0] *= inv;
-        l[1] *= inv;
-        inner = warp_sum(d[0] * l[0] + d[1] * l[1]);
-      } else {
+        const float m = warp_max(fmaxf(x[0], x[1]));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (id[i] >= 0) l[i] = __fdiv_rn(1.0f, 1.0f + expf(-x[i]));
+          if ((i == 0 || two) && x[i] > -kInf) p[i] = x[i] == m ? 1.0f : expf(x[i] - m);
+        const float sum = warp_sum(p[0] + p[1]);
+        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+        p[0] *= inv;
+        p[1] *= inv;
+        inner = warp_sum(d[0] * p[0] + d[1] * p[1]);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) g[i] = l[i] * q[i] * (d[i] - inner);
+      for (int i = 0; i < 2; ++i) g[i] = p[i] * q[i] * (d[i] - inner);
     }
     // Distinct experts at once; an expert named twice gets its gradients place by place.
     const unsigned same = __match_any_sync(kAll, id[0]);  // (every lane takes part)
@@ -1227,18 +1254,18 @@ __global__ void __launch_bounds__(kGradThreads) route_grad_kernel(const __grid_c
         __syncwarp();
       }
     } else if (id[0] >= 0) {
-      buf[id[0]] = g[0];
+      buf[id[0]] += g[0];
     }
     __syncwarp();
-    float b[NV];
-    load_lane<NV>(buf, lane, b);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = dense ? b[j] - v[j] * inner : b[j];
+    load_lane<NV>(buf, lane, v);
     __syncwarp();
-    if (id[0] >= 0) buf[id[0]] = 0.0f;
-    if (id[1] >= 0) buf[id[1]] = 0.0f;
+    if (!dense) {
+      if (id[0] >= 0) buf[id[0]] = 0.0f;
+      if (id[1] >= 0) buf[id[1]] = 0.0f;
+      __syncwarp();
+    }
     store_logits<L, NV>(static_cast<L*>(a.d_logits) + t * a.d_logits_stride, e0, a.E, v);
-    __syncwarp();
+    z = next;
   }
 }
 
@@ -1246,7 +1273,8 @@ template <typename L, int NV>
 cudaError_t launch_route_backward_nv(const mfr_route_backward_args& a, cudaStream_t stream) {
   const int per = kGradThreads / 32;
   const int64_t want = (static_cast<int64_t>(a.T) + per - 1) / per;
-  const int blocks = static_cast<int>(want < 152 * 8 ? want : 152 * 8);
+  // (so few CTAs that a warp has a next token to request: 8.5 us at 5 an SM, 8.6 at 8 or 16, 10.6 at 4, for the batch above)
+  const int blocks = static_cast<int>(want < 152 * 5 ? want : 152 * 5);
   return launch_pdl<mfr_route_backward_args>(route_grad_kernel<L, NV>, dim3(blocks), kGradThreads, 0, a.flags & MFR_FLAG_PDL, stream, a);
 }
 
