@@ -97,6 +97,10 @@ ROUTES = [  # T, E, K, score, renorm, logits, biased, G, Gk, top2, align
     (40, 64, 20, "sigmoid", True, "fp32", True, 8, 1, True, 16),  # fewer experts in the kept groups than places
     (200, 512, 62, "sigmoid", True, "fp32", True, 4, 2, False, 1),  # nearly as many places as candidates are ranked
     (90, 1024, 40, "softmax", False, "bf16", True, 1, 1, False, 1),
+    (30, 1024, 64, "sigmoid", True, "fp32", True, 1, 1, False, 16),  # one cluster of eight, at the largest sizes
+    (61, 512, 22, "softmax", True, "fp32", False, 1, 1, False, 1),
+    (128, 256, 8, "sigmoid", True, "fp32", True, 8, 4, True, 128),
+    (129, 256, 8, "sigmoid", True, "fp32", True, 8, 4, True, 128),   # and the first batch of two launches
 ]
 
 
