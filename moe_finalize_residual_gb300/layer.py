@@ -416,39 +416,35 @@ def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling
 # Per-head norm and rotation
 # ----------------------------------------------------------------------------------------------------------------
 
-def _heads(t, T, heads, D):
-    """Pointer and strides (those of a dimension of one are never used, whatever torch reports)."""
+def _heads(name, t, index, shape, act, check):
+    """Pointer and strides of a tensor of heads (those of a dimension of one are never used, whatever torch reports)."""
     s = t.stride()
+    if check and not (t.dtype is act and t.get_device() == index and t.shape == shape and s[2] == 1):
+        _check_tensor(name, t, torch.device("cuda", index), shape, act, contiguous=False)
+        raise ValueError(f"the elements of a head must be contiguous in {name}")
+    T, heads, D = shape
     return t.data_ptr(), s[0] if T > 1 else heads * D, s[1] if heads > 1 else D
 
 
-def _check_heads(name, t, dev, shape, act):
-    _check_tensor(name, t, dev, shape, act, contiguous=False)
-    if t.stride(2) != 1:
-        raise ValueError(f"the elements of a head must be contiguous in {name}")
-
-
-def _good_heads(t, index, shape, act):
-    return t.dtype is act and t.get_device() == index and t.shape == shape and t.stride(2) == 1
-
-
-def _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act):
+def _head_shapes(q, k, q_weight, k_weight, positions, inv_freq, check):
+    """Device index, type, and the shapes of the queries and the keys."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, heads, D] and k [T, kv_heads, D]")
-    T, _, D = q.shape
-    if not (index >= 0 and (act is torch.bfloat16 or act is torch.float16) and q.stride(2) == 1
-            and _good_heads(k, index, (T, k.shape[1], D), act)):
-        _check_heads("q", q, q.device, None, (torch.bfloat16, torch.float16))
-        _check_heads("k", k, q.device, (T, k.shape[1], D), act)
-    shape = (D,)
-    if q_weight is not None and not _good(q_weight, index, shape, act):
-        _check_tensor("q_weight", q_weight, q.device, shape, act)
-    if k_weight is not None and not _good(k_weight, index, shape, act):
-        _check_tensor("k_weight", k_weight, q.device, shape, act)
-    if not (positions.dtype is torch.int32 and _good(positions, index, (T,), torch.int32)):
-        _check_tensor("positions", positions, q.device, (T,), (torch.int32, torch.int64))
-    if not _good(inv_freq, index, (inv_freq.numel(),), torch.float32):
-        _check_tensor("inv_freq", inv_freq, q.device, (inv_freq.numel(),), torch.float32)
+    index, act = q.get_device(), q.dtype
+    T, hq, D = shape = tuple(q.shape)
+    if check:
+        if index < 0 or (act is not torch.bfloat16 and act is not torch.float16):
+            _check_tensor("q", q, q.device, None, (torch.bfloat16, torch.float16), contiguous=False)
+        one = (D,)
+        if q_weight is not None and not _good(q_weight, index, one, act):
+            _check_tensor("q_weight", q_weight, q.device, one, act)
+        if k_weight is not None and not _good(k_weight, index, one, act):
+            _check_tensor("k_weight", k_weight, q.device, one, act)
+        if not _good(positions, index, (T,), torch.int32):
+            _check_tensor("positions", positions, q.device, (T,), (torch.int32, torch.int64))
+        if not (inv_freq.dtype is torch.float32 and inv_freq.get_device() == index and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+            _check_tensor("inv_freq", inv_freq, q.device, (inv_freq.numel(),), torch.float32)
+    return index, act, shape, (T, k.shape[1], D)
 
 
 def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -466,28 +462,22 @@ def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     ``positions`` is int32 or int64.  A negative position marks a padding token: its values do not matter, and its
     output rows are left as they were (zeros in an allocated output).  ``q_out`` and ``k_out`` may be ``q`` and ``k``."""
     flags = _PDL if pdl else 0
-    allocated = []
-    index, act = q.get_device(), q.dtype
-    if check:
-        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act)
-    if (q_out is None) != (k_out is None):
-        raise ValueError("q_out and k_out are passed both or neither")
-    T, hq, D = q.shape
-    hk = k.shape[1]
-    if q_out is None:
-        q_out = torch.empty(T, hq, D, dtype=act, device=q.device)
-        k_out = torch.empty(T, hk, D, dtype=act, device=q.device)
-        flags |= _ZERO_PADDING
-        allocated += [q_out, k_out]
-    elif check and not (_good_heads(q_out, index, (T, hq, D), act) and _good_heads(k_out, index, (T, hk, D), act)):
-        _check_heads("q_out", q_out, q.device, (T, hq, D), act)
-        _check_heads("k_out", k_out, q.device, (T, hk, D), act)
     if positions.dtype is torch.int64:
         flags |= _POSITIONS_64
-    args = _pack_head_norm(T, hq, hk, D, 2 * inv_freq.numel(), _choice(ROTARY_STYLE, "style", style), DTYPE[act], eps,
-                           rotary_scale, *_heads(q, T, hq, D), *_heads(k, T, hk, D), *_heads(q_out, T, hq, D),
-                           *_heads(k_out, T, hk, D), 0, 0, 0, 0, 0, 0, _ptr(q_weight), _ptr(k_weight),
-                           positions.data_ptr(), inv_freq.data_ptr(), 0, 0, 0, 0, flags)
+    allocated = []
+    index, act, sq, sk = _head_shapes(q, k, q_weight, k_weight, positions, inv_freq, check)
+    if q_out is None and k_out is None:
+        q_out = torch.empty(sq, dtype=act, device=q.device)
+        k_out = torch.empty(sk, dtype=act, device=q.device)
+        flags |= _ZERO_PADDING
+        allocated += [q_out, k_out]
+    elif q_out is None or k_out is None:
+        raise ValueError("q_out and k_out are passed both or neither")
+    args = _pack_head_norm(sq[0], sq[1], sk[1], sq[2], 2 * inv_freq.numel(), _choice(ROTARY_STYLE, "style", style), DTYPE[act],
+                           eps, rotary_scale, *_heads("q", q, index, sq, act, check), *_heads("k", k, index, sk, act, check),
+                           *_heads("q_out", q_out, index, sq, act, check), *_heads("k_out", k_out, index, sk, act, check),
+                           0, 0, 0, 0, 0, 0, _ptr(q_weight), _ptr(k_weight), positions.data_ptr(), inv_freq.data_ptr(),
+                           0, 0, 0, 0, flags)
     _enqueue(_lib.moe_head_norm_rotary, args, index, stream, allocated)
     return q_out, k_out
 
@@ -514,54 +504,46 @@ def head_norm_rotary_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: t
     gradients, and their rows of ``d_q`` and ``d_k`` are set to zero.  ``d_q`` and ``d_k`` may be ``d_q_out`` and
     ``d_k_out``, or ``q`` and ``k``.  ``workspace`` must not be shared by calls that may run at the same time."""
     flags = _PDL if pdl else 0
-    allocated = []
-    index, act = q.get_device(), q.dtype
-    if check:
-        _check_head_norm(q, k, q_weight, k_weight, positions, inv_freq, index, act)
-    if (d_q is None) != (d_k is None):
-        raise ValueError("d_q and d_k are passed both or neither")
-    dev = q.device
-    T, hq, D = q.shape
-    hk = k.shape[1]
-    if d_q is None:
-        d_q = torch.empty(T, hq, D, dtype=act, device=dev)
-        d_k = torch.empty(T, hk, D, dtype=act, device=dev)
-        allocated += [d_q, d_k]
-    if want_weights:
-        if d_q_weight is None and q_weight is not None:
-            d_q_weight = torch.empty(D, dtype=torch.float32, device=dev)
-            allocated.append(d_q_weight)
-        if d_k_weight is None and k_weight is not None:
-            d_k_weight = torch.empty(D, dtype=torch.float32, device=dev)
-            allocated.append(d_k_weight)
-    space = 0
-    if d_q_weight is not None or d_k_weight is not None:
-        if workspace is not None:
-            if check:
-                _check_tensor("workspace", workspace, dev, None, torch.uint8)
-            space = workspace.numel()
-        else:
-            space = _head_space(T, hq, hk, D)
-            workspace = torch.empty(space, dtype=torch.uint8, device=dev)
-            allocated.append(workspace)
-    if check:
-        sq, sk = (T, hq, D), (T, hk, D)
-        if not (_good_heads(d_q_out, index, sq, act) and _good_heads(d_k_out, index, sk, act)
-                and _good_heads(d_q, index, sq, act) and _good_heads(d_k, index, sk, act)):
-            _check_heads("d_q_out", d_q_out, dev, sq, act)
-            _check_heads("d_k_out", d_k_out, dev, sk, act)
-            _check_heads("d_q", d_q, dev, sq, act)
-            _check_heads("d_k", d_k, dev, sk, act)
-        if d_q_weight is not None and not _good(d_q_weight, index, (D,), torch.float32):
-            _check_tensor("d_q_weight", d_q_weight, dev, (D,), torch.float32)
-        if d_k_weight is not None and not _good(d_k_weight, index, (D,), torch.float32):
-            _check_tensor("d_k_weight", d_k_weight, dev, (D,), torch.float32)
     if positions.dtype is torch.int64:
         flags |= _POSITIONS_64
-    args = _pack_head_norm(T, hq, hk, D, 2 * inv_freq.numel(), _choice(ROTARY_STYLE, "style", style), DTYPE[act], eps,
-                           rotary_scale, *_heads(q, T, hq, D), *_heads(k, T, hk, D), *_heads(d_q, T, hq, D),
-                           *_heads(d_k, T, hk, D), *_heads(d_q_out, T, hq, D), *_heads(d_k_out, T, hk, D),
+    allocated = []
+    index, act, sq, sk = _head_shapes(q, k, q_weight, k_weight, positions, inv_freq, check)
+    T, hq, D = sq
+    if d_q is None and d_k is None:
+        d_q = torch.empty(sq, dtype=act, device=q.device)
+        d_k = torch.empty(sk, dtype=act, device=q.device)
+        allocated += [d_q, d_k]
+    elif d_q is None or d_k is None:
+        raise ValueError("d_q and d_k are passed both or neither")
+    if want_weights:
+        if d_q_weight is None and q_weight is not None:
+            d_q_weight = torch.empty(D, dtype=torch.float32, device=q.device)
+            allocated.append(d_q_weight)
+        if d_k_weight is None and k_weight is not None:
+            d_k_weight = torch.empty(D, dtype=torch.float32, device=q.device)
+            allocated.append(d_k_weight)
+    if check:
+        one = (D,)
+        if d_q_weight is not None and not _good(d_q_weight, index, one, torch.float32):
+            _check_tensor("d_q_weight", d_q_weight, q.device, one, torch.float32)
+        if d_k_weight is not None and not _good(d_k_weight, index, one, torch.float32):
+            _check_tensor("d_k_weight", d_k_weight, q.device, one, torch.float32)
+    space, at = 0, 0
+    if d_q_weight is not None or d_k_weight is not None:
+        if workspace is None:
+            space = _head_space(T, hq, sk[1], D)
+            workspace = torch.empty(space, dtype=torch.uint8, device=q.device)
+            allocated.append(workspace)
+        else:
+            if check:
+                _check_tensor("workspace", workspace, q.device, None, torch.uint8)
+            space = workspace.numel()
+        at = workspace.data_ptr()
+    args = _pack_head_norm(T, hq, sk[1], D, 2 * inv_freq.numel(), _choice(ROTARY_STYLE, "style", style), DTYPE[act], eps,
+                           rotary_scale, *_heads("q", q, index, sq, act, check), *_heads("k", k, index, sk, act, check),
+                           *_heads("d_q", d_q, index, sq, act, check), *_heads("d_k", d_k, index, sk, act, check),
+                           *_heads("d_q_out", d_q_out, index, sq, act, check), *_heads("d_k_out", d_k_out, index, sk, act, check),
                            _ptr(q_weight), _ptr(k_weight), positions.data_ptr(), inv_freq.data_ptr(), _ptr(d_q_weight),
-                           _ptr(d_k_weight), workspace.data_ptr() if space else 0, space, flags)
+                           _ptr(d_k_weight), at, space, flags)
     _enqueue(_lib.moe_head_norm_rotary_backward, args, index, stream, allocated)
     return d_q, d_k, d_q_weight, d_k_weight
