@@ -173,6 +173,10 @@ __device__ __forceinline__ void merge_top2(F& a, F& b, F a2, F b2) {
   b = lo > hi ? lo : hi;
 }
 
+// How far apart two FP32 choice scores must lie for their order to be that of the exact ones: each holds a score that is
+// `err` off and the rounding of its bias's addition, 2^-24 of it (twice that here).
+__device__ __forceinline__ float near_of(float err, float v, float w) { return __fmaf_rn(1.2e-7f, fabsf(v) + fabsf(w), 2.0f * err); }
+
 // The group score of a group's two best choice scores (-inf: none).
 template <typename F>
 __device__ __forceinline__ F group_score(F best, F second, bool top2) {
@@ -650,7 +654,6 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       }
       if (biased) {
         // in order of rank: a chosen one within the error bound of the next is decided in FP64
-        const float near = 2.0f * err + 2.4e-7f * fmaxf(fabsf(most), fabsf(least));
         bool tie = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -658,7 +661,10 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h)  // (an infinite score is near to every other)
-          if (lane + 32 * h < n && rank[h] < a.K && rank[h] + 1 < n) tie |= !(v[h] - sc.scores[rank[h] + 1] > near);
+          if (lane + 32 * h < n && rank[h] < a.K && rank[h] + 1 < n) {
+            const float next = sc.scores[rank[h] + 1];
+            tie |= !(v[h] - next > near_of(err, v[h], next));
+          }
         if (__any_sync(kAll, tie)) {
           const int2 ranks = decide_candidates<L, NV>(a, row, lane, scratch, top, n);
           rank[0] = ranks.x;
@@ -691,7 +697,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       const float v = warp_max(best);
       if (!(v > -kInf)) break;
       if (biased) {
-        if (k > 0 && !(last - v > 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(v)))) close = true;
+        if (k > 0 && !(last - v > near_of(err, last, v))) close = true;
         if (k == a.K) break;
         last = v;
       }
