@@ -576,7 +576,12 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
     }
     const float most = unordered(first);
     // fewer lanes than that have any: all experts that can be taken are candidates
-    float least = tau > ordered(-kInf) ? unordered(tau) : -3.402823466e38f;
+    constexpr float kLowest = -3.402823466e38f;
+    float least = tau > ordered(-kInf) ? unordered(tau) : kLowest;
+    // An expert just below that one may come before it in 64 bits: with a bias the cut lies clear of the K-th best by
+    // near_of and a little for this subtraction's rounding.
+    if (biased) least = fmaxf(least - __fmaf_rn(3.6e-7f, fabsf(least), 2.5f * err), kLowest);
+    bool bisected = false;
     unsigned mask = 0;
     auto select = [&]() {
       mask = 0;
@@ -614,6 +619,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       }
       before = scan(select());
       if (n <= a.K) n = kList + 1;  // more equal scores than the list holds
+      bisected = true;
     }
     if (n <= kList) {
       // by expert index, so that among equal scores the earlier candidate is the lower expert
@@ -664,8 +670,11 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
           if (lane + 32 * h < n && rank[h] < a.K && rank[h] + 1 < n) {
             const float next = sc.scores[rank[h] + 1];
             tie |= !(v[h] - next > near_of(err, v[h], next));
+            // (this cut was taken where it fell: what lies below it may have to be looked at too)
+            if (bisected && rank[h] == a.K - 1) close = !(v[h] - least > near_of(err, v[h], least));
           }
-        if (__any_sync(kAll, tie)) {
+        close = __any_sync(kAll, close);
+        if (!close && __any_sync(kAll, tie)) {
           const int2 ranks = decide_candidates<L, NV>(a, row, lane, scratch, top, n);
           rank[0] = ranks.x;
           rank[1] = ranks.y;
@@ -673,7 +682,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (lane + 32 * h < n && rank[h] < a.K) {
+        if (!close && lane + 32 * h < n && rank[h] < a.K) {
           id[h] = sc.expert[lane + 32 * h];
           place[h] = rank[h];
         }

@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+import layer_reference as ref
+
 pytestmark = pytest.mark.gpu
 
 
@@ -15,6 +17,14 @@ def gen(seed):
     g = torch.Generator()
     g.manual_seed(seed)
     return g
+
+
+def wrong_tokens(mfr, x, K, score, bias, G=1, Gk=1, top2=False):
+    """How many tokens get other ids than the definition in 64 bits gives."""
+    got = mfr.moe_route(x.cuda(), K, score=score, bias=bias.cuda(), num_groups=G, topk_groups=Gk,
+                        group_score="top2" if top2 else "max", order=False).expert_ids.cpu().numpy()
+    want = ref.choose(x.double().numpy(), K, score, bias.double().numpy(), G, Gk, top2)[0]
+    return int((got != want).any(1).sum())
 
 
 def graph_time(f, launches=10):
@@ -48,3 +58,56 @@ def test_route_is_not_decided_again_where_few_lanes_hold_an_expert(mfr, score):
     two, four = (graph_time(lambda: mfr.moe_route(x, 8, score=score, bias=bias, num_groups=8, topk_groups=n,
                                                   group_score="top2", order=False)) for n in (2, 4))
     assert two < 2.5 * four, f"{two:.1f} us with 2 groups kept, {four:.1f} with 4"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 32, 64, 128, 256, 512, 896])
+@pytest.mark.parametrize("level", [0.0, 1.0, 0.5, -0.25])
+def test_route_scores_near_one_another_without_groups(mfr, score, E, level):
+    """Biases that level a token's scores to within an FP32 rounding: the candidates' cut must not lose an expert that
+    64 bits put first.  Token 0 of each draw is level (1.0 stands for 1 / E), token 1 is not."""
+    level = 1.0 / E if level == 1.0 else level
+    wrong = {}
+    for seed in range(12):
+        x = torch.randn(2, E, generator=gen(100 * E + seed))
+        s = ref.choose(x[:1].double().numpy(), 1, score)[1][0]
+        bias = torch.from_numpy(level - s).float()
+        for K in (1, 2, 8, 22, 33):
+            if K <= E:
+                n = wrong_tokens(mfr, x, K, score, bias)
+                wrong[K] = wrong.get(K, 0) + n
+    assert not any(wrong.values()), f"tokens with other ids, by K: {wrong}"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 4), (256, 8), (512, 8), (900, 4), (96, 3)])
+@pytest.mark.parametrize("top2", [False, True])
+@pytest.mark.parametrize("level", [0.0, 0.5])
+def test_route_scores_near_one_another_in_groups(mfr, score, E, G, top2, level):
+    wrong = {}
+    for seed in range(6):
+        x = torch.randn(2, E, generator=gen(7 * E + seed))
+        s = ref.choose(x[:1].double().numpy(), 1, score)[1][0]
+        bias = torch.from_numpy(level - s).float()
+        bias[: E // 2] += 0.125 * (seed % 2)  # every other draw: the groups' border lies elsewhere than the experts'
+        for K, Gk in ((2, 1), (8, 2), (8, G - 1), (20, G)):
+            n = wrong_tokens(mfr, x, K, score, bias, G, Gk, top2)
+            wrong[K, Gk] = wrong.get((K, Gk), 0) + n
+    assert not any(wrong.values()), f"tokens with other ids, by K and kept groups: {wrong}"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,few", [(256, 40), (512, 70), (1024, 90), (128, 30)])
+def test_route_few_near_scores_among_many(mfr, score, E, few):
+    """Only some experts are level; they lie in few lanes, so that the lanes' best say little about the cut."""
+    wrong = {}
+    for seed in range(8):
+        x = torch.randn(2, E, generator=gen(E + seed))
+        s = ref.choose(x[:1].double().numpy(), 1, score)[1][0]
+        bias = torch.from_numpy(-1.0 - s).float()
+        bias[:few] += 1.25
+        bias[few: 2 * few: 2] += 1.25 + 2.0 ** -20 * torch.arange(len(bias[few: 2 * few: 2])).float() / few
+        for K in (2, 8, 20, 40):
+            n = wrong_tokens(mfr, x, K, score, bias)
+            wrong[K] = wrong.get(K, 0) + n
+    assert not any(wrong.values()), f"tokens with other ids, by K: {wrong}"
