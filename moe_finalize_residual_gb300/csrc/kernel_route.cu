@@ -309,23 +309,25 @@ __device__ __forceinline__ Scratch scratch_of(uint8_t* base) {
   return s;
 }
 
-// The groups whose scores lie within `tol` of the border between kept and dropped ones, decided again in FP64.
-// sc.scores holds the values that the groups compare, lane g group g's score and second best value; `in`: whether
-// it is kept.  Returns the groups kept, or 0 when too many values matter.
+// The groups whose scores may lie on either side of the border between kept and dropped ones, decided again in FP64:
+// kept ones that may be as low as the highest a dropped one may be (`highest_out`), and dropped ones that may be as high
+// as the lowest a kept one may be (`lowest_in`).  sc.scores holds the values that the groups compare, lane g group g's
+// score, its error bound `slack` and its second best value; `in`: whether it is kept.  Returns the groups kept, or 0 when
+// too many values matter.
 template <typename L, int NV>
 __device__ __noinline__ unsigned decide_groups(const RouteParams& p, const L* row, int lane, uint8_t* scratch, float top, float mine,
-                                               float second, bool in, float worst, float best_out, float tol) {
+                                               float second, float slack, bool in, float lowest_in, float highest_out) {
   const Scratch sc = scratch_of<NV>(scratch);
   const mfr_route_args& a = p.a;
   const bool top2 = a.group_score == MFR_GROUP_TOP2, biased = a.bias != nullptr;
   const bool here = lane < a.num_groups && mine > -kInf;
   const unsigned kept = __ballot_sync(kAll, in);
-  const unsigned band = __ballot_sync(kAll, here && !(in ? mine - best_out > tol : worst - mine > tol));
+  const unsigned band = __ballot_sync(kAll, here && !(in ? mine - slack > highest_out : lowest_in > mine + slack));
   // the values that may be among a group's two best
   int n = 0, begin = 0, end = 0;
   for (unsigned m = band; m; m &= m - 1) {
     const int g = __ffs(m) - 1;
-    const float least = fmaxf(__shfl_sync(kAll, top2 ? second : mine, g) - tol, -3.402823466e38f);
+    const float least = fmaxf(__shfl_sync(kAll, (top2 ? second : mine) - 2.0f * slack, g), -3.402823466e38f);
     if (lane == g) begin = n;
     for (int i0 = 0; i0 < p.group_size; i0 += 32) {
       const int i = i0 + lane;
@@ -448,8 +450,15 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
       __syncwarp();
     };
     float mine = -kInf, second = -kInf;  // a group's score and second best value: its lanes hold them, or lane g group g's
-    float worst = -kInf, best_out = -kInf;  // the kept group nearest to a dropped one, and that one
-    bool on = false;                        // the lane's group is kept, or group `lane` is
+    // How far a group's FP32 score may be from the exact one: each value it adds is `err` off and has the rounding of its
+    // bias's addition, 2^-24 of that value (and not of the sum, where the two cancel); the rest is for the sum's rounding
+    // and for that of the comparisons.
+    float slack = 0.0f;
+    auto slack_of = [&](float best, float second) {
+      const float size = top2 && second > -kInf ? fabsf(best) + fabsf(second) : fabsf(best);
+      return (top2 ? 2.0f : 1.0f) * err + 2.4e-7f * fminf(size, 3.402823466e38f);
+    };
+    bool on = false;                     // the lane's group is kept, or group `lane` is
     const int w = p.width_log2;
     if (w >= 0) {
       if (sums) {
@@ -474,20 +483,17 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
         if (top2) second = fmaxf(fminf(mine, m2), fmaxf(second, __shfl_xor_sync(kAll, second, o)));
         mine = fmaxf(mine, m2);
       }
+      slack = slack_of(mine, second);
       if (top2) mine = group_score(mine, second, true);
       // the best group again and again; among equal ones the lowest lane's
       const uint32_t key = ordered(mine + 0.0f);
       const uint32_t none = ordered(-kInf);
-      uint32_t last = none;
       for (int i = 0; i < a.topk_groups; ++i) {
         const uint32_t m = __reduce_max_sync(kAll, on ? 0 : key);
         if (m <= none) break;
         const int first = __ffs(__ballot_sync(kAll, !on && key == m)) - 1;
         on = on || (lane >> w) == (first >> w);
-        last = m;
       }
-      worst = unordered(last);
-      best_out = unordered(max(none, __reduce_max_sync(kAll, on ? 0 : key)));
     } else {
       share_values();
       if (lane < a.num_groups) {
@@ -496,6 +502,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
           second = fmaxf(second, fminf(mine, v));
           mine = fmaxf(mine, v);
         }
+        slack = slack_of(mine, second);
         mine = group_score(mine, second, top2);
       }
       __syncwarp();
@@ -505,19 +512,18 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
         rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
       }
       on = rank < a.topk_groups && mine > -kInf;
-      worst = -warp_max(on ? -mine : -kInf);
-      best_out = warp_max(on ? -kInf : mine);
     }
     unsigned kept = 0;  // by group
     bool by_group = w < 0;
     if (top2 || biased) {
-      const float tol = (top2 ? 4.0f : 2.0f) * err + 2.4e-7f * (fabsf(worst) + fabsf(best_out));
-      if (__any_sync(kAll, best_out > -kInf && !(worst - best_out > tol))) {  // (the same for all lanes)
+      const float lowest_in = -warp_max(on ? slack - mine : -kInf), highest_out = warp_max(on ? -kInf : mine + slack);
+      if (__any_sync(kAll, highest_out > -kInf && !(lowest_in > highest_out))) {  // (the same for all lanes)
         if (w >= 0) {
           // group g's to lane g
           const int from = (lane << w) & 31;
           mine = __shfl_sync(kAll, mine, from);
           second = __shfl_sync(kAll, second, from);
+          slack = __shfl_sync(kAll, slack, from);
           on = __shfl_sync(kAll, on, from);
           if (lane >= a.num_groups) {
             mine = -kInf;
@@ -525,7 +531,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int64_t t, flo
           }
           share_values();
         }
-        kept = decide_groups<L, NV>(p, row, lane, scratch, top, mine, second, on, worst, best_out, tol);
+        kept = decide_groups<L, NV>(p, row, lane, scratch, top, mine, second, slack, on, lowest_in, highest_out);
         close = kept == 0;
         if (w >= 0) on = (kept >> (lane >> w)) & 1;
         by_group = false;

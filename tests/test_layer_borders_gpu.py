@@ -1,4 +1,5 @@
 """The operators around the finalize where a decision between experts is close."""
+import numpy as np
 import pytest
 import torch
 
@@ -111,3 +112,27 @@ def test_route_few_near_scores_among_many(mfr, score, E, few):
             n = wrong_tokens(mfr, x, K, score, bias)
             wrong[K] = wrong.get(K, 0) + n
     assert not any(wrong.values()), f"tokens with other ids, by K: {wrong}"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [8.0, 1000.0, 30000.0])
+@pytest.mark.parametrize("E,G,Gk,K", [(64, 32, 16, 8), (16, 8, 3, 2), (96, 32, 5, 4), (512, 16, 4, 8), (600, 24, 7, 6)])
+def test_route_group_sums_that_cancel(mfr, score, size, E, G, Gk, K):
+    """A group's two best scores near +size and -size: their sum is small, the roundings of the two are not."""
+    wrong = 0
+    for seed in range(20):
+        g = gen(E + seed)
+        x = torch.randn(3, E, generator=g)
+        s = ref.choose(x[:1].double().numpy(), 1, score)[1][0].reshape(G, E // G)
+        bias = np.full((G, E // G), -10.0 * size)  # the third and later ones of a group do not count
+        bias[:, 0] = size * (1 + torch.rand(G, generator=g).double().numpy() / 16)
+        bias[:, 0] = np.float32(bias[:, 0])
+        bias[:, 1] = 0.25 - s[:, 0] - s[:, 1] - bias[:, 0]  # level sums, to half a step of the second bias
+        wrong += wrong_tokens(mfr, x, K, score, torch.from_numpy(bias.reshape(-1)).float(), G, Gk, True)
+    assert wrong == 0, f"{wrong} of 60 tokens got other ids"
+
+
+def test_route_random_groups_of_two_whose_scores_cancel(mfr):
+    x = torch.randn(50000, 16, generator=gen(3))
+    bias = torch.tensor([1000.0, -1000.0]).repeat(8) + 0.1 * torch.randn(16, generator=gen(4))
+    assert wrong_tokens(mfr, x, 2, "sigmoid", bias, 8, 3, True) == 0
