@@ -177,10 +177,10 @@ __device__ __forceinline__ void merge_top2(F& a, F& b, F a2, F b2) {
 // `err` off and the rounding of its bias's addition, 2^-24 of it (twice that here).
 __device__ __forceinline__ float near_of(float err, float v, float w) { return __fmaf_rn(1.2e-7f, fabsf(v) + fabsf(w), 2.0f * err); }
 
-// The group score of a group's two best choice scores (-inf: none).
-template <typename F>
-__device__ __forceinline__ F group_score(F best, F second, bool top2) {
-  return top2 && second > static_cast<F>(-kInf) ? best + second : best;
+// The FP32 group score of a group's two best choice scores (-inf: none).  A sum that leaves FP32 stays at its ends: it is
+// finite in 64 bits, so the group can be kept, and the error bound sends what lies near to 64 bits.
+__device__ __forceinline__ float group_score(float best, float second, bool top2) {
+  return top2 && second > -kInf ? fminf(fmaxf(best + second, -3.402823466e38f), 3.402823466e38f) : best;
 }
 
 // ---------------------------------------------------------------------------------------------------

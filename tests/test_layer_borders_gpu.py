@@ -7,6 +7,8 @@ import layer_reference as ref
 
 pytestmark = pytest.mark.gpu
 
+FLOAT_MAX = torch.finfo(torch.float32).max
+
 
 @pytest.fixture(scope="module")
 def mfr():
@@ -136,3 +138,22 @@ def test_route_random_groups_of_two_whose_scores_cancel(mfr):
     x = torch.randn(50000, 16, generator=gen(3))
     bias = torch.tensor([1000.0, -1000.0]).repeat(8) + 0.1 * torch.randn(16, generator=gen(4))
     assert wrong_tokens(mfr, x, 2, "sigmoid", bias, 8, 3, True) == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,Gk,K", [(64, 8, 4, 8), (64, 8, 8, 40), (60, 4, 2, 10), (256, 8, 4, 8), (200, 8, 3, 60)])
+@pytest.mark.parametrize("end", [-1.0, 1.0])
+@pytest.mark.parametrize("top2", [False, True])
+def test_route_group_sums_past_the_largest_number(mfr, score, E, G, Gk, K, end, top2):
+    """Biases at either end of FP32 on some groups, as masks use them: a sum of two is finite in 64 bits."""
+    wrong = 0
+    for seed in range(8):
+        g = gen(E + seed)
+        x = torch.randn(20, E, generator=g)
+        bias = 0.1 * torch.randn(E, generator=g)
+        off = torch.rand(E, generator=g) < 0.3
+        off.view(G, E // G)[torch.randperm(G, generator=g)[: G - (seed % 3)]] = True  # all groups but 0, 1 or 2
+        bias[off] = end * FLOAT_MAX
+        bias[off & (torch.rand(E, generator=g) < 0.5)] = end * FLOAT_MAX * 0.75
+        wrong += wrong_tokens(mfr, x, K, score, bias, G, Gk, top2)
+    assert wrong == 0, f"{wrong} of 160 tokens got other ids"
