@@ -12,6 +12,7 @@ import ctypes
 import dataclasses
 import functools
 import struct
+import sys
 from typing import Optional, Tuple
 
 import torch
@@ -69,22 +70,31 @@ class _CHeadNorm(ctypes.Structure):
                 ("workspace_bytes", _L), ("flags", _U)]
 
 
-_CODES = {_I: "i", _L: "q", _F: "f", _P: "P", _U: "I"}
+_CODES = {_I: "i", _L: "q", _F: "f", _P: "Q", _U: "I"}
 
 
 def _packer(cls):
-    """Packs a structure's fields, nested ones in line: several times faster than filling a ctypes structure.  The
-    trailing "0q" pads to the structure's size (every one holds a 64-bit field)."""
-    def codes(c):
-        return "".join(codes(t) if issubclass(t, ctypes.Structure) else _CODES[t] for _, t in c._fields_)
+    """Packs a structure's fields, nested ones in line: several times faster than filling a ctypes structure.  The format
+    is the standard one, with the padding spelled out: the native one turns a float beyond FP32 into an infinity."""
+    def fields(c, at):
+        for name, t in c._fields_:
+            offset = at + getattr(c, name).offset
+            if issubclass(t, ctypes.Structure):
+                yield from fields(t, offset)
+            else:
+                yield offset, t
 
-    packer = struct.Struct("@" + codes(cls) + "0q")
-    assert packer.size == ctypes.sizeof(cls), cls
+    codes, end = "<", 0
+    for offset, t in fields(cls, 0):
+        codes += "x" * (offset - end) + _CODES[t]
+        end = offset + ctypes.sizeof(t)
+    packer = struct.Struct(codes + "x" * (ctypes.sizeof(cls) - end))
+    assert packer.size == ctypes.sizeof(cls) and sys.byteorder == "little", cls
 
     def pack(*values):
         try:
             return packer.pack(*values)
-        except struct.error as e:
+        except (struct.error, OverflowError) as e:  # (OverflowError: a float beyond FP32)
             raise ValueError(f"an argument is not a number of its range: {e}") from None
 
     return pack
