@@ -128,7 +128,15 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _size(n: int) -> int:
+_INTS = {n: struct.Struct("<%di" % n).pack for n in (3, 4)}
+
+
+def _size(query, *args) -> int:
+    try:
+        _INTS[len(args)](*args)  # (ctypes would keep the low 32 bits of a larger number)
+    except struct.error as e:
+        raise ValueError(f"a size is not a 32-bit integer: {e}") from None
+    n = query(*args)
     if n < 0:
         _raise_status(int(n))
     return int(n)
@@ -200,12 +208,12 @@ class Routing:
 
 def moe_route_max_rows(T: int, K: int, E: int, row_align: int = 1) -> int:
     """The most rows that T*K routes fill when every expert's rows are padded to a multiple of ``row_align``."""
-    return _size(_lib.moe_route_max_rows(T, K, E, row_align))
+    return _size(_lib.moe_route_max_rows, T, K, E, row_align)
 
 
 def moe_route_workspace_bytes(T: int, K: int, E: int) -> int:
     """Workspace of ``moe_route`` with the expert order (0 for small batches)."""
-    return _size(_lib.moe_route_workspace_bytes(T, K, E))
+    return _size(_lib.moe_route_workspace_bytes, T, K, E)
 
 
 _route_space = functools.lru_cache(maxsize=1024)(lambda T, K, E: moe_route_workspace_bytes(T, K, E))
@@ -494,7 +502,7 @@ def head_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
 
 def head_norm_rotary_workspace_bytes(T: int, q_heads: int, k_heads: int, D: int) -> int:
     """Workspace of ``head_norm_rotary_backward`` when a weight gradient is asked."""
-    return _size(_lib.moe_head_norm_rotary_workspace_bytes(T, q_heads, k_heads, D))
+    return _size(_lib.moe_head_norm_rotary_workspace_bytes, T, q_heads, k_heads, D)
 
 
 _head_space = functools.lru_cache(maxsize=1024)(lambda *sizes: head_norm_rotary_workspace_bytes(*sizes))

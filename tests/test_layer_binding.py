@@ -57,3 +57,14 @@ def test_numbers_beyond_their_type_are_refused(mfr, pack, bad):
         if t is mfr.layer._F:
             with pytest.raises(ValueError):
                 getattr(mfr.layer, pack)(*good[:i], bad, *good[i + 1:])
+
+
+@pytest.mark.parametrize("query,good", [("moe_route_max_rows", (4, 2, 8, 16)), ("moe_route_workspace_bytes", (4000, 2, 8)),
+                                        ("head_norm_rotary_workspace_bytes", (40, 4, 2, 64))])
+def test_sizes_beyond_32_bits_are_refused(mfr, query, good):
+    f = getattr(mfr, query)
+    assert f(*good) > 0
+    for i in range(len(good)):
+        for bad in (good[i] + 2 ** 32, good[i] - 2 ** 32, 2 ** 31, 10 ** 30, 2.0, None):
+            with pytest.raises(ValueError):
+                f(*good[:i], bad, *good[i + 1:])
