@@ -150,8 +150,12 @@ def _choice(table, name, value):
 
 
 def _good(t, index, shape, dtype):
-    """A contiguous tensor of this shape and type on this device."""
-    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+    """A contiguous tensor of this shape (None: any) and type (None: any of DTYPE) on this device."""
+    try:
+        return ((t.dtype is dtype or dtype is None and t.dtype in DTYPE) and t.get_device() == index
+                and (shape is None or t.shape == shape) and t.is_contiguous())
+    except AttributeError:  # None, or no tensor
+        return False
 
 
 def _check_tensor(name, t, device, shape, dtypes, contiguous=True):
@@ -267,10 +271,10 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
         shape = (T, top_k)
         if bias is not None and not _good(bias, index, (E,), torch.float32):
             _check_tensor("bias", bias, logits.device, (E,), torch.float32)
-        if not (_good(ids, index, shape, torch.int32) and _good(scales, index, shape, scales.dtype) and scales.dtype in DTYPE):
+        if not (_good(ids, index, shape, torch.int32) and _good(scales, index, shape, None)):
             _check_tensor("expert_ids", ids, logits.device, shape, torch.int32)
             _check_tensor("expert_scale", scales, logits.device, shape, DTYPE)
-        if ordered and not (_good(perm, index, shape, torch.int32) and _good(rows, index, rows.shape, torch.int32)
+        if ordered and not (_good(perm, index, shape, torch.int32) and _good(rows, index, None, torch.int32)
                             and _good(offsets, index, (E + 1,), torch.int32) and _good(counts, index, (E,), torch.int32)):
             _check_tensor("perm_idx", perm, logits.device, shape, torch.int32)
             _check_tensor("row_route", rows, logits.device, None, torch.int32)
@@ -320,7 +324,7 @@ def moe_route_backward(d_scale: torch.Tensor, logits: torch.Tensor, expert_ids: 
         dev, shape = logits.device, (T, K)
         if index < 0 or act not in DTYPE:
             _check_tensor("logits", logits, dev, None, DTYPE, contiguous=False)
-        if not (_good(expert_ids, index, shape, torch.int32) and _good(d_scale, index, shape, d_scale.dtype) and d_scale.dtype in DTYPE):
+        if not (_good(expert_ids, index, shape, torch.int32) and _good(d_scale, index, shape, None)):
             _check_tensor("expert_ids", expert_ids, dev, shape, torch.int32)
             _check_tensor("d_scale", d_scale, dev, shape, DTYPE)
         _check_tensor("out", out, dev, (T, E), act, contiguous=False)
@@ -356,7 +360,7 @@ def moe_dispatch(x: torch.Tensor, perm_idx: torch.Tensor, num_rows: Optional[int
     length of ``row_route``.
 
     The gradient to ``x`` is ``moe_finalize_routed([Partial(d_rows, perm_idx)])``."""
-    if x.dim() != 2 or perm_idx.dim() != 2:
+    if perm_idx is None or x.dim() != 2 or perm_idx.dim() != 2:
         raise ValueError("x must be [T, n] and perm_idx [T, K]")
     index = x.get_device()
     T, n = x.shape
@@ -396,7 +400,7 @@ def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling
     outputs overlap no input.  With ``row_route`` the rows of no route get zeros; without it they are left as they
     were, or zeros in an allocated output."""
     x, perm, scale = partial.gemm2_out, partial.perm_idx, partial.expert_scale
-    if d_out.dim() != 2 or perm.dim() != 2 or x.dim() != 2:
+    if perm is None or x is None or d_out.dim() != 2 or perm.dim() != 2 or x.dim() != 2:
         raise ValueError("d_out must be [T, H], gemm2_out [rows, H] and perm_idx [T, K]")
     T, H = d_out.shape
     K, rows = perm.shape[1], x.shape[0]
@@ -415,7 +419,7 @@ def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling
         if not (_good(x, index, (rows, H), act) and _good(perm, index, shape, torch.int32)):
             _check_tensor("gemm2_out", x, dev, (rows, H), act)
             _check_tensor("perm_idx", perm, dev, shape, torch.int32)
-        if scale is not None and not (sdt in DTYPE and _good(scale, index, shape, sdt)):
+        if scale is not None and not _good(scale, index, shape, None):
             _check_tensor("expert_scale", scale, dev, shape, DTYPE)
         if row_route is not None and not _good(row_route, index, (rows,), torch.int32):
             _check_tensor("row_route", row_route, dev, (rows,), torch.int32)
