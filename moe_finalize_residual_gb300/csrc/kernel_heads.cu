@@ -90,6 +90,12 @@ __device__ __forceinline__ LaneMap lane_map(int p, int rot, int style) {
   return m;
 }
 
+// Of the pairs 2j and 2j + 1 the turned element where the pair is rotated, else the one that passes: a turn by (1, 0) would
+// add zero times its partner, which may be an infinity or NaN.
+__device__ __forceinline__ float2 rotated_of(const LaneMap& m, int j, float2 turned, float2 passed) {
+  return make_float2(2 * j < m.pairs ? turned.x : passed.x, 2 * j + 1 < m.pairs ? turned.y : passed.y);
+}
+
 __device__ __forceinline__ int64_t position_of(const mfr_head_norm_args& a, int64_t t) {
   return (a.flags & MFR_FLAG_POSITIONS_64) ? static_cast<const int64_t*>(a.positions)[t]
                                            : static_cast<const int32_t*>(a.positions)[t];
@@ -178,18 +184,21 @@ __device__ __forceinline__ void fill_cache(const mfr_head_norm_args& a, int64_t 
     if (i >= entries || p >= a.D / 16) continue;  // (the same trip count for all lanes)
     const LaneMap m = lane_map(p, a.rot, STYLE);
     float2 t[2];
+    bool on[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int pair = 8 * p + 2 * j + k;
-      t[k] = pair < a.rot / 2 ? cos_sin(turn_of(a.inv_freq[pair]), at, a.rotary_scale) : make_float2(1.0f, 0.0f);
+      on[k] = pair < a.rot / 2;
+      t[k] = on[k] ? cos_sin(turn_of(a.inv_freq[pair]), at, a.rotary_scale) : make_float2(1.0f, 0.0f);
     }
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const void* weight = kind ? a.k_weight : a.q_weight;
       const float2 w0 = weight_pair<A, STYLE>(weight, p, 2 * j, m), w1 = weight_pair<A, STYLE>(weight, p, 2 * j + 1, m);
       auto entry = cache[kind * tokens + token][j];
-      entry[0][p] = make_float4(t[0].x * w0.x, t[1].x * w1.x, -t[0].y * w0.y, -t[1].y * w1.y);
-      entry[1][p] = make_float4(t[0].x * w0.y, t[1].x * w1.y, t[0].y * w0.x, t[1].y * w1.x);
+      // (an element that passes has nothing of its partner's weight, whatever that is)
+      entry[0][p] = make_float4(t[0].x * w0.x, t[1].x * w1.x, on[0] ? -t[0].y * w0.y : 0.0f, on[1] ? -t[1].y * w1.y : 0.0f);
+      entry[1][p] = make_float4(t[0].x * w0.y, t[1].x * w1.y, on[0] ? t[0].y * w0.x : 0.0f, on[1] ? t[1].y * w1.x : 0.0f);
     }
   }
   __syncwarp();
@@ -313,6 +322,18 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) head_norm_kernel(const 
       const float2 xa = __fmul2_rn(x.a[j], rr), xb = __fmul2_rn(x.b[j], rr);
       v.a[j] = __ffma2_rn(xb, make_float2(ta.z, ta.w), __fmul2_rn(xa, make_float2(ta.x, ta.y)));
       v.b[j] = __ffma2_rn(xa, make_float2(tb.z, tb.w), __fmul2_rn(xb, make_float2(tb.x, tb.y)));
+    }
+    if (rs == 0.0f) {
+      // An element is infinite, or as good as that: zero times it must not reach a partner that passes.  (The elements are
+      // taken from the slot again, so that the other heads keep no register for this.)
+      const LaneMap again = lane_map(lane_on ? lane % G : 0, a.rot, STYLE);
+      const Pairs y = unpack_pairs_of<A, STYLE>({lds16(from), lds16(from + 32 * 16)});
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 ta = turn[2 * j * G], tb = turn[(2 * j + 1) * G];
+        v.a[j] = rotated_of(again, j, v.a[j], __fmul2_rn(__fmul2_rn(y.a[j], rr), make_float2(ta.x, ta.y)));
+        v.b[j] = rotated_of(again, j, v.b[j], __fmul2_rn(__fmul2_rn(y.b[j], rr), make_float2(tb.x, tb.y)));
+      }
     }
     if (write && r < (r < cut.q_rounds ? q_last : k_last)) {
       if (pos >= 0) {
@@ -510,6 +531,15 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) head_norm_grad_kernel(c
       const Pairs x = unpack_pairs_of<A, STYLE>(xr);
       Pairs g = unpack_pairs_of<A, STYLE>(gr);
       turn_back<G>(g, turn);
+      if (a.rot < a.D) {  // (from the slot again: no register is kept for this)
+        const LaneMap again = lane_map(lane_on ? lane % G : 0, a.rot, STYLE);
+        const Pairs y = unpack_pairs_of<A, STYLE>({lds16(from + 2 * 32 * 16), lds16(from + 3 * 32 * 16)});
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g.a[j] = rotated_of(again, j, g.a[j], y.a[j]);
+          g.b[j] = rotated_of(again, j, g.b[j], y.b[j]);
+        }
+      }
       // sums of x^2 and of (g w) x
       float2 sq = make_float2(0.0f, 0.0f), dot = make_float2(0.0f, 0.0f);
       Pairs gw;
