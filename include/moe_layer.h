@@ -198,9 +198,10 @@ typedef struct {
  *   pair j of the first rot elements turned by the angle position * inv_freq[j], times rotary_scale:
  *     (a, b) -> (a cos - b sin, b cos + a sin) * rotary_scale;   the other elements pass
  *   out = round_act(...)                                       one rounding, after the rotation
- * The angle is reduced exactly (integer arithmetic modulo one turn), so that far positions lose nothing;
- * |inv_freq| < 2^20.  A token whose position is negative is padding: its values do not matter, and its output rows
- * are left as they were, or set to zero under MFR_FLAG_ZERO_PADDING.  An output may be its own input, with equal
+ * The angle is reduced by integer arithmetic modulo one turn, so that far positions lose nothing: to within 2^-33 of a
+ * turn for 32-bit positions and 2^-47 for 64-bit ones, of which the nearest 2^-32 is taken; |inv_freq| < 2^20.  A token
+ * whose position is negative is padding: its values do not matter, and its output rows are left as they were, or set to
+ * zero under MFR_FLAG_ZERO_PADDING.  An output may be its own input, with equal
  * strides (in place); otherwise outputs overlap no input and not each other. */
 typedef struct {
   int32_t T;                 /* tokens, >= 0                                                            */

@@ -10,9 +10,10 @@
 // the arithmetic runs on packed operations.  A warp computes the sines and cosines of its token's pairs once, in
 // shared memory, and turns every head of the token by them.
 //
-// The angle position * inv_freq is reduced without error: inv_freq / (2 pi) is held as a 64-bit fraction of
-// a turn (24-bit significand times 1 / (2 pi) to 64 bits), so the product with the position, modulo 2^64, is
-// the fraction of the turn, with an error of position * 2^-64 turns.
+// The angle position * inv_freq is reduced in integers: inv_freq / (2 pi) is held as a 128-bit fraction of a turn
+// (24-bit significand times 1 / (2 pi) to 128 bits), and the first 64 bits of its product with the position, modulo
+// 2^128, are the fraction of the turn: within 2^-47 of a turn for any 64-bit position and |inv_freq| < 2^20.  32-bit
+// positions make do with the first 64 bits of inv_freq's turn, within 2^-33.  The sine and cosine take the nearest 2^-32.
 //
 // The work is cut into rounds: one head for each of a warp's groups.  A warp keeps the vectors of its next rounds in
 // flight by cp.async into slots of shared memory that each lane fills and reads by itself, so no warp waits for
@@ -48,25 +49,23 @@ struct HeadParams {
   HeadCut cut;
 };
 
-// inv_freq / (2 pi) as a fraction of a turn times 2^64, modulo 2^64.
-__device__ __forceinline__ uint64_t turn_of(float inv_freq) {
+// position * inv_freq / (2 pi) as a fraction of a turn times 2^64, modulo 2^64, for |inv_freq| < 2^20.
+__device__ __forceinline__ uint64_t turns_of(float inv_freq, int64_t pos, bool wide) {
   const uint32_t bits = __float_as_uint(inv_freq);
   const int e = (bits >> 23) & 0xff;
   if (e == 0) return 0;  // zero, and subnormals (below 2^-126 turns a position)
-  // inv_freq = m 2^(e - 150);  1 / (2 pi) = c 2^-66, c rounded to 64 bits
-  const uint64_t m = (bits & 0x7fffffu) | 0x800000u, c = 0xA2F9836E4E44152AULL;
-  const uint64_t hi = __umul64hi(m, c), lo = m * c;
-  const int s = 152 - e;  // turns 2^64 = (m c) 2^-s
-  uint64_t r;
-  if (s >= 128)
-    r = 0;
-  else if (s >= 64)
-    r = hi >> (s - 64);
-  else if (s > 0)
-    r = (hi << (64 - s)) | (lo >> s);
-  else
-    r = s > -64 ? lo << -s : 0;
-  return (bits >> 31) ? 0 - r : r;
+  // inv_freq = m 2^(e - 150);  1 / (2 pi) = (c1 2^64 + c0) 2^-130, to 128 bits;  m (c1 2^64 + c0) = t1 2^128 + t0 2^64 + low
+  const uint64_t m = (bits & 0x7fffffu) | 0x800000u, c1 = 0xA2F9836E4E441529ULL, c0 = 0xFC2757D1F534DDC1ULL;
+  const uint64_t low = m * c0, carry = __umul64hi(m, c0), t0 = m * c1 + carry, t1 = __umul64hi(m, c1) + (t0 < carry ? 1 : 0);
+  // a position's turns times 2^128 are that times 2^-s: hi 2^64 + lo, modulo 2^128
+  const int s = max(152 - e, 1), k = s & 63;  // (s >= 6 for the frequencies allowed)
+  const uint64_t n = static_cast<uint64_t>(pos), hi = s < 64 ? (t1 << (64 - s)) | (t0 >> s) : s < 128 ? t1 >> k : 0;
+  uint64_t u = hi * n;
+  if (wide) {  // (a position below 2^31 has nothing of lo within 2^-33 of a turn)
+    const uint64_t up = k == 0 ? 0 : s < 64 ? t0 << (64 - k) : t1 << (64 - k);
+    u += __umul64hi(s < 64 ? up | (low >> s) : s < 128 ? up | (t0 >> k) : t1 >> k, n);
+  }
+  return (bits >> 31) ? 0 - u : u;
 }
 
 // Where a lane's two vectors lie, and its 8 pairs.
@@ -101,9 +100,9 @@ __device__ __forceinline__ int64_t position_of(const mfr_head_norm_args& a, int6
                                            : static_cast<const int32_t*>(a.positions)[t];
 }
 
-// The cosine and sine of an angle at a position, times `scale`.
-__device__ __forceinline__ float2 cos_sin(uint64_t turn, int64_t pos, float scale) {
-  const uint64_t u = turn * static_cast<uint64_t>(pos);
+// The cosine and sine of the angle at a position, times `scale`; `wide`: the position may be 2^31 or more.
+__device__ __forceinline__ float2 cos_sin(float inv_freq, int64_t pos, bool wide, float scale) {
+  const uint64_t u = turns_of(inv_freq, pos, wide);
   // the nearest 2^-32 turn, as a half turn in [-1, 1)
   const float h = static_cast<float>(static_cast<int32_t>((u + 0x80000000ULL) >> 32)) * 4.656612873077393e-10f;
   float s, c;
@@ -189,7 +188,7 @@ __device__ __forceinline__ void fill_cache(const mfr_head_norm_args& a, int64_t 
     for (int k = 0; k < 2; ++k) {
       const int pair = 8 * p + 2 * j + k;
       on[k] = pair < a.rot / 2;
-      t[k] = on[k] ? cos_sin(turn_of(a.inv_freq[pair]), at, a.rotary_scale) : make_float2(1.0f, 0.0f);
+      t[k] = on[k] ? cos_sin(a.inv_freq[pair], at, a.flags & MFR_FLAG_POSITIONS_64, a.rotary_scale) : make_float2(1.0f, 0.0f);
     }
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
@@ -384,7 +383,7 @@ __device__ __forceinline__ void fill_turns(const mfr_head_norm_args& a, int64_t 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int pair = 8 * p + 2 * j + k;
-      t[k] = pair < a.rot / 2 ? cos_sin(turn_of(a.inv_freq[pair]), at, a.rotary_scale) : make_float2(1.0f, 0.0f);
+      t[k] = pair < a.rot / 2 ? cos_sin(a.inv_freq[pair], at, a.flags & MFR_FLAG_POSITIONS_64, a.rotary_scale) : make_float2(1.0f, 0.0f);
     }
     cache[token][j][p] = make_float4(t[0].x, t[1].x, t[0].y, t[1].y);
   }

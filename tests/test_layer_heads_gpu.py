@@ -2,6 +2,9 @@
 import pytest
 import torch
 
+import layer_reference as ref
+from layer_reference import smallest, step
+
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
@@ -77,3 +80,47 @@ def test_a_gradient_stays_out_of_unrotated_weights(mfr, D, rot, style, bad):
         keep = (torch.arange(D) != i).cuda()
         assert torch.equal(got[2][keep], want[2][keep]) and not torch.isfinite(got[2][i]), i
         assert torch.equal(got[3], want[3]) and torch.equal(got[0][0], want[0][0]) and torch.equal(got[0][1, 0], want[0][1, 0])
+
+
+# As a share of its pair's length, before the rounding: the mean square 15 u, half of it in the root, and the root 4 u; the
+# element times the root u; the angle pi 2^-25 (the nearest 2^-32 turn, and the half turn's rounding) and 2^-47 of a turn;
+# the sine or cosine 2 u, times rotary_scale u, times the weight u; the products and their sum 2 u on both elements.
+U = 2.0 ** -24
+SHARE = 22 * U + 1.2e-7 + 2.0 ** -44
+
+
+@pytest.mark.parametrize("style", ["half", "interleaved"])
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("wide", [False, True])
+def test_far_positions_lose_nothing(mfr, style, act, wide):
+    """Every position that its type holds, and frequencies up to the largest allowed, forward and back."""
+    D = 64
+    pos = [0, 1, 2 ** 24 + 1, 2 ** 30 + 12345, 2 ** 31 - 1] + [2 ** 33 + 5, 2 ** 39 + 3, 10 ** 13 + 9, 10 ** 15 + 7, 2 ** 53 + 1, 2 ** 62 - 3,
+                                                              2 ** 63 - 1] * wide
+    freq = torch.cat([torch.tensor([1.0, 0.5, 3.25, -0.7, 0.0, 900.0, 1e-9, -1e-18, 3e-39, 60000.5, 1048575.9, -777777.7]),
+                      torch.rand(D // 2 - 12, generator=gen(1))])
+    x = torch.randn(len(pos), 2, D, generator=gen(2)).to(act)
+    d = torch.randn(len(pos), 2, D, generator=gen(3)).to(act)
+    at = torch.tensor(pos, dtype=torch.int64 if wide else torch.int32).cuda()
+    y, _ = mfr.head_norm_rotary(x.cuda(), x.cuda(), None, None, at, freq.cuda(), style=style, eps=1e-5)
+    x64 = x.double().requires_grad_()
+    want = ref.head_norm(x64, None, pos, freq, style, 1e-5, 1.0)
+    r = 1 / (x.double().pow(2).mean(2, keepdim=True) + 1e-5).sqrt()
+
+    def pair_size(v):
+        a, b = (v[..., :D // 2], v[..., D // 2:]) if style == "half" else (v[..., 0::2], v[..., 1::2])
+        n = torch.hypot(a, b)
+        return torch.cat([n, n], 2) if style == "half" else n.repeat_interleave(2, dim=2)
+
+    def close(got, want, before):
+        bound = before + step(act) * (want.abs() + before) + smallest(act)
+        bad = (got.double().cpu() - want).abs() > bound
+        assert not bad.any(), f"positions {[pos[i] for i in bad.any(2).any(1).nonzero().flatten()]}"
+
+    close(y, want.detach(), SHARE * pair_size((x.double() * r)))
+    (want * d.double()).sum().backward()
+    dx = mfr.head_norm_rotary_backward(d.cuda(), d.cuda(), x.cuda(), x.cuda(), None, None, at, freq.cuda(), style=style, eps=1e-5)[0]
+    # r (g - x r^2 mean(g x)): the share on every factor, and the mean's 21 additions on its terms
+    size = pair_size(d.double())
+    mean = (size * x.double().abs()).mean(2, keepdim=True)
+    close(dx, x64.grad, r * (2 * SHARE * size + x.double().abs() * r * r * mean * (3 * SHARE + 24 * U)))
