@@ -84,12 +84,13 @@ int check_route(const mfr_route_args* a) {
   } else if (a->perm_idx != nullptr || a->row_route != nullptr || a->expert_counts != nullptr) {
     return fail(MFR_ERR_INVALID_ARG, "perm_idx, row_route and expert_counts need expert_offsets");
   }
+  if (!aligned(a->bias, 4)) return fail(MFR_ERR_INVALID_ARG, "bias not aligned to its type");  // (read without tokens too)
   if (a->T == 0) return MFR_OK;
   if (a->logits == nullptr || a->expert_ids == nullptr || a->expert_scale == nullptr)
     return fail(MFR_ERR_INVALID_ARG, "logits, expert_ids or expert_scale is NULL");
-  if (!aligned(a->logits, dtype_bytes(a->logits_dtype)) || !aligned(a->bias, 4) || !aligned(a->expert_ids, 4) ||
+  if (!aligned(a->logits, dtype_bytes(a->logits_dtype)) || !aligned(a->expert_ids, 4) ||
       !aligned(a->expert_scale, dtype_bytes(a->scale_dtype)))
-    return fail(MFR_ERR_INVALID_ARG, "logits, bias, expert_ids or expert_scale not aligned to its type");
+    return fail(MFR_ERR_INVALID_ARG, "logits, expert_ids or expert_scale not aligned to its type");
   return MFR_OK;
 }
 

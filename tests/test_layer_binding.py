@@ -1,4 +1,5 @@
 """What the Python binding of the operators around the finalize refuses by its own checks, without a GPU."""
+import ctypes
 import os
 import sys
 
@@ -68,3 +69,12 @@ def test_sizes_beyond_32_bits_are_refused(mfr, query, good):
         for bad in (good[i] + 2 ** 32, good[i] - 2 ** 32, 2 ** 31, 10 ** 30, 2.0, None):
             with pytest.raises(ValueError):
                 f(*good[:i], bad, *good[i + 1:])
+
+
+def test_empty_batch_with_a_bias_off_its_alignment_is_refused(mfr):
+    """Without tokens the expert order is still written, by a kernel that reads the bias.  (The pointers are refused, not read.)"""
+    a = mfr.layer._CRoute(T=0, E=64, K=8, logits_dtype=2, scale_dtype=2, score=0, num_groups=1, topk_groups=1, group_score=0,
+                          renormalize=1, row_align=16, scale=1.0, logits_stride=64, bias=0x20002, perm_idx=0x50000,
+                          row_route=0x60000, num_rows=1000, expert_offsets=0x70000, expert_counts=0x80000, flags=1)
+    assert mfr.raw_library().moe_route(ctypes.byref(a), None) == -1
+    assert "bias" in mfr.raw_library().moe_finalize_last_error().decode()
