@@ -68,16 +68,14 @@ __device__ __forceinline__ uint64_t turns_of(float inv_freq, int64_t pos, bool w
   return (bits >> 31) ? 0 - u : u;
 }
 
-// Where a lane's two vectors lie, and its 8 pairs.
+// Where a lane's two vectors lie, and how many of its 8 pairs are rotated.
 struct LaneMap {
   int off_a, off_b;  // element offsets of the vectors
-  int pair0;         // the first of its 8 pairs
-  int pairs;         // how many of the 8 are rotated
+  int pairs;
 };
 
 __device__ __forceinline__ LaneMap lane_map(int p, int rot, int style) {
   LaneMap m;
-  m.pair0 = 8 * p;
   if (style == MFR_ROTARY_INTERLEAVED || 16 * p >= rot) {
     m.off_a = 16 * p;
     m.off_b = 16 * p + 8;

@@ -870,7 +870,7 @@ __device__ __forceinline__ int load_peer(const int* local, uint32_t rank) {
   return v;
 }
 
-template <int NV, bool GENERAL>
+template <int NV>
 constexpr int kRouteThreads = NV <= 8 ? 1024 : 512;
 
 // Shared memory: each warp's scratch, the biases, and for the order the bitmap, the counts (of the chunk, of the chunks
@@ -897,7 +897,7 @@ __device__ __forceinline__ OrderSmem order_smem(uint8_t* base, int E) {
 }
 
 template <typename L, int NV, bool GENERAL>
-__global__ void __launch_bounds__(kRouteThreads<NV, GENERAL>, 1) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kRouteThreads<NV>, 1) route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const mfr_route_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, nwarps = blockDim.x >> 5;
@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(kOrderThreads, 1) order_kernel(const __grid_co
 template <typename L, int NV, bool GENERAL>
 cudaError_t launch_route_nv(const mfr_route_args& a, cudaStream_t stream) {
   const bool order = a.expert_offsets != nullptr, pdl = a.flags & MFR_FLAG_PDL;
-  constexpr int kThreads = kRouteThreads<NV, GENERAL>;
+  constexpr int kThreads = kRouteThreads<NV>;
   const int fixed = kThreads / 32 * kScratchBytes<NV> + (GENERAL ? 32 * NV * 4 : 0);
   const int smem = fixed + (order ? order_smem_bytes(a.E, a.K) : 0);
   auto kern = route_kernel<L, NV, GENERAL>;
