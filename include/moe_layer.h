@@ -41,7 +41,7 @@ extern "C" {
 typedef enum { MFR_SCORE_SOFTMAX = 0, MFR_SCORE_SIGMOID = 1 } mfr_score;
 typedef enum {
   MFR_GROUP_MAX = 0, /* a group's score is its best choice score                                        */
-  MFR_GROUP_TOP2 = 1 /* a group's score is the sum of its two best choice scores                         */
+  MFR_GROUP_TOP2 = 1 /* a group's score is the sum of its two best choice scores (its best where it has one) */
 } mfr_group_score;
 
 /* Per token t, over its logits x_e:
@@ -129,8 +129,8 @@ int moe_route_backward(const mfr_route_backward_args* args, struct CUstream_st* 
 
 /* rows[perm_idx[t, k]] = x[t] for every route whose perm_idx lies in [0, num_rows); no two routes may name
  * the same row.  With row_route (perm_idx the other way round, as moe_route writes it), rows whose route is
- * negative are set to zero; without it they are left as they were.  Rows of any type, copied as bytes.  Its gradient to x is moe_finalize_fused in finalize-only
- * mode over the gradient rows, with expert_scale NULL and a factor of 1. */
+ * negative are set to zero; without it they are left as they were.  Rows of any type, copied as bytes.  Its gradient to
+ * x is moe_finalize_fused in finalize-only mode over the gradient rows, with expert_scale NULL and a factor of 1. */
 typedef struct {
   int32_t T, K;              /* K in 1..MFR_MAX_TOP_K, T*K < 2^31                                        */
   int64_t row_bytes;         /* bytes of a row, a positive multiple of 16, <= 2^20                       */
@@ -144,7 +144,8 @@ typedef struct {
 
 int moe_dispatch_rows(const mfr_dispatch_args* args, struct CUstream_st* stream);
 
-/* The gradient of one partial's finalize, out[t] = rsf * sum_k scale[t,k] * row[perm[t,k]] (+ shared row),
+/* The gradient of one partial's finalize (finalize-only mode; the residual and the RMSNorm of the fused call have no
+ * gradient here), out[t] = rsf * sum_k scale[t,k] * row[perm[t,k]] (+ shared row),
  * given d_out:
  *   d_gemm2[perm[t,k]] = round_act((scale[t,k] * rsf) * d_out[t])
  *   d_scale[t,k]       = round(rsf * sum_h row[perm[t,k], h] * d_out[t, h])        0 for a skipped route

@@ -20,8 +20,8 @@
 // another.
 //
 // Bound by HBM: forward reads and writes each element once; backward reads two and writes one.  Measured on GB300 (copy
-// bandwidth 6779 GB/s), 48 + 8 heads of 128, BF16, from a packed projection: forward of 16384 tokens, 470 MB, 71.4 us
-// (0.97 of the copy); gradient of 8192 tokens, 352 MB, 60 us (0.86), of which 3 us are the sum of the weight gradients.
+// bandwidth 6779 GB/s), 48 + 8 heads of 128, BF16, from a packed projection: forward of 16384 tokens, 470 MB, 71.7 us
+// (0.97 of the copy); gradient of 8192 tokens, 352 MB, 60.5 us (0.86), of which 3 us are the sum of the weight gradients.
 #include <algorithm>
 
 #include "layer_launch.h"
@@ -246,7 +246,7 @@ constexpr int kFwdCtas = 12;  // CTAs an SM holds, by registers
 
 // Forward: a warp takes its rounds of one block of tokens.  The CTAs are small and come and go, which evens out the
 // SMs' load; a warp requests its first vectors, its position, frequencies and weights all at once.  Persistent warps
-// with equal shares took 82 to 88 us for the 71.4 above: their streams lie far apart, or the last of them end late.
+// with equal shares took 82 to 88 us for the 71.7 above: their streams lie far apart, or the last of them end late.
 template <typename A, int G, int STYLE>
 __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) head_norm_kernel(const __grid_constant__ HeadParams p) {
   extern __shared__ __align__(16) uint8_t smem[];

@@ -6,9 +6,10 @@
 //
 // The order of the chosen experts is that of 64-bit choice scores.  Without a bias a score orders as its
 // logit, and the logits are compared as they are.  With a bias (and for group scores that are sums) the
-// scores are computed in FP32 with a proven bound on their error; where two neighbours in the order lie
-// closer than the bound, the token is decided again in FP64 (slow_choice), which random inputs need about
-// once in a thousand tokens.
+// scores are computed in FP32 with a bound on the error of each, from its own size (near_of, slack_of).  Where the
+// ranges of two neighbours in the order meet, or those of a kept and a dropped group, what lies there is decided
+// again in FP64: the groups and candidates concerned, or, where they are many, all experts (slow_choice).  Random
+// inputs need that about once in a thousand tokens.
 //
 // The expert order is a stable counting sort.  A CTA takes a contiguous chunk of tokens and marks each
 // route in a bitmap [expert][token of the segment]: a route's rank among its expert's routes is the number
@@ -17,10 +18,11 @@
 // the chunks' counts in the workspace, and a second kernel (order_kernel) adds those of the chunks before its own.
 //
 // Bound by instructions, not by HBM: a token of 256 experts takes about 430 warp instructions for a choice by logits
-// and about 900 with a bias, groups and 64-bit decisions, while its logits take 0.15 ns of HBM time.  Ranking the few
-// candidates by counting is what keeps it there: one expert after the other took 1835.  Measured on GB300, in a graph:
-// 16384 tokens of 256 experts, top-8, 9.3 us by logits and 19.4 us with bias and groups (the logits are 2.5 us at the
-// copy bandwidth), and 7 us more for the order; one token 2.5 us, 3.8 us with the order.
+// and about 1000 with a bias, groups, 64-bit decisions and the order's marks, while its logits take 0.15 ns of HBM time.
+// Ranking the few candidates by counting is what keeps it there: one expert after the other took 1835.  Measured on
+// GB300, in a graph: 16384 tokens of 256 experts, top-8, 9.3 us by logits and 19.8 us with bias and groups (the logits
+// are 2.5 us at the copy bandwidth; 28.5 us with 2 of 8 groups kept, whose 64 experts are all candidates), and 7 us more
+// for the order; one token 2.5 us, 3.8 us with the order.
 #include "layer_launch.h"
 
 namespace mfr {

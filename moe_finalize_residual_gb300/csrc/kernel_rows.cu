@@ -7,7 +7,7 @@
 // zero by the CTAs behind the tokens'.
 //
 // Measured on GB300 (copy bandwidth 6779 GB/s): dispatch of 4096 tokens of 7168 FP16 elements to 8 experts, a
-// quarter of the routes masked, 529 MB in 81 us (0.96 of the copy); the gradient of the same batch in BF16, 881 MB
+// quarter of the routes masked, 529 MB in 82 us (0.95 of the copy); the gradient of the same batch in BF16, 881 MB
 // in 132 us (0.98).
 #include "layer_launch.h"
 

@@ -398,7 +398,8 @@ def moe_finalize_routed_backward(d_out: torch.Tensor, partial, *, routed_scaling
     out).  The gradient of ``shared_out`` is ``d_out`` itself, and every partial of a rank sum has the same ``d_out``.
     ``d_scale`` has the scales' dtype (fp32 where the partial has none).  No two routes may name the same row, and
     outputs overlap no input.  With ``row_route`` the rows of no route get zeros; without it they are left as they
-    were, or zeros in an allocated output."""
+    were, or zeros in an allocated output.  The residual addition and the RMSNorm of ``moe_finalize_fused`` have no
+    gradient here: a program that trains through them gets ``d_out`` from its own norm's gradient."""
     x, perm, scale = partial.gemm2_out, partial.perm_idx, partial.expert_scale
     if perm is None or x is None or d_out.dim() != 2 or perm.dim() != 2 or x.dim() != 2:
         raise ValueError("d_out must be [T, H], gemm2_out [rows, H] and perm_idx [T, K]")
