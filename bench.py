@@ -190,8 +190,13 @@ def alloc_outs(mfr, case, quant="none", sf_layout="row_major"):
     return (ro, no, qo, sf), qs
 
 
+# what the finalize kernels are compiled from (the operators around the finalize have files of their own)
+FINALIZE_SOURCES = ("api.cu", "kernel_bulk.cu", "kernel_cluster.cu", "kernel_stream.cu", "mfr_device.cuh", "mfr_launch.h",
+                    "mfr_rowlist.cuh")
+
+
 def traffic_for(kernel_name: str):
-    """DRAM bytes per launch from the committed ncu summary, if it was taken on the current kernel source."""
+    """DRAM bytes per launch from the committed ncu summary, if it was taken on the current source of the kernels."""
     p = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(p):
         return None
@@ -200,7 +205,7 @@ def traffic_for(kernel_name: str):
         import hashlib
         csrc = os.path.join(ROOT, "moe_finalize_residual_gb300", "csrc")
         h = hashlib.sha256()
-        for name in sorted(os.listdir(csrc)):
+        for name in FINALIZE_SOURCES:
             h.update(open(os.path.join(csrc, name), "rb").read())
         e = d.get(kernel_name)
         if e and e.get("source_sha256") == h.hexdigest():
