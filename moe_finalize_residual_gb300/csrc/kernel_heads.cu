@@ -61,7 +61,7 @@ __device__ __forceinline__ uint64_t turns_of(float inv_freq, int64_t pos, bool w
   const int s = max(152 - e, 1), k = s & 63;  // (s >= 6 for the frequencies allowed)
   const uint64_t n = static_cast<uint64_t>(pos), hi = s < 64 ? (t1 << (64 - s)) | (t0 >> s) : s < 128 ? t1 >> k : 0;
   uint64_t u = hi * n;
-  if (wide) {  // (a position below 2^31 has nothing of lo within 2^-33 of a turn)
+  if (wide) {  // (times a position below 2^31, lo is less than 2^-33 of a turn)
     const uint64_t up = k == 0 ? 0 : s < 64 ? t0 << (64 - k) : t1 << (64 - k);
     u += __umul64hi(s < 64 ? up | (low >> s) : s < 128 ? up | (t0 >> k) : t1 >> k, n);
   }
