@@ -365,3 +365,10 @@ _layer._bind(_lib, _check)
 from .layer import *  # noqa: E402,F401,F403
 
 __all__ += _layer.__all__
+
+from . import experts as _experts  # noqa: E402  (the experts' products, over the same library)
+
+_experts._bind(_lib, _check)
+from .experts import *  # noqa: E402,F401,F403
+
+__all__ += _experts.__all__

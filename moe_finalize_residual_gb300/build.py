@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_finalize.so")
 SOURCES = ["api.cu", "kernel_cluster.cu", "kernel_stream.cu", "kernel_bulk.cu", "layer_api.cu", "kernel_route.cu",
-           "kernel_rows.cu", "kernel_heads.cu"]
+           "kernel_rows.cu", "kernel_heads.cu", "experts_api.cu", "kernel_experts.cu", "kernel_experts_fp4.cu", "kernel_gate.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

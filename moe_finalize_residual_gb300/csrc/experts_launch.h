@@ -1,0 +1,26 @@
+// Host-side launch interface between the C ABI of the experts' products (experts_api.cu) and their kernels.
+#pragma once
+
+#include "layer_launch.h"
+#include "moe_experts.h"
+
+namespace mfr {
+
+cudaError_t launch_expert_matmul(const mfr_expert_matmul_args& a, cudaStream_t stream);
+cudaError_t launch_expert_rows_grad(const mfr_expert_matmul_backward_args& a, cudaStream_t stream);
+cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const mfr_swiglu_backward_args& a, cudaStream_t stream);
+cudaError_t launch_nvfp4_quantize(const mfr_nvfp4_args& a, cudaStream_t stream);
+cudaError_t launch_nvfp4_dequantize(const mfr_nvfp4_args& a, cudaStream_t stream);
+cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cudaStream_t stream);
+cudaError_t read_and_reset_expert_timeouts(unsigned int* count);
+cudaError_t read_and_reset_expert_nvfp4_timeouts(unsigned int* count);
+
+// Rows of an operand that one CTA's tile spans, and the most tiles of a call (tile numbers are 32-bit).
+constexpr int kExpertTileRows = 128;
+constexpr int64_t kExpertMaxTiles = int64_t{1} << 31;
+
+// Tiles of `tile` rows that R rows of E experts fill at most.
+inline int64_t expert_row_tiles(int64_t R, int E, int tile) { return R / tile + (R < E ? R : E); }
+
+}  // namespace mfr

@@ -1,0 +1,190 @@
+// sm_103a wrappers shared by the experts' products: bounded mbarrier waits, tensor copies (TMA), tensor memory and the
+// fifth-generation tensor-core instructions (tcgen05), with their operand and instruction descriptors.
+#pragma once
+
+#include <cuda.h>
+
+#include "mfr_device.cuh"
+
+namespace mfr {
+
+// ------------------------------------------------------------------------------------------------
+// Tensor copies
+// ------------------------------------------------------------------------------------------------
+
+// One box of a tensor map into this CTA's shared memory, its bytes counted on `bar`.  The CTA pair's form (Ctas 2) may
+// count on the barrier of the pair's other CTA: `bar` is then a shared::cluster address.
+template <int Ctas>
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (Ctas == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int Ctas>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (Ctas == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// The shared::cluster address that `local` has in CTA `rank` of this cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What this thread's loads and stores did to shared memory, before what tensor copies and tcgen05 do to it.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ------------------------------------------------------------------------------------------------
+// Tensor memory
+// ------------------------------------------------------------------------------------------------
+
+// Called by one whole warp (of each CTA of a pair); the address goes to shared memory at `dst`.
+template <int Ctas>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t columns) {
+  if constexpr (Ctas == 1)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns) : "memory");
+  else
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns) : "memory");
+}
+template <int Ctas>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+  if constexpr (Ctas == 1)
+    asm volatile(
+        "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\ntcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(
+            addr),
+        "r"(columns)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\ntcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(
+            addr),
+        "r"(columns)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 32 columns of FP32: register i of lane l is column i of tensor-memory lane l of the warp's quarter.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+
+// ------------------------------------------------------------------------------------------------
+// Matrix instructions
+// ------------------------------------------------------------------------------------------------
+
+// Operand descriptor of a tile in shared memory in the 128-byte swizzle, as tensor copies with that swizzle leave it
+// (1024-byte aligned).  Reduction-major tiles (the reduction runs along the 128-byte lines): `stride` is the distance
+// of groups of 8 lines, `lead` is not used.  The other kind (lines along M or N, one line for each step of the
+// reduction): `stride` is the distance of groups of 8 lines, `lead` that of the next 64 values of M or N.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t stride, uint32_t lead) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// Instruction descriptor of kind::f16 with FP32 accumulation: both operands BF16 or both FP16; a_lines / b_lines: the
+// operand's lines run along M / N instead of the reduction.
+__host__ __device__ constexpr uint32_t f16_idesc(bool bf16, bool a_lines, bool b_lines, int M, int N) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_lines ? 1u : 0u) << 15) |
+         ((b_lines ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// d (+)= a * b by one thread (of the pair's first CTA); `add` 0 overwrites d.
+template <int Ctas>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (Ctas == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// `bar` (in both CTAs of a pair) gets an arrival once this thread's matrix instructions so far are done.
+template <int Ctas>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (Ctas == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// NVFP4: E2M1 values, an E4M3 scale for every 16 of them.
+__host__ __device__ constexpr uint32_t nvfp4_idesc(int M, int N) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// d (+)= a * b over 64 values of the reduction.  `sfa`, `sfb`: tensor-memory columns of the scales, 4 for every 128 rows: row
+// r has its four scales in lane r % 32 (of each quarter), column r / 32.
+template <int Ctas>
+__device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t add) {
+  if constexpr (Ctas == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(add)
+        : "memory");
+}
+
+// 512 bytes of shared memory (32 lines of 16) to 4 columns of each quarter of tensor memory, in order before the matrix
+// instructions that this thread issues afterwards.
+template <int Ctas>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t dst, uint32_t src) {
+  // no swizzle; 128 bytes from 8 lines to the next 8
+  const uint64_t desc = static_cast<uint64_t>((src & 0x3ffffu) >> 4) | (uint64_t{128 >> 4} << 32) | (uint64_t{1} << 46);
+  if constexpr (Ctas == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc) : "memory");
+}
+
+}  // namespace mfr
