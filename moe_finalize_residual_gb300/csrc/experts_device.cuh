@@ -129,20 +129,31 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return f;
 }
 
-// A map of rank 2 or 3 (x, y, z with strides of y and z in bytes) with boxes of `bx` x `by`, bx * bytes of an element =
-// 128, in the 128-byte swizzle; what lies outside reads as zeros.
-inline cudaError_t encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* data, int64_t nx, int64_t ny, int64_t nz,
-                              int64_t sy, int64_t sz, int bx, int by, int rank) {
+// A map of `rank` dimensions (the first one's values next to one another, `strides` in bytes those of the others) with boxes
+// of `box` values, the first 128 bytes, in the 128-byte swizzle; what lies outside reads as zeros.
+inline cudaError_t encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* data, int rank, const cuuint64_t* dims,
+                              const cuuint64_t* strides, const cuuint32_t* box) {
   const auto f = tensor_map_encoder();
   if (f == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(nx), static_cast<cuuint64_t>(ny), static_cast<cuuint64_t>(nz)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sy), static_cast<cuuint64_t>(sz)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(bx), static_cast<cuuint32_t>(by), 1};
-  const cuuint32_t step[3] = {1, 1, 1};
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
   const CUresult r = f(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(data), dims, strides, box, step,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// Rows: `nx` values, `ny` rows `sy` bytes apart.
+inline cudaError_t encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* data, int64_t nx, int64_t ny, int64_t sy, int bx, int by) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(nx), static_cast<cuuint64_t>(ny)}, strides[1] = {static_cast<cuuint64_t>(sy)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(bx), static_cast<cuuint32_t>(by)};
+  return encode_map(map, type, data, 2, dims, strides, box);
+}
+// Weights: `nz` experts of `ny` rows of `nx` values.
+inline cudaError_t encode_weights(CUtensorMap* map, CUtensorMapDataType type, const void* data, int64_t nx, int64_t ny, int64_t nz, int64_t sy,
+                                  int64_t sz, int bx, int by) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(nx), static_cast<cuuint64_t>(ny), static_cast<cuuint64_t>(nz)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sy), static_cast<cuuint64_t>(sz)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(bx), static_cast<cuuint32_t>(by), 1};
+  return encode_map(map, type, data, 3, dims, strides, box);
 }
 
 // SMs of the current device.

@@ -1,15 +1,19 @@
 // The experts' 16-bit products: rows in expert order times their experts' weights, and the gradients to the rows and to
 // the weights, on the fifth-generation tensor cores.
 //
-// The three directions are one kernel over tiles of the output, D = A * B summed over the reduction:
-//   forward          A = rows [r, i]         B = weight [n, i]       over i: both operands' lines run along the reduction
-//   gradient to rows A = d_out [r, n]        B = weight [n, i]       over n: B's lines run along its columns i
-//   to weights       A = d_out [r, n]        B = rows [r, i]         over the expert's rows r: both along the columns
-// The instruction takes either kind of lines, so nothing is transposed in memory.
+// The three directions are one kernel over tiles of D = A * B summed over the reduction, D's rows in the lanes of tensor
+// memory and its columns in tensor memory's:
+//   forward          A = weight [n, i]        B = rows [r, i]         over i: both operands' lines run along the reduction
+//   gradient to rows A = weight [n, i]        B = d_out [r, n]        over n: A's lines run along D's rows i
+//   to weights       A = d_out [r, n]         B = rows [r, i]         over the expert's rows r: both along D's rows and columns
+// The instruction takes either kind of lines, so nothing is transposed in memory.  An expert's rows are D's columns in the
+// first two: an instruction takes any multiple of 16 (a pair's: 32) of them, so a ragged expert costs what its rows cost,
+// and a decode step's few rows hardly anything beside the weights.
 //
-// A persistent CTA (or a pair of CTAs) takes tiles of 128 rows (256) x BN columns.  One warp copies the operands in by
-// tensor copies, 64 values of the reduction a stage; one thread issues the matrix instructions into one of two
-// accumulators in tensor memory; four warps take finished accumulators out, round and store them meanwhile.
+// A persistent CTA, or a pair of CTAs that share the columns' operand, takes tiles of 128 (256) weight rows x at most BN
+// rows.  One warp copies the operands in by tensor copies, 64 values of the reduction a stage; one thread issues the matrix
+// instructions into one of two accumulators in tensor memory; four warps take finished accumulators out, round and store
+// them meanwhile.
 #include "experts_device.cuh"
 
 namespace mfr {
@@ -25,21 +29,21 @@ constexpr int kEpilogueWarp = 4;                 // first of four
 constexpr int kDepth = 64;                       // reduction values of a stage: lines of 128 bytes
 constexpr int kTileM = kExpertTileRows;          // rows of A of one CTA
 constexpr int kABytes = kTileM * kDepth * 2;
-constexpr int kSmallRows = 16;                   // rows of the small box of A
-constexpr int kBarBytes = 256;
+constexpr int kBoxRows = 32;                     // rows of a small box of B
+constexpr int kBarBytes = 512;
 
 template <typename T> constexpr bool kIsBf16 = false;
 template <> constexpr bool kIsBf16<__nv_bfloat16> = true;
 
 struct Params {
-  CUtensorMap a, a_small, b;
+  CUtensorMap a, b, b_small, d;  // (d: the weights' gradient)
   const int32_t* offsets;
   const int32_t* counts;
   int32_t E, R;
   int32_t n_red;       // reduction length (the weights' gradient: the expert's rows)
-  int32_t n_m, n_out;  // the weights' gradient: rows of D; columns of D (gated: of the output)
-  int32_t tiles_n;     // column tiles
-  int32_t tiles_m;     // the weights' gradient: row tiles
+  int32_t n_m;         // values of an output row (the weights' gradient: rows of D)
+  int32_t n_n;         // the weights' gradient: columns of D
+  int32_t tiles_m, tiles_n;  // row tiles of D; the weights' gradient: column tiles
   int32_t zero_free, accumulate;
   uint8_t* out;
   int64_t out_stride;  // bytes
@@ -52,53 +56,72 @@ struct Shape {
   static constexpr int kBRows = BN / Ctas;  // columns of D whose operand this CTA copies
   static constexpr int kBBytes = kBRows * kDepth * 2;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr bool kALines = D == kWeightGrad;
-  static constexpr bool kBLines = D == kRowsGrad || D == kWeightGrad;
+  // the weights' gradient leaves by two buffers of 128 lines of 128 bytes
+  static constexpr int kOutBytes = D == kWeightGrad ? kTileM * 128 : 0;
+  static constexpr int kStages = D == kWeightGrad ? 196608 / kStage : 204800 / kStage;
+  static constexpr bool kALines = D == kRowsGrad || D == kWeightGrad;
+  static constexpr bool kBLines = D == kWeightGrad;
+  static constexpr int kFeatures = (D == kGated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
+  static constexpr int kUnit = Ctas == 1 ? 16 : 32;  // an instruction's columns are a multiple
   // what one CTA holds besides the stages: the barriers and, but for the weights' gradient, the experts' first tiles
   static constexpr int kFixed = kBarBytes + (D == kWeightGrad ? 0 : (MFR_MAX_EXPERTS + 1 + 33) * 4);
-  static constexpr int kSmem = 1024 + kStages * kStage + kFixed;
+  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kOutBytes + kFixed;
 };
 
 struct Tile {
   int e;      // expert
-  int row0;   // first row of D that is a row in expert order (weights' gradient: the expert's first row)
-  int left;   // rows of the expert from row0 on
-  int m0;     // weights' gradient: first row of D
-  int n0;     // first column of D
+  int row0;   // its first row in the tile (weights' gradient: its first row)
+  int rows;   // its rows in the tile (weights' gradient: its rows)
+  int m0;     // first value of the output row (weights' gradient: first row of D)
+  int n0;     // weights' gradient: first column of D
   int steps;  // stages of the reduction
 };
 
 template <int D, int Ctas, int BN>
 __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint32_t t) {
+  using S = Shape<D, Ctas, BN>;
   Tile x;
-  constexpr int kCols = D == kGated ? BN / 2 : BN;
   if constexpr (D == kWeightGrad) {
     const uint32_t per = static_cast<uint32_t>(p.tiles_m) * p.tiles_n;
     x.e = t / per;
     const uint32_t in = t % per;
-    x.m0 = in / p.tiles_n * (kTileM * Ctas);
-    x.n0 = in % p.tiles_n * kCols;
+    x.m0 = in / p.tiles_n * S::kFeatures;
+    x.n0 = in % p.tiles_n * BN;
     const RowSpan s = expert_rows(p.offsets, p.counts, x.e, p.R);
     x.row0 = s.begin;
-    x.left = s.end - s.begin;
-    x.steps = (x.left + kDepth - 1) / kDepth;
+    x.rows = s.end - s.begin;
+    x.steps = (x.rows + kDepth - 1) / kDepth;
   } else {
-    const int m = t / p.tiles_n;
-    x.n0 = t % p.tiles_n * kCols;
+    const int m = t / p.tiles_m;
+    x.m0 = t % p.tiles_m * S::kFeatures;
+    x.n0 = 0;
     x.e = tile_expert(first, p.E, m);
     const RowSpan s = expert_rows(p.offsets, p.counts, x.e, p.R);
-    x.row0 = s.begin + (m - first[x.e]) * (kTileM * Ctas);
-    x.left = s.end - x.row0;
-    x.m0 = 0;
-    x.steps = (p.n_red + kDepth - 1) / kDepth;
+    // the expert's rows in equal parts: a short last one would use the weights' copies badly
+    const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
+    const int part = ((n + parts - 1) / parts + S::kUnit - 1) / S::kUnit * S::kUnit;
+    const int at = (m - first[x.e]) * part;
+    x.row0 = s.begin + at;
+    x.rows = n - at < part ? n - at : part;  // (not positive: the parts before it took all)
+    x.steps = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
   }
   return x;
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(uint8_t* dst, const float v[8]) {
-  *reinterpret_cast<uint4*>(dst) = make_uint4(Act<T>::pack(v[0], v[1]), Act<T>::pack(v[2], v[3]), Act<T>::pack(v[4], v[5]), Act<T>::pack(v[6], v[7]));
+__device__ __forceinline__ T to_act(float v) {
+  if constexpr (kIsBf16<T>) return __float2bfloat16_rn(v); else return __float2half_rn(v);
+}
+
+// Zeros, by one warp, in the lines from `from` on of a stage whose operands' lines are steps of the reduction: they hold rows
+// behind the expert's last, which must not count.  In both operands, since 0 * NaN is NaN.
+template <int BRows>
+__device__ __forceinline__ void clear_lines(uint32_t stage, int from) {
+  const int each = (kDepth - from) * 8;  // 16-byte pieces of a block of 64 columns
+  for (int i = threadIdx.x & 31; i < (kTileM + BRows) / 64 * each; i += 32)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + i / each * (64 * kDepth * 2) + from * 128 + i % each * 16), "r"(0) : "memory");
+  fence_async_shared();
+  __syncwarp();
 }
 
 // T: the operands' type; O: that of D (FP32 for the weights' gradient alone).
@@ -108,13 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const uint32_t stage0 = smem_addr(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage + 2 * S::kOutBytes);
   const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * S::kStages;
-  const uint32_t dfull0 = empty0 + 8 * S::kStages, dempty0 = dfull0 + 16, ready = dempty0 + 16;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 2 * S::kStages + 5);
+  // (the last two kinds: a pair's weights' gradient alone)
+  const uint32_t tail0 = empty0 + 8 * S::kStages, ready0 = tail0 + 8 * S::kStages;
+  const uint32_t dfull0 = ready0 + 8 * S::kStages, dempty0 = dfull0 + 16;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 4 * S::kStages + 4);
   volatile int* give_up = reinterpret_cast<volatile int*>(tmem_at + 1);
-  int* first = reinterpret_cast<int*>(smem + S::kStages * S::kStage + kBarBytes);
-  static_assert((2 * S::kStages + 6) * 8 <= kBarBytes, "barriers");
+  int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
+  static_assert((4 * S::kStages + 5) * 8 <= kBarBytes, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = Ctas == 2 ? cluster_ctarank() : 0;
@@ -123,12 +148,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(tail0 + 8 * s, 1);
+      mbar_init(ready0 + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(dfull0 + 8 * i, 1);
       mbar_init(dempty0 + 8 * i, 4 * Ctas);
     }
-    mbar_init(ready, 1);
     *give_up = 0;
     fence_mbar_init();
     tma_prefetch_map(&p.a);
@@ -138,12 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   pdl_launch_dependents();
   pdl_wait();
   if constexpr (D != kWeightGrad)
-    count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, kTileM * Ctas);
+    count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, BN);
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_at;
-  const uint32_t tiles = D == kWeightGrad ? static_cast<uint32_t>(p.E) * p.tiles_m * p.tiles_n : static_cast<uint32_t>(first[p.E]) * p.tiles_n;
+  const uint32_t tiles = D == kWeightGrad ? static_cast<uint32_t>(p.E) * p.tiles_m * p.tiles_n : static_cast<uint32_t>(first[p.E]) * p.tiles_m;
   const uint32_t t0 = blockIdx.x / Ctas, dt = gridDim.x / Ctas;
 
   if (warp == 0) {
@@ -153,16 +179,23 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       bool ok = true;
       for (uint32_t t = t0; t < tiles && ok; t += dt) {
         const Tile x = tile_at<D, Ctas, BN>(p, first, t);
-        // rows of A behind the expert's end may hold another's: they only make rows of D that are not stored
-        const int need = x.left - static_cast<int>(rank) * kTileM;
-        const int small = Ctas == 1 && D != kWeightGrad && need <= 64 ? (need + kSmallRows - 1) / kSmallRows : 0;
-        const uint32_t bytes = Ctas * (small > 0 ? small * kSmallRows * kDepth * 2 : kABytes) + Ctas * S::kBBytes;
+        // B's boxes may reach behind the expert's last row: that only makes columns of D that are not stored
+        const int mine = (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit / Ctas;  // rows that this CTA copies, but for the boxes' ends
+        const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;  // one box for all of them, or several of 32
+        const int boxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = Ctas * (kABytes + (D == kWeightGrad || whole ? S::kBBytes : boxes * kBoxRows * kDepth * 2));
         for (int k = 0; k < x.steps; ++k) {
           if (!(ok = wait_phase(empty0 + 8 * s, phase ^ 1, give_up, &g_expert_wait_timeouts))) break;
           const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
           uint32_t bar = full0 + 8 * s;
-          if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
-          if constexpr (Ctas == 2) bar = cluster_addr(bar, 0);
+          if (Ctas == 2 && D == kWeightGrad && x.rows < (k + 1) * kDepth) {
+            // the expert's last rows: each CTA of the pair sees its own copies land, and clears the lines behind them
+            if (rank == 1) bar = tail0 + 8 * s;
+            mbar_arrive_expect_tx(bar, S::kStage);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
+            if constexpr (Ctas == 2) bar = cluster_addr(bar, 0);
+          }
           const int r0 = k * kDepth;
           if constexpr (D == kWeightGrad) {
             for (int i = 0; i < kTileM / 64; ++i)
@@ -170,18 +203,18 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             for (int i = 0; i < S::kBRows / 64; ++i)
               tma_load_2d<Ctas>(b + i * 64 * kDepth * 2, &p.b, x.n0 + rank * S::kBRows + i * 64, x.row0 + r0, bar);
           } else {
-            if (small > 0)
-              for (int i = 0; i < small; ++i) tma_load_2d<Ctas>(a + i * kSmallRows * kDepth * 2, &p.a_small, r0, x.row0 + i * kSmallRows, bar);
-            else
-              tma_load_2d<Ctas>(a, &p.a, r0, x.row0 + rank * kTileM, bar);
             if constexpr (D == kForward)
-              tma_load_3d<Ctas>(b, &p.b, r0, x.n0 + rank * S::kBRows, x.e, bar);
-            else if constexpr (D == kGated)  // half of the tile's columns are the gate's, half the others'
-              for (int i = 0; i < 2 / Ctas; ++i)
-                tma_load_3d<Ctas>(b + i * (BN / 2) * kDepth * 2, &p.b, r0, x.n0 + (rank + i) * p.n_out, x.e, bar);
+              tma_load_3d<Ctas>(a, &p.a, r0, x.m0 + rank * kTileM, x.e, bar);
+            else if constexpr (D == kGated)  // 8 rows of the gate, 8 of the others, and so on
+              tma_load_5d<Ctas>(a, &p.a, r0, 0, 0, (x.m0 + rank * (kTileM / 2)) / 8, x.e, bar);
             else
-              for (int i = 0; i < S::kBRows / 64; ++i)
-                tma_load_3d<Ctas>(b + i * 64 * kDepth * 2, &p.b, x.n0 + rank * S::kBRows + i * 64, r0, x.e, bar);
+              for (int i = 0; i < kTileM / 64; ++i)
+                tma_load_3d<Ctas>(a + i * 64 * kDepth * 2, &p.a, x.m0 + rank * kTileM + i * 64, r0, x.e, bar);
+            if (S::kBRows <= kBoxRows || whole)  // (p.b_small is there for larger tiles alone)
+              tma_load_2d<Ctas>(b, &p.b, r0, x.row0 + rank * mine, bar);
+            else
+              for (int i = 0; i < boxes; ++i)
+                tma_load_2d<Ctas>(b + i * kBoxRows * kDepth * 2, &p.b_small, r0, x.row0 + rank * mine + i * kBoxRows, bar);
           }
           if (++s == S::kStages) { s = 0; phase ^= 1; }
         }
@@ -192,122 +225,170 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       }
     }
   } else if (warp == 1) {
-    // ---- matrix instructions
-    if (rank == 0 || D == kWeightGrad) {
-      constexpr uint32_t idesc = f16_idesc(kIsBf16<T>, S::kALines, S::kBLines, kTileM * Ctas, BN);
-      uint32_t s = 0, phase = 0, buf = 0, dphase = 0;
-      bool ok = true;
-      for (uint32_t t = t0; t < tiles && ok; t += dt) {
-        int steps = (p.n_red + kDepth - 1) / kDepth, last = kDepth;
+    // ---- matrix instructions (of a pair: by its first CTA)
+    uint32_t s = 0, phase = 0, buf = 0, dphase = 0, tail_phase = 0;
+    bool ok = true;
+    for (uint32_t t = t0; t < tiles && ok; t += dt) {
+      const Tile x = tile_at<D, Ctas, BN>(p, first, t);
+      const int steps = x.steps;
+      if (steps == 0) continue;
+      const int last = x.rows - (steps - 1) * kDepth;  // (weights' gradient) rows of the last stage
+      const int columns = D == kWeightGrad ? BN : (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit;
+      const uint32_t idesc = f16_idesc(kIsBf16<T>, S::kALines, S::kBLines, kTileM * Ctas, columns);
+      if (rank != 0) {
+        // the pair's other CTA clears the lines of its own operands behind the expert's last row, and says so
         if constexpr (D == kWeightGrad) {
-          const RowSpan r = expert_rows(p.offsets, p.counts, t / (static_cast<uint32_t>(p.tiles_m) * p.tiles_n), p.R);
-          steps = (r.end - r.begin + kDepth - 1) / kDepth;
-          last = r.end - r.begin - (steps - 1) * kDepth;
-          if (steps == 0) continue;
+          s = (s + steps - 1) % S::kStages;
+          if (last < kDepth) {
+            if (!(ok = __all_sync(0xffffffffu, wait_phase(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
+            tail_phase ^= 1u << s;
+            clear_lines<S::kBRows>(stage0 + s * S::kStage, last);
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(ready0 + 8 * s, 0));
+          }
+          s = (s + 1) % S::kStages;
         }
-        if (!(ok = __all_sync(0xffffffffu, wait_phase(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
+        continue;
+      }
+      // (one thread waits and issues; the others go ahead to where they are needed, or to the tile's end)
+      if (lane == 0) {
+        ok = wait_phase(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts);
         tmem_fence_after();
-        for (int k = 0; k < steps; ++k) {
-          if (!(ok = __all_sync(0xffffffffu, wait_phase(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts)))) break;
-          const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
-          if constexpr (D == kWeightGrad) {
-            // the lines behind the expert's last row hold other rows: zeros in both operands (0 * NaN is NaN)
-            if (k == steps - 1 && last < kDepth) {
-              const int lines = kDepth - last;
-              for (int i = lane; i < (kTileM + S::kBRows) / 64 * lines * 8; i += 32) {
-                const int block = i / (lines * 8), in = i % (lines * 8);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a + block * 64 * kDepth * 2 + last * 128 + in * 16), "r"(0) : "memory");
-              }
-              fence_async_shared();
-              __syncwarp();
+      }
+      for (int k = 0; k < steps; ++k) {
+        if (lane == 0) ok = ok && wait_phase(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts);
+        const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
+        if constexpr (D == kWeightGrad) {
+          if (k == steps - 1 && last < kDepth) {
+            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
+            clear_lines<S::kBRows>(a, last);
+            if constexpr (Ctas == 2) {
+              if (lane == 0) ok = wait_phase(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts);
+              tail_phase ^= 1u << s;
             }
           }
-          tmem_fence_after();
-          if (lane == 0) {
-            const uint64_t da = S::kALines ? swizzled_desc(a, 1024, 64 * kDepth * 2) : swizzled_desc(a, 1024, 16);
-            const uint64_t db = S::kBLines ? swizzled_desc(b, 1024, 64 * kDepth * 2) : swizzled_desc(b, 1024, 16);
-#pragma unroll
-            for (int i = 0; i < kDepth / 16; ++i)  // 16 values of the reduction: 32 bytes of a line, or 16 lines
-              mma_f16<Ctas>(tmem + buf * BN, da + i * (S::kALines ? 128 : 2), db + i * (S::kBLines ? 128 : 2), idesc, (k | i) != 0);
-            mma_commit<Ctas>(empty0 + 8 * s);
-            if (k == steps - 1) mma_commit<Ctas>(dfull0 + 8 * buf);
-          }
-          __syncwarp();
-          if (++s == S::kStages) { s = 0; phase ^= 1; }
         }
-        if (buf ^= 1; buf == 0) dphase ^= 1;
+        if (lane == 0 && ok) {
+          tmem_fence_after();
+          const uint64_t da = S::kALines ? swizzled_desc(a, 1024, 64 * kDepth * 2) : swizzled_desc(a, 1024, 16);
+          const uint64_t db = S::kBLines ? swizzled_desc(b, 1024, 64 * kDepth * 2) : swizzled_desc(b, 1024, 16);
+#pragma unroll
+          for (int i = 0; i < kDepth / 16; ++i)  // 16 values of the reduction: 32 bytes of a line, or 16 lines
+            mma_f16<Ctas>(tmem + buf * BN, da + i * (S::kALines ? 128 : 2), db + i * (S::kBLines ? 128 : 2), idesc, (k | i) != 0);
+          mma_commit<Ctas>(empty0 + 8 * s);
+          if (k == steps - 1) mma_commit<Ctas>(dfull0 + 8 * buf);
+        }
+        if (++s == S::kStages) { s = 0; phase ^= 1; }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (buf ^= 1; buf == 0) dphase ^= 1;
     }
   } else if (warp < kEpilogueWarp) {
     // ---- rows of no expert
     if (D != kWeightGrad && p.zero_free) {
       const int w = blockIdx.x * 2 + warp - 2, nw = gridDim.x * 2;
-      zero_free_rows(p.out, p.out_stride, static_cast<int64_t>(p.n_out) * 2, p.offsets, p.counts, p.E, p.R, w, nw);
+      zero_free_rows(p.out, p.out_stride, static_cast<int64_t>(p.n_m) * 2, p.offsets, p.counts, p.E, p.R, w, nw);
       if (D == kGated && p.gate_up != nullptr)
-        zero_free_rows(p.gate_up, p.gate_up_stride, static_cast<int64_t>(p.n_out) * 4, p.offsets, p.counts, p.E, p.R, w, nw);
+        zero_free_rows(p.gate_up, p.gate_up_stride, static_cast<int64_t>(p.n_m) * 4, p.offsets, p.counts, p.E, p.R, w, nw);
     }
   } else {
     // ---- finished accumulators
     const int quarter = warp - kEpilogueWarp;
     uint32_t buf = 0, dphase = 0;
+    int stored = 0;  // (weights' gradient) boxes so far
     for (uint32_t t = t0; t < tiles; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
-      const int r = rank * kTileM + quarter * 32 + lane;
-      const bool live = D == kWeightGrad ? x.m0 + r < p.n_m : r < x.left;
-      const int64_t row = D == kWeightGrad ? static_cast<int64_t>(x.e) * p.n_m + x.m0 + r : static_cast<int64_t>(x.row0) + r;
-      uint8_t* out = p.out + row * p.out_stride;
-      const bool some = D != kWeightGrad || x.steps > 0;
+      const bool some = x.steps > 0;
       if (some) {
-        if (!__all_sync(0xffffffffu, wait_phase(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts))) break;
+        const bool ok = wait_phase(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
+        if (D == kWeightGrad ? !named_all(1, 128, ok) : !__all_sync(0xffffffffu, ok)) break;  // (the warps of the first share their stores)
         tmem_fence_after();
       }
       const uint32_t d = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-      constexpr int kCols = D == kGated ? BN / 2 : BN;
+      const int r = quarter * 32 + lane;  // this thread's lane of D
+      if constexpr (D == kWeightGrad) {
+        // through shared memory, since a thread has a row: lines of 128 bytes (kLine values) of 128 rows, a box each
+        constexpr int kLine = 128 / sizeof(O);
+        const int m0 = x.m0 + rank * kTileM;
+        if (some || !p.accumulate) {
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t v[32], u[32];
-        if (some) {
-          tmem_load32(d + c, v);
-          if constexpr (D == kGated) tmem_load32(d + BN / 2 + c, u);
-          tmem_wait_load();
-        } else {
+          for (int c = 0; c < BN && x.n0 + c < p.n_n; c += kLine, ++stored) {
+            const uint32_t box = stage0 + S::kStages * S::kStage + (stored & 1) * S::kOutBytes;
+            if (threadIdx.x == kEpilogueWarp * 32) tma_store_wait_read<1>();  // the buffer's last box has left it
+            named_sync(1, 128);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0;
-        }
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const int n = x.n0 + c + i;
-            if (n < p.n_out) {
-              float y[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(v[i + j]);
-              if constexpr (D == kGated) {
-                float z[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(u[i + j]);
-                if (p.gate_up != nullptr) {
-                  uint8_t* g = p.gate_up + row * p.gate_up_stride;
-                  store8<T>(g + static_cast<int64_t>(n) * 2, y);
-                  store8<T>(g + (static_cast<int64_t>(p.n_out) + n) * 2, z);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = swiglu(y[j], z[j]);
-              }
-              if constexpr (sizeof(O) == 4) {
-                float4* o = reinterpret_cast<float4*>(out + static_cast<int64_t>(n) * 4);
-                float4 lo = make_float4(y[0], y[1], y[2], y[3]), hi = make_float4(y[4], y[5], y[6], y[7]);
-                if (p.accumulate) {
-                  const float4 a = o[0], b = o[1];
-                  lo = make_float4(lo.x + a.x, lo.y + a.y, lo.z + a.z, lo.w + a.w);
-                  hi = make_float4(hi.x + b.x, hi.y + b.y, hi.z + b.z, hi.w + b.w);
-                }
-                o[0] = lo;
-                o[1] = hi;
+            for (int h = 0; h < kLine; h += 32) {
+              uint32_t v[32];
+              if (some) {
+                tmem_load32(d + c + h, v);
+                tmem_wait_load();
               } else {
-                store8<T>(out + static_cast<int64_t>(n) * 2, y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+              }
+              constexpr int kPiece = 16 / sizeof(O);  // values of 16 bytes, in the 128-byte swizzle
+#pragma unroll
+              for (int i = 0; i < 32; i += kPiece) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if constexpr (sizeof(O) == 4)
+                    w[j] = v[i + j];
+                  else
+                    w[j] = Act<T>::pack(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + r * 128 + ((((h + i) / kPiece) ^ (r & 7)) << 4)), "r"(w[0]),
+                             "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
               }
             }
+            fence_async_shared();
+            named_sync(1, 128);
+            if (threadIdx.x == kEpilogueWarp * 32 && m0 < p.n_m) {
+              if (p.accumulate)
+                tma_add_3d(&p.d, box, x.n0 + c, m0, x.e);
+              else
+                tma_store_3d(&p.d, box, x.n0 + c, m0, x.e);
+            }
+            if (threadIdx.x == kEpilogueWarp * 32) tma_store_commit();
+          }
+        }
+      } else if constexpr (D == kGated) {
+        // lanes 0..7 of each 16 hold gates, 8..15 the others; each of the two computes every second row
+        const int f = x.m0 + rank * (kTileM / 2) + r / 16 * 8 + r % 8;
+        const bool upper = (r & 8) != 0, live = f < p.n_m;
+        T* out = reinterpret_cast<T*>(p.out + static_cast<int64_t>(x.row0) * p.out_stride) + f;
+        T* kept = reinterpret_cast<T*>(p.gate_up + static_cast<int64_t>(x.row0) * p.gate_up_stride) + (upper ? p.n_m : 0) + f;
+#pragma unroll 1
+        for (int c = 0; c < x.rows; c += 32) {
+          uint32_t v[32];
+          tmem_load32(d + c, v);
+          tmem_wait_load();
+          if (p.gate_up != nullptr && live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < x.rows) *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(kept) + (c + j) * p.gate_up_stride) = to_act<T>(__uint_as_float(v[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
+            const float y = swiglu(__uint_as_float(upper ? other : v[j]), __uint_as_float(upper ? v[j + 1] : other));
+            const int row = c + j + (upper ? 1 : 0);
+            if (live && row < x.rows) *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(out) + row * p.out_stride) = to_act<T>(y);
+          }
+        }
+      } else {
+        // 32 neighbouring values of one row in a warp: whole sectors
+        const int f = x.m0 + rank * kTileM + r;
+        uint8_t* out = p.out + static_cast<int64_t>(x.row0) * p.out_stride + static_cast<int64_t>(f) * 2;
+#pragma unroll 1
+        for (int c = 0; c < x.rows; c += 32) {
+          uint32_t v[32];
+          tmem_load32(d + c, v);
+          tmem_wait_load();
+          if (f < p.n_m) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < x.rows) *reinterpret_cast<T*>(out + (c + j) * p.out_stride) = to_act<T>(__uint_as_float(v[j]));
           }
         }
       }
@@ -320,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         if (buf ^= 1; buf == 0) dphase ^= 1;
       }
     }
+    if (D == kWeightGrad && threadIdx.x == kEpilogueWarp * 32) tma_store_wait();
   }
   __syncwarp();
   tmem_fence_before();
@@ -349,11 +431,24 @@ cudaError_t launch(Params& p, int64_t most_tiles, bool pdl, cudaStream_t stream)
 CUtensorMapDataType map_type(int act) { return act == MFR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }
 
 template <int D, int Ctas, int BN>
-cudaError_t launch_rows(int act, int64_t R, int E, Params& p, bool pdl, cudaStream_t stream) {
-  p.tiles_n = (p.n_out + (D == kGated ? BN / 2 : BN) - 1) / (D == kGated ? BN / 2 : BN);
-  const int64_t tiles = expert_row_tiles(R, E, kTileM * Ctas) * p.tiles_n;
+cudaError_t launch_rows(int act, int64_t R, int E, const void* rows, int64_t rows_stride, Params& p, bool pdl, cudaStream_t stream) {
+  using S = Shape<D, Ctas, BN>;
+  static_assert(S::kBRows % kBoxRows == 0, "boxes of B");
+  cudaError_t e = encode_rows(&p.b, map_type(act), rows, p.n_red, R, rows_stride * 2, kDepth, S::kBRows);
+  if (e == cudaSuccess && S::kBRows > kBoxRows) e = encode_rows(&p.b_small, map_type(act), rows, p.n_red, R, rows_stride * 2, kDepth, kBoxRows);
+  if (e != cudaSuccess) return e;
+  p.tiles_m = (p.n_m + S::kFeatures - 1) / S::kFeatures;
+  const int64_t tiles = expert_row_tiles(R, E, BN) * p.tiles_m;
   return act == MFR_BF16 ? launch<D, Ctas, BN, __nv_bfloat16, __nv_bfloat16>(p, tiles, pdl, stream)
                          : launch<D, Ctas, BN, __half, __half>(p, tiles, pdl, stream);
+}
+
+// The tile by the rows that an expert has: with few of them the stages hold weights alone, as many as fit; with many, a pair
+// of CTAs halves the copies of the columns' operand.
+template <int D>
+cudaError_t launch_by_rows(int act, int64_t R, int E, const void* rows, int64_t rows_stride, Params& p, bool pdl, cudaStream_t stream) {
+  if (R <= int64_t{16} * E) return launch_rows<D, 1, 32>(act, R, E, rows, rows_stride, p, pdl, stream);
+  return launch_rows<D, 2, 256>(act, R, E, rows, rows_stride, p, pdl, stream);
 }
 
 }  // namespace
@@ -361,52 +456,69 @@ cudaError_t launch_rows(int act, int64_t R, int E, Params& p, bool pdl, cudaStre
 cudaError_t launch_expert_matmul(const mfr_expert_matmul_args& a, cudaStream_t stream) {
   Params p = {};
   const CUtensorMapDataType type = map_type(a.act_dtype);
-  const int wide = a.gated ? 2 * a.n_out : a.n_out;
-  constexpr int BN = 256;
-  const int b_rows = a.gated ? BN / 2 : BN;
-  cudaError_t e = encode_map(&p.a, type, a.rows, a.n_in, a.num_rows, 1, a.rows_stride * 2, 0, kDepth, kTileM, 2);
-  if (e == cudaSuccess) e = encode_map(&p.a_small, type, a.rows, a.n_in, a.num_rows, 1, a.rows_stride * 2, 0, kDepth, kSmallRows, 2);
-  if (e == cudaSuccess)
-    e = encode_map(&p.b, type, a.weight, a.n_in, wide, a.E, a.weight_stride * 2, (a.E > 1 ? a.weight_expert_stride : wide * a.weight_stride) * 2,
-                   kDepth, b_rows, 3);
+  const int64_t row = a.weight_stride * 2, wide = a.gated ? int64_t{2} * a.n_out : a.n_out;
+  const int64_t expert = (a.E > 1 ? a.weight_expert_stride * 2 : wide * row);
+  cudaError_t e;
+  if (a.gated) {
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(a.n_in), 8, 2, static_cast<cuuint64_t>(a.n_out / 8), static_cast<cuuint64_t>(a.E)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(a.n_out * row), static_cast<cuuint64_t>(8 * row),
+                                   static_cast<cuuint64_t>(expert)};
+    const cuuint32_t box[5] = {kDepth, 8, 2, kTileM / 16, 1};
+    e = encode_map(&p.a, type, a.weight, 5, dims, strides, box);
+  } else {
+    e = encode_weights(&p.a, type, a.weight, a.n_in, a.n_out, a.E, row, expert, kDepth, kTileM);
+  }
   if (e != cudaSuccess) return e;
   p.offsets = a.expert_offsets;
   p.counts = a.expert_counts;
   p.E = a.E;
   p.R = static_cast<int32_t>(a.num_rows);
   p.n_red = a.n_in;
-  p.n_out = a.n_out;
+  p.n_m = a.n_out;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
   p.out = static_cast<uint8_t*>(a.out);
   p.out_stride = a.out_stride * 2;
   p.gate_up = static_cast<uint8_t*>(a.gate_up);
   p.gate_up_stride = a.gate_up_stride * 2;
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
-  return a.gated ? launch_rows<kGated, 1, BN>(a.act_dtype, a.num_rows, a.E, p, pdl, stream)
-                 : launch_rows<kForward, 1, BN>(a.act_dtype, a.num_rows, a.E, p, pdl, stream);
+  return a.gated ? launch_by_rows<kGated>(a.act_dtype, a.num_rows, a.E, a.rows, a.rows_stride, p, pdl, stream)
+                 : launch_by_rows<kForward>(a.act_dtype, a.num_rows, a.E, a.rows, a.rows_stride, p, pdl, stream);
 }
 
 cudaError_t launch_expert_rows_grad(const mfr_expert_matmul_backward_args& a, cudaStream_t stream) {
   Params p = {};
-  const CUtensorMapDataType type = map_type(a.act_dtype);
-  constexpr int BN = 256;
-  cudaError_t e = encode_map(&p.a, type, a.d_out, a.n_out, a.num_rows, 1, a.d_out_stride * 2, 0, kDepth, kTileM, 2);
-  if (e == cudaSuccess) e = encode_map(&p.a_small, type, a.d_out, a.n_out, a.num_rows, 1, a.d_out_stride * 2, 0, kDepth, kSmallRows, 2);
-  if (e == cudaSuccess)
-    e = encode_map(&p.b, type, a.weight, a.n_in, a.n_out, a.E, a.weight_stride * 2,
-                   (a.E > 1 ? a.weight_expert_stride : a.n_out * a.weight_stride) * 2, 64, kDepth, 3);
+  const cudaError_t e = encode_weights(&p.a, map_type(a.act_dtype), a.weight, a.n_in, a.n_out, a.E, a.weight_stride * 2,
+                                       (a.E > 1 ? a.weight_expert_stride : a.n_out * a.weight_stride) * 2, 64, kDepth);
   if (e != cudaSuccess) return e;
   p.offsets = a.expert_offsets;
   p.counts = a.expert_counts;
   p.E = a.E;
   p.R = static_cast<int32_t>(a.num_rows);
   p.n_red = a.n_out;
-  p.n_out = a.n_in;
+  p.n_m = a.n_in;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
   p.out = static_cast<uint8_t*>(a.d_rows);
   p.out_stride = a.d_rows_stride * 2;
-  return launch_rows<kRowsGrad, 1, BN>(a.act_dtype, a.num_rows, a.E, p, (a.flags & MFR_FLAG_PDL) != 0, stream);
+  return launch_by_rows<kRowsGrad>(a.act_dtype, a.num_rows, a.E, a.d_out, a.d_out_stride, p, (a.flags & MFR_FLAG_PDL) != 0, stream);
 }
+
+namespace {
+
+template <int Ctas>
+cudaError_t launch_weights(const mfr_expert_matmul_backward_args& a, Params& p, cudaStream_t stream) {
+  constexpr int BN = 256;
+  p.tiles_m = (a.n_out + kTileM * Ctas - 1) / (kTileM * Ctas);
+  p.tiles_n = (a.n_in + BN - 1) / BN;
+  const int64_t tiles = static_cast<int64_t>(a.E) * p.tiles_m * p.tiles_n;
+  const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
+  if (a.d_weight_dtype == MFR_FP32)
+    return a.act_dtype == MFR_BF16 ? launch<kWeightGrad, Ctas, BN, __nv_bfloat16, float>(p, tiles, pdl, stream)
+                                   : launch<kWeightGrad, Ctas, BN, __half, float>(p, tiles, pdl, stream);
+  return a.act_dtype == MFR_BF16 ? launch<kWeightGrad, Ctas, BN, __nv_bfloat16, __nv_bfloat16>(p, tiles, pdl, stream)
+                                 : launch<kWeightGrad, Ctas, BN, __half, __half>(p, tiles, pdl, stream);
+}
+
+}  // namespace
 
 cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, cudaStream_t stream) {
   const int64_t size = a.d_weight_dtype == MFR_FP32 ? 4 : 2;
@@ -414,28 +526,20 @@ cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, 
     return a.accumulate ? cudaSuccess : cudaMemsetAsync(a.d_weight, 0, static_cast<size_t>(a.E) * a.n_out * a.n_in * size, stream);
   Params p = {};
   const CUtensorMapDataType type = map_type(a.act_dtype);
-  constexpr int BN = 256;
-  cudaError_t e = encode_map(&p.a, type, a.d_out, a.n_out, a.num_rows, 1, a.d_out_stride * 2, 0, 64, kDepth, 2);
-  if (e == cudaSuccess) e = encode_map(&p.b, type, a.rows, a.n_in, a.num_rows, 1, a.rows_stride * 2, 0, 64, kDepth, 2);
+  cudaError_t e = encode_rows(&p.a, type, a.d_out, a.n_out, a.num_rows, a.d_out_stride * 2, 64, kDepth);
+  if (e == cudaSuccess) e = encode_rows(&p.b, type, a.rows, a.n_in, a.num_rows, a.rows_stride * 2, 64, kDepth);
+  if (e == cudaSuccess)
+    e = encode_weights(&p.d, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, a.d_weight, a.n_in, a.n_out, a.E, a.n_in * size,
+                       static_cast<int64_t>(a.n_out) * a.n_in * size, static_cast<int>(128 / size), kTileM);
   if (e != cudaSuccess) return e;
   p.offsets = a.expert_offsets;
   p.counts = a.expert_counts;
   p.E = a.E;
   p.R = static_cast<int32_t>(a.num_rows);
   p.n_m = a.n_out;
-  p.n_out = a.n_in;
-  p.tiles_m = (a.n_out + kTileM - 1) / kTileM;
-  p.tiles_n = (a.n_in + BN - 1) / BN;
+  p.n_n = a.n_in;
   p.accumulate = a.accumulate;
-  p.out = static_cast<uint8_t*>(a.d_weight);
-  p.out_stride = a.n_in * size;
-  const int64_t tiles = static_cast<int64_t>(a.E) * p.tiles_m * p.tiles_n;
-  const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
-  if (a.d_weight_dtype == MFR_FP32)
-    return a.act_dtype == MFR_BF16 ? launch<kWeightGrad, 1, BN, __nv_bfloat16, float>(p, tiles, pdl, stream)
-                                   : launch<kWeightGrad, 1, BN, __half, float>(p, tiles, pdl, stream);
-  return a.act_dtype == MFR_BF16 ? launch<kWeightGrad, 1, BN, __nv_bfloat16, __nv_bfloat16>(p, tiles, pdl, stream)
-                                 : launch<kWeightGrad, 1, BN, __half, __half>(p, tiles, pdl, stream);
+  return a.n_out > kTileM ? launch_weights<2>(a, p, stream) : launch_weights<1>(a, p, stream);
 }
 
 cudaError_t read_and_reset_expert_timeouts(unsigned int* count) {

@@ -272,9 +272,9 @@ cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cu
   Params p = {};
   constexpr CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const int64_t line = a.n_in / 2, wide = a.gated ? 2 * a.n_out : a.n_out;
-  cudaError_t e = encode_map(&p.a, type, a.codes, line, a.num_rows, 1, line, 0, 128, kTileM, 2);
-  if (e == cudaSuccess) e = encode_map(&p.a_small, type, a.codes, line, a.num_rows, 1, line, 0, 128, kSmallRows, 2);
-  if (e == cudaSuccess) e = encode_map(&p.b, type, a.weight_codes, line, wide, a.E, line, wide * line, 128, a.gated ? kTileN / 2 : kTileN, 3);
+  cudaError_t e = encode_rows(&p.a, type, a.codes, line, a.num_rows, line, 128, kTileM);
+  if (e == cudaSuccess) e = encode_rows(&p.a_small, type, a.codes, line, a.num_rows, line, 128, kSmallRows);
+  if (e == cudaSuccess) e = encode_weights(&p.b, type, a.weight_codes, line, wide, a.E, line, wide * line, 128, a.gated ? kTileN / 2 : kTileN);
   if (e != cudaSuccess) return e;
   p.offsets = a.expert_offsets;
   p.counts = a.expert_counts;

@@ -42,6 +42,7 @@ COUNTS = [
     ([17, 128, 0, 129, 0], 1, 7),
     ([65, 3, 0, 200], 128, 0),
     ([300], 8, 130),
+    ([256, 515, 0, 31], 1, 3),
 ]
 
 
@@ -79,7 +80,7 @@ def test_gradients_of_whole_numbers_are_exact(mfr, counts, align, free, n_in, n_
 
 
 @pytest.mark.parametrize("act", [BF, HF])
-@pytest.mark.parametrize("counts,align,free", COUNTS[2:5])
+@pytest.mark.parametrize("counts,align,free", COUNTS[2:])
 @pytest.mark.parametrize("gated", [False, True])
 def test_forward(mfr, act, counts, align, free, gated):
     n_in, n_out = 328, 168
@@ -104,7 +105,7 @@ def test_forward(mfr, act, counts, align, free, gated):
 
 
 @pytest.mark.parametrize("act", [BF, HF])
-@pytest.mark.parametrize("counts,align,free", COUNTS[2:5])
+@pytest.mark.parametrize("counts,align,free", COUNTS[2:])
 def test_backward(mfr, act, counts, align, free):
     n_in, n_out = 168, 328
     x, off, cnt, g = _case(counts, n_in, act, 6, align, free)
@@ -270,7 +271,7 @@ def test_nvfp4_whole_numbers_are_exact(mfr, counts, align, free, n_in, n_out):
 
 
 @pytest.mark.parametrize("act", [BF, HF])
-@pytest.mark.parametrize("counts,align,free", COUNTS[2:5])
+@pytest.mark.parametrize("counts,align,free", COUNTS[2:])
 @pytest.mark.parametrize("gated", [False, True])
 def test_nvfp4_product(mfr, act, counts, align, free, gated):
     n_in, n_out = 832, 256
