@@ -56,8 +56,8 @@ struct Shape {
   static constexpr int kBRows = BN / Ctas;  // columns of D whose operand this CTA copies
   static constexpr int kBBytes = kBRows * kDepth * 2;
   static constexpr int kStage = kABytes + kBBytes;
-  // the weights' gradient leaves by two buffers of 128 lines of 128 bytes
-  static constexpr int kOutBytes = D == kWeightGrad ? kTileM * 128 : 0;
+  // results leave by two buffers: 128 lines of 128 bytes of the weights' gradient, or 32 rows of the tile's values
+  static constexpr int kOutBytes = D == kWeightGrad ? kTileM * 128 : 32 * kTileM * 2;
   static constexpr int kStages = D == kWeightGrad ? 196608 / kStage : 204800 / kStage;
   static constexpr bool kALines = D == kRowsGrad || D == kWeightGrad;
   static constexpr bool kBLines = D == kWeightGrad;
@@ -111,6 +111,18 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
 template <typename T>
 __device__ __forceinline__ T to_act(float v) {
   if constexpr (kIsBf16<T>) return __float2bfloat16_rn(v); else return __float2half_rn(v);
+}
+
+// `rows` rows of `Line` bytes, `pitch` bytes apart in shared memory, to rows of an output, by the 128 threads of the epilogue;
+// of each row the first `values` values that are there.
+template <int Line>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t stride, const uint8_t* box, int pitch, int rows, int values) {
+  constexpr int kPieces = Line / 16;  // threads a row
+  const int piece = threadIdx.x % kPieces;
+  if (piece * 8 >= values) return;
+#pragma unroll
+  for (int j = threadIdx.x % 128 / kPieces; j < 32; j += 128 / kPieces)
+    if (j < rows) *reinterpret_cast<uint4*>(out + j * stride + piece * 16) = *reinterpret_cast<const uint4*>(box + j * pitch + piece * 16);
 }
 
 // Zeros, by one warp, in the lines from `from` on of a stage whose operands' lines are steps of the reduction: they hold rows
@@ -249,26 +261,22 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         }
         continue;
       }
-      // (one thread waits and issues; the others go ahead to where they are needed, or to the tile's end)
-      if (lane == 0) {
-        ok = wait_phase(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts);
-        tmem_fence_after();
-      }
+      if (!(ok = __all_sync(0xffffffffu, wait_phase(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
+      tmem_fence_after();
       for (int k = 0; k < steps; ++k) {
-        if (lane == 0) ok = ok && wait_phase(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts);
+        if (!(ok = __all_sync(0xffffffffu, wait_phase(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts)))) break;
         const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
         if constexpr (D == kWeightGrad) {
           if (k == steps - 1 && last < kDepth) {
-            if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
             clear_lines<S::kBRows>(a, last);
             if constexpr (Ctas == 2) {
-              if (lane == 0) ok = wait_phase(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts);
+              if (!(ok = __all_sync(0xffffffffu, wait_phase(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
               tail_phase ^= 1u << s;
             }
           }
         }
-        if (lane == 0 && ok) {
-          tmem_fence_after();
+        tmem_fence_after();
+        if (lane == 0) {
           const uint64_t da = S::kALines ? swizzled_desc(a, 1024, 64 * kDepth * 2) : swizzled_desc(a, 1024, 16);
           const uint64_t db = S::kBLines ? swizzled_desc(b, 1024, 64 * kDepth * 2) : swizzled_desc(b, 1024, 16);
 #pragma unroll
@@ -277,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           mma_commit<Ctas>(empty0 + 8 * s);
           if (k == steps - 1) mma_commit<Ctas>(dfull0 + 8 * buf);
         }
+        __syncwarp();
         if (++s == S::kStages) { s = 0; phase ^= 1; }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (buf ^= 1; buf == 0) dphase ^= 1;
     }
   } else if (warp < kEpilogueWarp) {
@@ -294,13 +302,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     // ---- finished accumulators
     const int quarter = warp - kEpilogueWarp;
     uint32_t buf = 0, dphase = 0;
-    int stored = 0;  // (weights' gradient) boxes so far
+    int stored = 0;  // buffers so far
     for (uint32_t t = t0; t < tiles; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
       const bool some = x.steps > 0;
       if (some) {
         const bool ok = wait_phase(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
-        if (D == kWeightGrad ? !named_all(1, 128, ok) : !__all_sync(0xffffffffu, ok)) break;  // (the warps of the first share their stores)
+        if (!named_all(1, 128, ok)) break;  // (the four warps share their stores)
         tmem_fence_after();
       }
       const uint32_t d = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -352,43 +360,47 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             if (threadIdx.x == kEpilogueWarp * 32) tma_store_commit();
           }
         }
-      } else if constexpr (D == kGated) {
-        // lanes 0..7 of each 16 hold gates, 8..15 the others; each of the two computes every second row
-        const int f = x.m0 + rank * (kTileM / 2) + r / 16 * 8 + r % 8;
-        const bool upper = (r & 8) != 0, live = f < p.n_m;
-        T* out = reinterpret_cast<T*>(p.out + static_cast<int64_t>(x.row0) * p.out_stride) + f;
-        T* kept = reinterpret_cast<T*>(p.gate_up + static_cast<int64_t>(x.row0) * p.gate_up_stride) + (upper ? p.n_m : 0) + f;
-#pragma unroll 1
-        for (int c = 0; c < x.rows; c += 32) {
-          uint32_t v[32];
-          tmem_load32(d + c, v);
-          tmem_wait_load();
-          if (p.gate_up != nullptr && live) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < x.rows) *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(kept) + (c + j) * p.gate_up_stride) = to_act<T>(__uint_as_float(v[j]));
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
-            const float y = swiglu(__uint_as_float(upper ? other : v[j]), __uint_as_float(upper ? v[j + 1] : other));
-            const int row = c + j + (upper ? 1 : 0);
-            if (live && row < x.rows) *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(out) + row * p.out_stride) = to_act<T>(y);
-          }
-        }
       } else {
-        // 32 neighbouring values of one row in a warp: whole sectors
-        const int f = x.m0 + rank * kTileM + r;
-        uint8_t* out = p.out + static_cast<int64_t>(x.row0) * p.out_stride + static_cast<int64_t>(f) * 2;
+        // A thread has one value of 32 rows; through shared memory, where 16 (gated: 8) threads find 16 bytes each of a row.
+        // Storing from the registers, 2 bytes a thread, took 10 us a tile, more than most reductions.
+        constexpr int kLine = S::kFeatures / Ctas * 2;  // bytes of a row in this CTA's tile
+        const int f0 = x.m0 + rank * (S::kFeatures / Ctas);
+        const int64_t at = static_cast<int64_t>(f0) * 2;
 #pragma unroll 1
         for (int c = 0; c < x.rows; c += 32) {
           uint32_t v[32];
           tmem_load32(d + c, v);
           tmem_wait_load();
-          if (f < p.n_m) {
+          const int rows = x.rows - c < 32 ? x.rows - c : 32;
+          const int64_t row = static_cast<int64_t>(x.row0) + c;
+          if constexpr (D == kGated) {
+            // lanes 0..7 of each 16 hold gates, 8..15 the others; each of the two computes every second row
+            const int f = r / 16 * 8 + r % 8;
+            const bool upper = (r & 8) != 0;
+            if (p.gate_up != nullptr) {
+              uint8_t* box = smem + S::kStages * S::kStage + (stored++ & 1) * S::kOutBytes;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < x.rows) *reinterpret_cast<T*>(out + (c + j) * p.out_stride) = to_act<T>(__uint_as_float(v[j]));
+              for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kTileM + (upper ? kTileM / 2 : 0) + f] = to_act<T>(__uint_as_float(v[j]));
+              named_sync(1, 128);
+              store_rows<kLine>(p.gate_up + row * p.gate_up_stride + at, p.gate_up_stride, box, 2 * kLine, rows, p.n_m - f0);
+              store_rows<kLine>(p.gate_up + row * p.gate_up_stride + at + static_cast<int64_t>(p.n_m) * 2, p.gate_up_stride, box + kLine, 2 * kLine, rows,
+                                p.n_m - f0);
+            }
+            uint8_t* box = smem + S::kStages * S::kStage + (stored++ & 1) * S::kOutBytes;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
+              const float y = swiglu(__uint_as_float(upper ? other : v[j]), __uint_as_float(upper ? v[j + 1] : other));
+              reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kTileM / 2) + f] = to_act<T>(y);
+            }
+            named_sync(1, 128);
+            store_rows<kLine>(p.out + row * p.out_stride + at, p.out_stride, box, kLine, rows, p.n_m - f0);
+          } else {
+            uint8_t* box = smem + S::kStages * S::kStage + (stored++ & 1) * S::kOutBytes;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kTileM + r] = to_act<T>(__uint_as_float(v[j]));
+            named_sync(1, 128);
+            store_rows<kLine>(p.out + row * p.out_stride + at, p.out_stride, box, kLine, rows, p.n_m - f0);
           }
         }
       }
