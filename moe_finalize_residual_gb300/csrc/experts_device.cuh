@@ -13,11 +13,14 @@ constexpr uint64_t kExpertWaitNs = 2000000000ull;
 
 // Bounded wait on an mbarrier phase: false if the CTA is giving up or the limit (about 2 s) ran out; that is counted, and
 // starts the giving up.
+// Ctas 2: of arrivals from both CTAs of a pair.
+template <int Ctas>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* give_up, unsigned int* timeouts) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const auto arrived = [&] { return Ctas == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity); };
+  if (arrived()) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (arrived()) return true;
     if ((it & 15u) == 0) {
       if (*give_up) return false;
       if (global_timer_ns() - t0 > kExpertWaitNs) {
@@ -109,8 +112,94 @@ __device__ __forceinline__ void zero_free_rows(uint8_t* out, int64_t stride_byte
   }
 }
 
-// g / (1 + exp(-g)) * u; where exp(-g) is infinite the quotient is 0.
-__device__ __forceinline__ float swiglu(float g, float u) { return g * __frcp_rn(1.0f + __expf(-g)) * u; }
+// g / (1 + exp(-g)) * u.  The quotient is 0 below g = -87, where it is smaller than 1e-35 (the fast division's largest divisor
+// is 2^126).
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// ------------------------------------------------------------------------------------------------
+// Results
+// ------------------------------------------------------------------------------------------------
+
+template <typename T> constexpr bool kIsBf16 = false;
+template <> constexpr bool kIsBf16<__nv_bfloat16> = true;
+
+template <typename T>
+__device__ __forceinline__ T to_act(float v) {
+  if constexpr (kIsBf16<T>) return __float2bfloat16_rn(v); else return __float2half_rn(v);
+}
+
+// `rows` rows of `Line` bytes, `pitch` bytes apart in shared memory, to rows of an output, by the 128 threads of the epilogue;
+// of each row the first `values` values that are there.
+template <int Line>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t stride, const uint8_t* box, int pitch, int rows, int values) {
+  constexpr int kPieces = Line / 16;  // threads a row
+  const int piece = threadIdx.x % kPieces;
+  if (piece * 8 >= values) return;
+#pragma unroll
+  for (int j = threadIdx.x % 128 / kPieces; j < 32; j += 128 / kPieces)
+    if (j < rows) *reinterpret_cast<uint4*>(out + j * stride + piece * 16) = *reinterpret_cast<const uint4*>(box + j * pitch + piece * 16);
+}
+
+// Where the products' rows go: strides in bytes, `n` values a row; gate_up may be NULL.
+struct RowsOut {
+  uint8_t* out;
+  int64_t out_stride;
+  uint8_t* gate_up;
+  int64_t gate_up_stride;
+  int32_t n;
+};
+
+// One CTA's part of a finished tile, by the 128 threads of the epilogue: 128 lanes of tensor memory at `d` (this warp's
+// quarter), the values f0.. of the rows row0 .. row0 + rows - 1, a column each, times `alpha`.  Gated, the lanes hold 8 gates,
+// their 8 others, and so on.  A thread has one value of 32 rows; through shared memory (two buffers of 8 KB at `boxes`),
+// where 16 (gated: 8) threads find 16 bytes each of a row: storing from the registers, 2 bytes a thread, took 10 us a tile of
+// 256 rows, more than most reductions, and this 3.4.
+template <typename T, bool Gated>
+__device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, int f0, float alpha, const RowsOut& to, uint8_t* boxes, int& stored) {
+  constexpr int kLanes = 128, kLine = (Gated ? kLanes / 2 : kLanes) * 2;  // bytes of a row in this CTA's tile
+  const int r = threadIdx.x % kLanes;
+  const int64_t at = static_cast<int64_t>(f0) * 2;
+#pragma unroll 1
+  for (int c = 0; c < rows_all; c += 32) {
+    uint32_t w[32];
+    tmem_load32(d + c, w);
+    tmem_wait_load();
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * alpha;
+    const int rows = rows_all - c < 32 ? rows_all - c : 32;
+    const int64_t row = static_cast<int64_t>(row0) + c;
+    if constexpr (Gated) {
+      // lanes 0..7 of each 16 and 8..15 exchange, and each of the two computes every second row
+      const int f = r / 16 * 8 + r % 8;
+      const bool upper = (r & 8) != 0;
+      if (to.gate_up != nullptr) {
+        uint8_t* box = boxes + (stored++ & 1) * (32 * kLanes * 2);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kLanes + (upper ? kLanes / 2 : 0) + f] = to_act<T>(v[j]);
+        named_sync(1, 128);
+        store_rows<kLine>(to.gate_up + row * to.gate_up_stride + at, to.gate_up_stride, box, 2 * kLine, rows, to.n - f0);
+        store_rows<kLine>(to.gate_up + row * to.gate_up_stride + at + static_cast<int64_t>(to.n) * 2, to.gate_up_stride, box + kLine, 2 * kLine, rows,
+                          to.n - f0);
+      }
+      uint8_t* box = boxes + (stored++ & 1) * (32 * kLanes * 2);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
+        const float y = swiglu(upper ? other : v[j], upper ? v[j + 1] : other);
+        reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kLanes / 2) + f] = to_act<T>(y);
+      }
+      named_sync(1, 128);
+      store_rows<kLine>(to.out + row * to.out_stride + at, to.out_stride, box, kLine, rows, to.n - f0);
+    } else {
+      uint8_t* box = boxes + (stored++ & 1) * (32 * kLanes * 2);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kLanes + r] = to_act<T>(v[j]);
+      named_sync(1, 128);
+      store_rows<kLine>(to.out + row * to.out_stride + at, to.out_stride, box, kLine, rows, to.n - f0);
+    }
+  }
+}
 
 // ------------------------------------------------------------------------------------------------
 // Tensor maps (host)
@@ -130,14 +219,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // A map of `rank` dimensions (the first one's values next to one another, `strides` in bytes those of the others) with boxes
-// of `box` values, the first 128 bytes, in the 128-byte swizzle; what lies outside reads as zeros.
+// of `box` values, by default the first 128 bytes, in the 128-byte swizzle; what lies outside reads as zeros.
 inline cudaError_t encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* data, int rank, const cuuint64_t* dims,
-                              const cuuint64_t* strides, const cuuint32_t* box) {
+                              const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const auto f = tensor_map_encoder();
   if (f == nullptr) return cudaErrorNotSupported;
   const cuuint32_t step[5] = {1, 1, 1, 1, 1};
   const CUresult r = f(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(data), dims, strides, box, step,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -154,6 +243,16 @@ inline cudaError_t encode_weights(CUtensorMap* map, CUtensorMapDataType type, co
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sy), static_cast<cuuint64_t>(sz)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(bx), static_cast<cuuint32_t>(by), 1};
   return encode_map(map, type, data, 3, dims, strides, box);
+}
+
+// The same, gated: `n` gates' rows and `n` others an expert, n a multiple of 8, in boxes of 8 and 8 rows alternately, 128 in all.
+inline cudaError_t encode_gated_weights(CUtensorMap* map, CUtensorMapDataType type, const void* data, int64_t nx, int64_t n, int64_t nz, int64_t sy,
+                                        int64_t sz, int bx) {
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(nx), 8, 2, static_cast<cuuint64_t>(n / 8), static_cast<cuuint64_t>(nz)};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(sy), static_cast<cuuint64_t>(n * sy), static_cast<cuuint64_t>(8 * sy),
+                                 static_cast<cuuint64_t>(sz)};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(bx), 8, 2, 8, 1};
+  return encode_map(map, type, data, 5, dims, strides, box);
 }
 
 // SMs of the current device.

@@ -33,23 +33,17 @@ constexpr int kABytes = kTileM * kDepth * 2;
 constexpr int kBoxRows = 32;                     // rows of a small box of B
 constexpr int kBarBytes = 512;
 
-template <typename T> constexpr bool kIsBf16 = false;
-template <> constexpr bool kIsBf16<__nv_bfloat16> = true;
-
 struct Params {
   CUtensorMap a, b, b_small, d;  // (d: the weights' gradient)
   const int32_t* offsets;
   const int32_t* counts;
   int32_t E, R;
   int32_t n_red;       // reduction length (the weights' gradient: the expert's rows)
-  int32_t n_m;         // values of an output row (the weights' gradient: rows of D)
+  int32_t n_m;         // values of an output row, as in `to` (the weights' gradient: rows of D)
   int32_t n_n;         // the weights' gradient: columns of D
   int32_t tiles_m, tiles_n;  // row tiles of D; the weights' gradient: column tiles
   int32_t zero_free, accumulate;
-  uint8_t* out;
-  int64_t out_stride;  // bytes
-  uint8_t* gate_up;
-  int64_t gate_up_stride;
+  RowsOut to;          // (but for the weights' gradient)
 };
 
 template <int D, int Ctas, int BN>
@@ -107,23 +101,6 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     x.chunks = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
   }
   return x;
-}
-
-template <typename T>
-__device__ __forceinline__ T to_act(float v) {
-  if constexpr (kIsBf16<T>) return __float2bfloat16_rn(v); else return __float2half_rn(v);
-}
-
-// `rows` rows of `Line` bytes, `pitch` bytes apart in shared memory, to rows of an output, by the 128 threads of the epilogue;
-// of each row the first `values` values that are there.
-template <int Line>
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t stride, const uint8_t* box, int pitch, int rows, int values) {
-  constexpr int kPieces = Line / 16;  // threads a row
-  const int piece = threadIdx.x % kPieces;
-  if (piece * 8 >= values) return;
-#pragma unroll
-  for (int j = threadIdx.x % 128 / kPieces; j < 32; j += 128 / kPieces)
-    if (j < rows) *reinterpret_cast<uint4*>(out + j * stride + piece * 16) = *reinterpret_cast<const uint4*>(box + j * pitch + piece * 16);
 }
 
 // Zeros, by one warp, in the lines from `from` on of a stage's chunk whose operands' lines are steps of the reduction: they
@@ -203,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const int boxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
         const uint32_t bytes = kABytes + (D == kWeightGrad || whole ? S::kBBytes : boxes * kBoxRows * kDepth * 2);
         for (int k = 0; k < x.chunks; k += kChunks) {
-          if (!(ok = wait_phase(empty0 + 8 * s, phase ^ 1, give_up, &g_expert_wait_timeouts))) break;
+          if (!(ok = wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, &g_expert_wait_timeouts))) break;
           const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
           uint32_t bar = full0 + 8 * s;
           if (Ctas == 2 && D == kWeightGrad && x.rows < (k + n) * kDepth) {
@@ -268,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           const int n = x.chunks % kChunks == 0 ? kChunks : x.chunks % kChunks;  // chunks of the last stage
           s = (s + (x.chunks - 1) / kChunks) % S::kStages;
           if (last < kDepth) {
-            if (!(ok = __all_sync(0xffffffffu, wait_phase(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
+            if (!(ok = __all_sync(0xffffffffu, wait_phase<1>(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
             tail_phase ^= 1u << s;
             clear_lines<S>(stage0 + s * S::kStage, n - 1, last);
             if (lane == 0) mbar_arrive_cluster(cluster_addr(ready0 + 8 * s, 0));
@@ -277,16 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         }
         continue;
       }
-      if (!(ok = __all_sync(0xffffffffu, wait_phase(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
       tmem_fence_after();
       for (int k = 0; k < x.chunks; k += kChunks) {
         const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
-        if (!(ok = __all_sync(0xffffffffu, wait_phase(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts)))) break;
         if constexpr (D == kWeightGrad) {
           if (k + n == x.chunks && last < kDepth) {
             clear_lines<S>(stage0 + s * S::kStage, n - 1, last);
             if constexpr (Ctas == 2) {
-              if (!(ok = __all_sync(0xffffffffu, wait_phase(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
+              if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
               tail_phase ^= 1u << s;
             }
           }
@@ -315,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     // ---- rows of no expert
     if (D != kWeightGrad && p.zero_free) {
       const int w = blockIdx.x * 2 + warp - 2, nw = gridDim.x * 2;
-      zero_free_rows(p.out, p.out_stride, static_cast<int64_t>(p.n_m) * 2, p.offsets, p.counts, p.E, p.R, w, nw);
-      if (D == kGated && p.gate_up != nullptr)
-        zero_free_rows(p.gate_up, p.gate_up_stride, static_cast<int64_t>(p.n_m) * 4, p.offsets, p.counts, p.E, p.R, w, nw);
+      zero_free_rows(p.to.out, p.to.out_stride, static_cast<int64_t>(p.n_m) * 2, p.offsets, p.counts, p.E, p.R, w, nw);
+      if (D == kGated && p.to.gate_up != nullptr)
+        zero_free_rows(p.to.gate_up, p.to.gate_up_stride, static_cast<int64_t>(p.n_m) * 4, p.offsets, p.counts, p.E, p.R, w, nw);
     }
   } else {
     // ---- finished accumulators
@@ -328,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
       const bool some = x.chunks > 0;
       if (some) {
-        const bool ok = wait_phase(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
+        const bool ok = wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
         if (!named_all(1, 128, ok)) break;  // (the four warps share their stores)
         tmem_fence_after();
       }
@@ -382,48 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           }
         }
       } else {
-        // A thread has one value of 32 rows; through shared memory, where 16 (gated: 8) threads find 16 bytes each of a row.
-        // Storing from the registers, 2 bytes a thread, took 10 us a tile, more than most reductions.
-        constexpr int kLine = S::kFeatures / Ctas * 2;  // bytes of a row in this CTA's tile
-        const int f0 = x.m0 + rank * (S::kFeatures / Ctas);
-        const int64_t at = static_cast<int64_t>(f0) * 2;
-#pragma unroll 1
-        for (int c = 0; c < x.rows; c += 32) {
-          uint32_t v[32];
-          tmem_load32(d + c, v);
-          tmem_wait_load();
-          const int rows = x.rows - c < 32 ? x.rows - c : 32;
-          const int64_t row = static_cast<int64_t>(x.row0) + c;
-          if constexpr (D == kGated) {
-            // lanes 0..7 of each 16 hold gates, 8..15 the others; each of the two computes every second row
-            const int f = r / 16 * 8 + r % 8;
-            const bool upper = (r & 8) != 0;
-            if (p.gate_up != nullptr) {
-              uint8_t* box = smem + S::kStages * S::kStage + (stored++ & 1) * S::kOutBytes;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kTileM + (upper ? kTileM / 2 : 0) + f] = to_act<T>(__uint_as_float(v[j]));
-              named_sync(1, 128);
-              store_rows<kLine>(p.gate_up + row * p.gate_up_stride + at, p.gate_up_stride, box, 2 * kLine, rows, p.n_m - f0);
-              store_rows<kLine>(p.gate_up + row * p.gate_up_stride + at + static_cast<int64_t>(p.n_m) * 2, p.gate_up_stride, box + kLine, 2 * kLine, rows,
-                                p.n_m - f0);
-            }
-            uint8_t* box = smem + S::kStages * S::kStage + (stored++ & 1) * S::kOutBytes;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
-              const float y = swiglu(__uint_as_float(upper ? other : v[j]), __uint_as_float(upper ? v[j + 1] : other));
-              reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kTileM / 2) + f] = to_act<T>(y);
-            }
-            named_sync(1, 128);
-            store_rows<kLine>(p.out + row * p.out_stride + at, p.out_stride, box, kLine, rows, p.n_m - f0);
-          } else {
-            uint8_t* box = smem + S::kStages * S::kStage + (stored++ & 1) * S::kOutBytes;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kTileM + r] = to_act<T>(__uint_as_float(v[j]));
-            named_sync(1, 128);
-            store_rows<kLine>(p.out + row * p.out_stride + at, p.out_stride, box, kLine, rows, p.n_m - f0);
-          }
-        }
+        store_tile<T, D == kGated>(d, x.rows, x.row0, x.m0 + rank * (S::kFeatures / Ctas), 1.0f, p.to, smem + S::kStages * S::kStage, stored);
       }
       if (some) {
         tmem_fence_before();
@@ -493,11 +429,7 @@ cudaError_t launch_expert_matmul(const mfr_expert_matmul_args& a, cudaStream_t s
   const int64_t expert = (a.E > 1 ? a.weight_expert_stride * 2 : wide * row);
   cudaError_t e;
   if (a.gated) {
-    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(a.n_in), 8, 2, static_cast<cuuint64_t>(a.n_out / 8), static_cast<cuuint64_t>(a.E)};
-    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(a.n_out * row), static_cast<cuuint64_t>(8 * row),
-                                   static_cast<cuuint64_t>(expert)};
-    const cuuint32_t box[5] = {kDepth, 8, 2, kTileM / 16, 1};
-    e = encode_map(&p.a, type, a.weight, 5, dims, strides, box);
+    e = encode_gated_weights(&p.a, type, a.weight, a.n_in, a.n_out, a.E, row, expert, kDepth);
   } else {
     e = encode_weights(&p.a, type, a.weight, a.n_in, a.n_out, a.E, row, expert, kDepth, kTileM);
   }
@@ -509,10 +441,7 @@ cudaError_t launch_expert_matmul(const mfr_expert_matmul_args& a, cudaStream_t s
   p.n_red = a.n_in;
   p.n_m = a.n_out;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
-  p.out = static_cast<uint8_t*>(a.out);
-  p.out_stride = a.out_stride * 2;
-  p.gate_up = static_cast<uint8_t*>(a.gate_up);
-  p.gate_up_stride = a.gate_up_stride * 2;
+  p.to = {static_cast<uint8_t*>(a.out), a.out_stride * 2, static_cast<uint8_t*>(a.gate_up), a.gate_up_stride * 2, a.n_out};
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
   return a.gated ? launch_by_rows<kGated>(a.act_dtype, a.num_rows, a.E, a.rows, a.rows_stride, p, pdl, stream)
                  : launch_by_rows<kForward>(a.act_dtype, a.num_rows, a.E, a.rows, a.rows_stride, p, pdl, stream);
@@ -530,8 +459,7 @@ cudaError_t launch_expert_rows_grad(const mfr_expert_matmul_backward_args& a, cu
   p.n_red = a.n_out;
   p.n_m = a.n_in;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
-  p.out = static_cast<uint8_t*>(a.d_rows);
-  p.out_stride = a.d_rows_stride * 2;
+  p.to = {static_cast<uint8_t*>(a.d_rows), a.d_rows_stride * 2, nullptr, 0, a.n_in};
   return launch_by_rows<kRowsGrad>(a.act_dtype, a.num_rows, a.E, a.d_out, a.d_out_stride, p, (a.flags & MFR_FLAG_PDL) != 0, stream);
 }
 

@@ -1,10 +1,12 @@
 // The experts' NVFP4 product: rows in expert order times their experts' weights, both as E2M1 codes with an E4M3 scale for
 // every 16 values, on the fifth-generation tensor cores, which take codes and scales as they are.
 //
-// The kernel is that of the 16-bit products (kernel_experts.cu): persistent CTAs, tiles of 128 rows x 256 columns, operands by
-// tensor copies, the accumulator in tensor memory.  A stage is 256 values of the reduction.  The weights' scales lie in the
-// tiles that tensor memory wants and are copied as they are; the rows' scales are row-major (rows begin anywhere), so four
-// warps, a stage each in turn, put them into that order on their way through shared memory.
+// The kernel is that of the 16-bit products (kernel_experts.cu): weight rows in the lanes of tensor memory, an expert's rows
+// as its columns, persistent CTAs or pairs of them, operands by tensor copies, results through shared memory.  A stage is 256
+// values of the reduction.  The scales take a second way: tensor memory wants them in blocks of 128 rows x 4 scales, which
+// the issuing thread copies there from shared memory before each stage's instructions.  The weights' lie in such tiles and
+// come by tensor copies as they are; gated, where a tile's lanes are 8 gates and 8 others alternately, and for the rows, whose
+// scales are row-major since rows begin anywhere, six warps, a stage each in turn, put them in order.
 #include "experts_device.cuh"
 
 namespace mfr {
@@ -13,27 +15,20 @@ __device__ unsigned int g_expert_nvfp4_wait_timeouts = 0;
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 448;
 constexpr int kEpilogueWarp = 4;  // first of four
-constexpr int kScaleWarp = 8;     // first of four
+constexpr int kScaleWarp = 8;     // first of six
+constexpr int kScaleWarps = 6;
 constexpr int kDepth = 256;       // reduction values of a stage: lines of 128 bytes
 constexpr int kTileM = kExpertTileRows;
-constexpr int kTileN = 256;
-constexpr int kABytes = kTileM * kDepth / 2;
-constexpr int kBBytes = kTileN * kDepth / 2;
+constexpr int kABytes = kTileM * 128;
 constexpr int kSfaBytes = kTileM * kDepth / 16;
-constexpr int kSfbBytes = kTileN * kDepth / 16;
-constexpr int kStage = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-constexpr int kStages = 4;
-constexpr int kSmallRows = 16;
-constexpr int kBarBytes = 256;
-constexpr int kSmem = 1024 + kStages * kStage + kBarBytes + (MFR_MAX_EXPERTS + 1 + 33) * 4;
-constexpr uint32_t kSfColumn = 256;                          // tensor-memory columns: D, then the stages' scales
-constexpr uint32_t kSfColumns = (kSfaBytes + kSfbBytes) / 128;  // of a stage: 4 bytes a lane and column
-static_assert(kSfColumn + kStages * kSfColumns <= 512, "tensor memory");
+constexpr int kBoxRows = 32;      // rows of a box of B
+constexpr int kBarBytes = 512;
+constexpr int kOutBytes = 32 * kTileM * 2;
 
 struct Params {
-  CUtensorMap a, a_small, b;
+  CUtensorMap a, b, b_small, sfa;  // (sfa: not gated, 512 bytes of 4 columns of a tile a row)
   const int32_t* offsets;
   const int32_t* counts;
   const uint8_t* sf;         // rows' scales, row-major
@@ -41,69 +36,99 @@ struct Params {
   const float* alpha;
   int32_t E, R;
   int32_t n_in, n_out;
-  int32_t tiles_n;
+  int32_t tiles_m;
   int32_t sf_tiles;          // tiles of 128 weight rows an expert
   int32_t zero_free;
-  uint8_t* out;
-  int64_t out_stride;        // bytes
+  RowsOut to;
+};
+
+template <bool Gated, int Ctas, int BN>
+struct Shape {
+  static constexpr int kBRows = BN / Ctas;  // rows whose codes this CTA copies (their scales: all BN)
+  static constexpr int kBBytes = kBRows * 128;
+  static constexpr int kSfBlocks = (BN + 127) / 128;  // blocks of 128 rows' scales
+  static constexpr int kSfbBytes = kSfBlocks * 128 * kDepth / 16;
+  static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  static constexpr int kStage = (kStageBytes + 1023) / 1024 * 1024;
+  static constexpr int kStages = 209920 / kStage;
+  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kOutBytes + kBarBytes + (MFR_MAX_EXPERTS + 1 + 33) * 4;
+  static constexpr int kFeatures = (Gated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
+  static constexpr int kUnit = Ctas == 1 ? 16 : 32;
+  // tensor-memory columns: two accumulators, then areas of a stage's scales, 4 bytes a lane and column
+  static constexpr uint32_t kSfColumns = (kSfaBytes + kSfbBytes) / 128;
+  static constexpr int kAreas = 2;
+  static_assert(2 * BN + kAreas * kSfColumns <= 512 && kStageBytes % 512 == 0 && kBBytes % 1024 == 0, "tensor memory, alignment");
+  static_assert(kSmem <= 232448, "shared memory");
+  // (a warp that waits for its stage's place has filled the stage kScaleWarps before; were they more than the places, that
+  // place could be two turns behind, which its parity does not show)
+  static_assert(kScaleWarps <= kStages, "scale warps");
 };
 
 struct Tile {
-  int e, row0, left, n0;
+  int e, row0, rows, m0;
 };
 
-template <bool Gated>
+template <bool Gated, int Ctas, int BN>
 __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint32_t t) {
+  using S = Shape<Gated, Ctas, BN>;
   Tile x;
-  const int m = t / p.tiles_n;
-  x.n0 = t % p.tiles_n * (Gated ? kTileN / 2 : kTileN);
+  const int m = t / p.tiles_m;
+  x.m0 = t % p.tiles_m * S::kFeatures;
   x.e = tile_expert(first, p.E, m);
   const RowSpan s = expert_rows(p.offsets, p.counts, x.e, p.R);
-  x.row0 = s.begin + (m - first[x.e]) * kTileM;
-  x.left = s.end - x.row0;
+  const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
+  const int part = ((n + parts - 1) / parts + S::kUnit - 1) / S::kUnit * S::kUnit;
+  const int at = (m - first[x.e]) * part;
+  x.row0 = s.begin + at;
+  x.rows = n - at < part ? n - at : part;
   return x;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
+__device__ __forceinline__ void sts32(uint32_t dst, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory"); }
 
-template <bool Gated, typename T>
+template <bool Gated, int Ctas, int BN, typename T>
 __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_constant__ Params p) {
+  using S = Shape<Gated, Ctas, BN>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const uint32_t stage0 = smem_addr(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
-  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kStages, dfull = empty0 + 8 * kStages, dempty = dfull + 8;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 2);
+  uint8_t* boxes = smem + S::kStages * S::kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + 2 * kOutBytes);
+  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * S::kStages, sf0 = empty0 + 8 * S::kStages;
+  const uint32_t dfull0 = sf0 + 8 * S::kStages, dempty0 = dfull0 + 16;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 3 * S::kStages + 4);
   volatile int* give_up = reinterpret_cast<volatile int*>(tmem_at + 1);
-  int* first = reinterpret_cast<int*>(smem + kStages * kStage + kBarBytes);
+  int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
+  static_assert((3 * S::kStages + 5) * 8 <= kBarBytes, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = Ctas == 2 ? cluster_ctarank() : 0;
   unsigned int* const timeouts = &g_expert_nvfp4_wait_timeouts;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 2);  // the copies' bytes, and the rows' scales
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);    // the copies' bytes
+      mbar_init(sf0 + 8 * s, Ctas);   // the scales that the warps put in order
       mbar_init(empty0 + 8 * s, 1);
     }
-    mbar_init(dfull, 1);
-    mbar_init(dempty, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(dfull0 + 8 * i, 1);
+      mbar_init(dempty0 + 8 * i, 4 * Ctas);
+    }
     *give_up = 0;
     fence_mbar_init();
     tma_prefetch_map(&p.a);
     tma_prefetch_map(&p.b);
   }
-  if (warp == 2) tmem_alloc<1>(smem_addr(tmem_at), 512);
+  if (warp == 2) tmem_alloc<Ctas>(smem_addr(tmem_at), 512);
   pdl_launch_dependents();
   pdl_wait();
-  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, kTileM);
+  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, BN);
   tmem_fence_before();
-  __syncthreads();
+  if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_at;
-  const uint32_t tiles = static_cast<uint32_t>(first[p.E]) * p.tiles_n;
-  const int steps = (p.n_in + kDepth - 1) / kDepth;
+  const uint32_t tiles = static_cast<uint32_t>(first[p.E]) * p.tiles_m;
+  const uint32_t t0 = blockIdx.x / Ctas, dt = gridDim.x / Ctas;
   const int chunks = p.n_in / 64;  // instructions a tile, and columns of 512 bytes of the scales' tiles
 
   if (warp == 0) {
@@ -111,30 +136,35 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
     if (lane == 0) {
       uint32_t s = 0, phase = 0;
       bool ok = true;
-      for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile x = tile_at<Gated>(p, first, t);
-        const int small = x.left <= 64 ? (x.left + kSmallRows - 1) / kSmallRows : 0;
-        const int sf0 = x.n0 / 128, sf1 = Gated ? (p.n_out + x.n0) / 128 : sf0 + 1;
-        const int n_sf = sf1 < p.sf_tiles ? 2 : 1;  // (the last tile of columns may hold 128 of them)
-        const uint8_t* wsf = p.weight_sf + static_cast<int64_t>(x.e) * p.sf_tiles * chunks * 512;
-        for (int k = 0; k < steps; ++k) {
-          if (!(ok = wait_phase(empty0 + 8 * s, phase ^ 1, give_up, timeouts))) break;
-          const uint32_t a = stage0 + s * kStage, b = a + kABytes, sfb = b + kBBytes + kSfaBytes, bar = full0 + 8 * s;
-          const int n = chunks - 4 * k < 4 ? chunks - 4 * k : 4;
-          mbar_arrive_expect_tx(bar, (small > 0 ? small * kSmallRows * 128 : kABytes) + kBBytes + n_sf * n * 512);
-          if (small > 0)
-            for (int i = 0; i < small; ++i) tma_load_2d<1>(a + i * kSmallRows * 128, &p.a_small, k * 128, x.row0 + i * kSmallRows, bar);
+      for (uint32_t t = t0; t < tiles && ok; t += dt) {
+        const Tile x = tile_at<Gated, Ctas, BN>(p, first, t);
+        if (x.rows <= 0) continue;
+        const int mine = (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit / Ctas;
+        const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;
+        const int nboxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
+        const int sf_tile = x.m0 / 128 + rank;  // (not gated) of this CTA's lanes; behind the weights' last row there is none
+        const bool sfa = !Gated && sf_tile < p.sf_tiles;
+        const int sf_row = (x.e * p.sf_tiles + sf_tile) * chunks;
+        const uint32_t codes = kABytes + (whole ? S::kBBytes : nboxes * kBoxRows * 128);
+        const int sf_all = Gated ? 0 : Ctas == 2 && x.m0 / 128 + 1 < p.sf_tiles ? 2 : 1;  // of both CTAs
+        for (int k = 0; k < chunks; k += 4) {
+          if (!(ok = wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, timeouts))) break;
+          const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
+          uint32_t bar = full0 + 8 * s;
+          if (rank == 0) mbar_arrive_expect_tx(bar, Ctas * codes + sf_all * kSfaBytes);
+          if constexpr (Ctas == 2) bar = cluster_addr(bar, 0);
+          if constexpr (Gated)
+            tma_load_5d<Ctas>(a, &p.a, k * 32, 0, 0, (x.m0 + rank * (kTileM / 2)) / 8, x.e, bar);
           else
-            tma_load_2d<1>(a, &p.a, k * 128, x.row0, bar);
-          if constexpr (Gated) {
-            tma_load_3d<1>(b, &p.b, k * 128, x.n0, x.e, bar);
-            tma_load_3d<1>(b + kBBytes / 2, &p.b, k * 128, p.n_out + x.n0, x.e, bar);
+            tma_load_3d<Ctas>(a, &p.a, k * 32, x.m0 + rank * kTileM, x.e, bar);
+          if (S::kBRows <= kBoxRows || whole) {  // (p.b_small is there for larger tiles alone)
+            tma_load_2d<Ctas>(b, &p.b, k * 32, x.row0 + rank * mine, bar);
           } else {
-            tma_load_3d<1>(b, &p.b, k * 128, x.n0, x.e, bar);
+            for (int i = 0; i < nboxes; ++i)
+              tma_load_2d<Ctas>(b + i * kBoxRows * 128, &p.b_small, k * 32, x.row0 + rank * mine + i * kBoxRows, bar);
           }
-          bulk_load(sfb, wsf + (static_cast<int64_t>(sf0) * chunks + 4 * k) * 512, n * 512, bar);
-          if (n_sf == 2) bulk_load(sfb + 2048, wsf + (static_cast<int64_t>(sf1) * chunks + 4 * k) * 512, n * 512, bar);
-          if (++s == kStages) { s = 0; phase ^= 1; }
+          if (sfa) tma_load_2d<Ctas>(b + S::kBBytes, &p.sfa, 0, sf_row + k, bar);  // (may reach into the next tile's columns)
+          if (++s == S::kStages) { s = 0; phase ^= 1; }
         }
       }
       if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
@@ -143,127 +173,195 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
       }
     }
   } else if (warp == 1) {
-    // ---- matrix instructions
-    if (lane == 0) {
-      constexpr uint32_t idesc = nvfp4_idesc(kTileM, kTileN);
-      uint32_t s = 0, phase = 0, dphase = 0;
+    // ---- matrix instructions (of a pair: by its first CTA)
+    if (rank == 0) {
+      uint32_t s = 0, phase = 0, buf = 0, dphase = 0, area = 0;
       bool ok = true;
-      for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        if (!(ok = wait_phase(dempty, dphase ^ 1, give_up, timeouts))) break;
-        tmem_fence_after();
-        for (int k = 0; k < steps; ++k) {
-          if (!(ok = wait_phase(full0 + 8 * s, phase, give_up, timeouts))) break;
+      for (uint32_t t = t0; t < tiles && ok; t += dt) {
+        const Tile x = tile_at<Gated, Ctas, BN>(p, first, t);
+        if (x.rows <= 0) continue;
+        const uint32_t idesc = nvfp4_idesc(kTileM * Ctas, (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit);
+        if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(dempty0 + 8 * buf, dphase ^ 1, give_up, timeouts)))) break;
+        for (int k = 0; k < chunks; k += 4) {
+          if (!(ok = __all_sync(0xffffffffu, wait_phase<1>(full0 + 8 * s, phase, give_up, timeouts) &&
+                                                 wait_phase<Ctas>(sf0 + 8 * s, phase, give_up, timeouts)))) break;
           tmem_fence_after();
-          const uint32_t a = stage0 + s * kStage, b = a + kABytes, sfa = b + kBBytes, sfb = sfa + kSfaBytes;
-          const uint64_t da = swizzled_desc(a, 1024, 16), db = swizzled_desc(b, 1024, 16);
-          const uint32_t ta = tmem + kSfColumn + s * kSfColumns, tb = ta + kSfaBytes / 128;
-          const int n = chunks - 4 * k < 4 ? chunks - 4 * k : 4;
-          for (int i = 0; i < n; ++i) {
-            tmem_copy_scales<1>(ta + 4 * i, sfa + 512 * i);
-            tmem_copy_scales<1>(tb + 8 * i, sfb + 512 * i);
-            tmem_copy_scales<1>(tb + 8 * i + 4, sfb + 2048 + 512 * i);
+          if (lane == 0) {
+            const uint32_t a = stage0 + s * S::kStage, b = a + kABytes, sfa = b + S::kBBytes, sfb = sfa + kSfaBytes;
+            const uint64_t da = swizzled_desc(a, 1024, 16), db = swizzled_desc(b, 1024, 16);
+            const uint32_t ta = tmem + 2 * BN + area * S::kSfColumns, tb = ta + kSfaBytes / 128;
+            const int n = chunks - k < 4 ? chunks - k : 4;
+            // (copies and instructions of one thread run in the order of their issue; two areas let the next stage's copies
+            // go beside this stage's instructions)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i >= n) break;
+              tmem_copy_scales<Ctas>(ta + 4 * i, sfa + 512 * i);
+#pragma unroll
+              for (int j = 0; j < S::kSfBlocks; ++j) tmem_copy_scales<Ctas>(tb + 4 * (S::kSfBlocks * i + j), sfb + 512 * (4 * j + i));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i >= n) break;
+              mma_nvfp4<Ctas>(tmem + buf * BN, da + 2 * i, db + 2 * i, idesc, ta + 4 * i, tb + 4 * S::kSfBlocks * i, (k | i) != 0);
+            }
+            mma_commit<Ctas>(empty0 + 8 * s);
+            if (k + 4 >= chunks) mma_commit<Ctas>(dfull0 + 8 * buf);
           }
-          for (int i = 0; i < n; ++i) mma_nvfp4<1>(tmem, da + 2 * i, db + 2 * i, idesc, ta + 4 * i, tb + 8 * i, (k | i) != 0);
-          mma_commit<1>(empty0 + 8 * s);
-          if (k == steps - 1) mma_commit<1>(dfull);
-          if (++s == kStages) { s = 0; phase ^= 1; }
+          __syncwarp();
+          if (++area == S::kAreas) area = 0;
+          if (++s == S::kStages) { s = 0; phase ^= 1; }
         }
-        dphase ^= 1;
+        if (buf ^= 1; buf == 0) dphase ^= 1;
       }
     }
   } else if (warp < kEpilogueWarp) {
     // ---- rows of no expert
     if (p.zero_free)
-      zero_free_rows(p.out, p.out_stride, static_cast<int64_t>(p.n_out) * 2, p.offsets, p.counts, p.E, p.R, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
+      zero_free_rows(p.to.out, p.to.out_stride, static_cast<int64_t>(p.n_out) * 2, p.offsets, p.counts, p.E, p.R, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
   } else if (warp < kScaleWarp) {
     // ---- finished accumulators
     const int quarter = warp - kEpilogueWarp;
-    uint32_t dphase = 0;
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const Tile x = tile_at<Gated>(p, first, t);
-      const int r = quarter * 32 + lane;
-      const bool live = r < x.left;
-      uint8_t* out = p.out + (static_cast<int64_t>(x.row0) + r) * p.out_stride;
+    uint32_t buf = 0, dphase = 0;
+    int stored = 0;
+    for (uint32_t t = t0; t < tiles; t += dt) {
+      const Tile x = tile_at<Gated, Ctas, BN>(p, first, t);
+      if (x.rows <= 0) continue;
       const float alpha = p.alpha == nullptr ? 1.0f : p.alpha[x.e];
-      if (!__all_sync(0xffffffffu, wait_phase(dfull, dphase, give_up, timeouts))) break;
+      if (!named_all(1, 128, wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, timeouts))) break;  // (the four warps share their stores)
       tmem_fence_after();
-      const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      constexpr int kCols = Gated ? kTileN / 2 : kTileN;
-#pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t v[32], u[32];
-        tmem_load32(d + c, v);
-        if constexpr (Gated) tmem_load32(d + kTileN / 2 + c, u);
-        tmem_wait_load();
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const int n = x.n0 + c + i;
-            if (n < p.n_out) {
-              float y[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                y[j] = __uint_as_float(v[i + j]) * alpha;
-                if constexpr (Gated) y[j] = swiglu(y[j], __uint_as_float(u[i + j]) * alpha);
-              }
-              *reinterpret_cast<uint4*>(out + static_cast<int64_t>(n) * 2) =
-                  make_uint4(Act<T>::pack(y[0], y[1]), Act<T>::pack(y[2], y[3]), Act<T>::pack(y[4], y[5]), Act<T>::pack(y[6], y[7]));
-            }
-          }
-        }
-      }
+      store_tile<T, Gated>(tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16), x.rows, x.row0, x.m0 + rank * (S::kFeatures / Ctas), alpha,
+                           p.to, boxes, stored);
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(dempty);
-      dphase ^= 1;
+      if (lane == 0) {
+        if constexpr (Ctas == 2) mbar_arrive_cluster(cluster_addr(dempty0 + 8 * buf, 0)); else mbar_arrive(dempty0 + 8 * buf);
+      }
+      if (buf ^= 1; buf == 0) dphase ^= 1;
     }
   } else {
-    // ---- the rows' scales: row r of the tile, chunk i of 64 values, to the word r / 32 of line r % 32 of block i
-    uint32_t at = 0;  // stages so far; this warp takes every fourth
-    bool ok = true;
-    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at<Gated>(p, first, t);
-      for (int k = 0; k < steps; ++k, ++at) {
-        if ((at & 3) != static_cast<uint32_t>(warp - kScaleWarp)) continue;
-        const int n = chunks - 4 * k < 4 ? chunks - 4 * k : 4;
-        uint32_t w[4][4];
+    // ---- scales to put in order: row r of a block, chunk i of 64 values, to word r / 32 of line r % 32 of the chunk's 512
+    // bytes.  A warp takes every sixth stage, and loads the next one's before it waits for this one's place.
+    const bool wide = p.n_in % 256 == 0 && reinterpret_cast<uintptr_t>(p.sf) % 16 == 0;  // (a row's 16 scales of a stage on 16 bytes)
+    const int line = p.n_in / 16;
+    struct {
+      uint32_t t;
+      int k;
+      Tile x;
+    } at = {t0, 0, {}};
+    bool more = true;
+    const auto advance = [&](int stages) {  // to the next but `stages` - 1 stage; over tiles without rows
+      at.k += 4 * stages;
+      while (at.t < tiles) {
+        at.x = tile_at<Gated, Ctas, BN>(p, first, at.t);
+        const int all = at.x.rows > 0 ? (chunks + 3) / 4 * 4 : 0;
+        if (at.k < all) return true;
+        at.k -= all;
+        at.t += dt;
+      }
+      return false;
+    };
+    uint32_t w[2][BN / 32][4];
+    uint2 g[2][4], u[2][4];
+    const auto load = [&](int b) {
+      const int n = chunks - at.k < 4 ? chunks - at.k : 4;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = q * 32 + lane;
-          const uint8_t* src = p.sf + (static_cast<int64_t>(x.row0) + r) * (p.n_in / 16) + k * 16;
+      for (int q = 0; q < BN / 32; ++q) {
+        const int r = q * 32 + lane;
+        const uint8_t* src = p.sf + (static_cast<int64_t>(at.x.row0) + r) * line + at.k * 4;
+        if (wide) {
+          const uint4 v = r < at.x.rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          w[b][q][0] = v.x; w[b][q][1] = v.y; w[b][q][2] = v.z; w[b][q][3] = v.w;
+        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[q][i] = r < x.left && i < n ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0;
+          for (int i = 0; i < 4; ++i) w[b][q][i] = r < at.x.rows && i < n ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0;
         }
-        const uint32_t s = at % kStages, phase = at / kStages & 1;
-        if (!(ok = __all_sync(0xffffffffu, wait_phase(empty0 + 8 * s, phase ^ 1, give_up, timeouts)))) break;
-        const uint32_t sfa = stage0 + s * kStage + kABytes + kBBytes;
+      }
+      if constexpr (Gated) {
+        // this CTA's gates are two neighbouring words of a tile's lines, the others two of another's
+        const int f0 = at.x.m0 + rank * (kTileM / 2);
+        const uint8_t* wsf = p.weight_sf + (static_cast<int64_t>(at.x.e) * p.sf_tiles + f0 / 128) * chunks * 512 + at.k * 512 + lane * 16 + f0 % 128 / 32 * 4;
+        const int64_t other = static_cast<int64_t>(p.n_out / 128) * chunks * 512;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sfa + i * 512 + lane * 16), "r"(w[0][i]), "r"(w[1][i]), "r"(w[2][i]), "r"(w[3][i])
-                       : "memory");
+        for (int i = 0; i < 4; ++i) {
+          g[b][i] = i < n ? __ldg(reinterpret_cast<const uint2*>(wsf + i * 512)) : make_uint2(0, 0);
+          u[b][i] = i < n ? __ldg(reinterpret_cast<const uint2*>(wsf + other + i * 512)) : make_uint2(0, 0);
+        }
+      }
+    };
+    uint32_t stage = warp - kScaleWarp;
+    more = advance(static_cast<int>(stage));
+    if (more) load(0);
+    for (bool ok = true; more && ok;) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (!more || !ok) break;
+        more = advance(kScaleWarps);
+        if (more) load(b ^ 1);
+        const uint32_t s = stage % S::kStages, phase = stage / S::kStages & 1;
+        stage += kScaleWarps;
+        if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, timeouts)))) break;
+        const uint32_t sfa = stage0 + s * S::kStage + kABytes + S::kBBytes, sfb = sfa + kSfaBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int q = 0; q < BN / 32; ++q) sts32(sfb + (4 * (q / 4) + i) * 512 + lane * 16 + q % 4 * 4, w[b][q][i]);
+          if constexpr (Gated) {
+            // gate j (lane, and 32 + lane) is lane j / 8 * 16 + j % 8 of the tile, the other 8 further
+            const uint32_t a = sfa + i * 512 + (lane / 8 % 2 * 16 + lane % 8) * 16 + lane / 16 * 4;
+            sts32(a, g[b][i].x);
+            sts32(a + 8, g[b][i].y);
+            sts32(a + 128, u[b][i].x);
+            sts32(a + 136, u[b][i].y);
+          }
+        }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full0 + 8 * s);
+        if (lane == 0) {
+          if constexpr (Ctas == 2) mbar_arrive_cluster(cluster_addr(sf0 + 8 * s, 0)); else mbar_arrive(sf0 + 8 * s);
+        }
       }
     }
   }
   __syncwarp();
   tmem_fence_before();
-  __syncthreads();
+  if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   if (warp == 2) {
     tmem_fence_after();
-    tmem_free<1>(tmem, 512);
+    tmem_free<Ctas>(tmem, 512);
   }
 }
 
-template <bool Gated, typename T>
-cudaError_t launch(const Params& p, int64_t most_tiles, bool pdl, cudaStream_t stream) {
-  constexpr auto kern = expert_nvfp4_kernel<Gated, T>;
-  const cudaError_t e = allow_smem<kern>(kSmem);
+template <bool Gated, int Ctas, int BN, typename T>
+cudaError_t launch(const Params& p, int64_t tiles, bool pdl, cudaStream_t stream) {
+  using S = Shape<Gated, Ctas, BN>;
+  constexpr auto kern = expert_nvfp4_kernel<Gated, Ctas, BN, T>;
+  const cudaError_t e = allow_smem<kern>(S::kSmem);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
+  const int sms = sm_count() / Ctas * Ctas;
   if (sms == 0) return cudaErrorInvalidDevice;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(most_tiles < sms ? most_tiles : sms)), kThreads, kSmem, pdl, stream, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(tiles * Ctas < sms ? tiles * Ctas : sms)), kThreads, S::kSmem, pdl, stream, p, Ctas);
+}
+
+template <bool Gated, int Ctas, int BN>
+cudaError_t launch_tile(const mfr_expert_matmul_nvfp4_args& a, Params& p, cudaStream_t stream) {
+  using S = Shape<Gated, Ctas, BN>;
+  constexpr CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const int64_t line = a.n_in / 2;
+  cudaError_t e = encode_rows(&p.b, type, a.codes, line, a.num_rows, line, 128, S::kBRows);
+  if (e == cudaSuccess && S::kBRows > kBoxRows) e = encode_rows(&p.b_small, type, a.codes, line, a.num_rows, line, 128, kBoxRows);
+  if (e != cudaSuccess) return e;
+  p.tiles_m = (a.n_out + S::kFeatures - 1) / S::kFeatures;
+  const int64_t tiles = expert_row_tiles(a.num_rows, a.E, BN) * p.tiles_m;
+  const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
+  return a.out_dtype == MFR_BF16 ? launch<Gated, Ctas, BN, __nv_bfloat16>(p, tiles, pdl, stream) : launch<Gated, Ctas, BN, __half>(p, tiles, pdl, stream);
+}
+
+// The tile by the rows that an expert has, as in kernel_experts.cu.
+template <bool Gated>
+cudaError_t launch_by_rows(const mfr_expert_matmul_nvfp4_args& a, Params& p, cudaStream_t stream) {
+  if (a.num_rows <= int64_t{16} * a.E) return launch_tile<Gated, 1, 32>(a, p, stream);
+  return launch_tile<Gated, 2, 192>(a, p, stream);
 }
 
 }  // namespace
@@ -271,11 +369,17 @@ cudaError_t launch(const Params& p, int64_t most_tiles, bool pdl, cudaStream_t s
 cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cudaStream_t stream) {
   Params p = {};
   constexpr CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const int64_t line = a.n_in / 2, wide = a.gated ? 2 * a.n_out : a.n_out;
-  cudaError_t e = encode_rows(&p.a, type, a.codes, line, a.num_rows, line, 128, kTileM);
-  if (e == cudaSuccess) e = encode_rows(&p.a_small, type, a.codes, line, a.num_rows, line, 128, kSmallRows);
-  if (e == cudaSuccess) e = encode_weights(&p.b, type, a.weight_codes, line, wide, a.E, line, wide * line, 128, a.gated ? kTileN / 2 : kTileN);
+  const int64_t line = a.n_in / 2, wide = a.gated ? int64_t{2} * a.n_out : a.n_out;
+  const cudaError_t e = a.gated ? encode_gated_weights(&p.a, type, a.weight_codes, line, a.n_out, a.E, line, wide * line, 128)
+                                : encode_weights(&p.a, type, a.weight_codes, line, a.n_out, a.E, line, wide * line, 128, kTileM);
   if (e != cudaSuccess) return e;
+  p.sf_tiles = static_cast<int32_t>((wide + 127) / 128);
+  if (!a.gated) {
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(a.E) * p.sf_tiles * (a.n_in / 64)}, strides[1] = {512};
+    const cuuint32_t box[2] = {128, 4};
+    const cudaError_t es = encode_map(&p.sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, a.weight_sf, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (es != cudaSuccess) return es;
+  }
   p.offsets = a.expert_offsets;
   p.counts = a.expert_counts;
   p.sf = static_cast<const uint8_t*>(a.sf);
@@ -285,15 +389,9 @@ cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cu
   p.R = static_cast<int32_t>(a.num_rows);
   p.n_in = a.n_in;
   p.n_out = a.n_out;
-  p.tiles_n = a.gated ? a.n_out / (kTileN / 2) : (a.n_out + kTileN - 1) / kTileN;
-  p.sf_tiles = static_cast<int32_t>((wide + 127) / 128);
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
-  p.out = static_cast<uint8_t*>(a.out);
-  p.out_stride = a.out_stride * 2;
-  const int64_t tiles = expert_row_tiles(a.num_rows, a.E, kTileM) * p.tiles_n;
-  const bool pdl = (a.flags & MFR_FLAG_PDL) != 0, bf16 = a.out_dtype == MFR_BF16;
-  if (a.gated) return bf16 ? launch<true, __nv_bfloat16>(p, tiles, pdl, stream) : launch<true, __half>(p, tiles, pdl, stream);
-  return bf16 ? launch<false, __nv_bfloat16>(p, tiles, pdl, stream) : launch<false, __half>(p, tiles, pdl, stream);
+  p.to = {static_cast<uint8_t*>(a.out), a.out_stride * 2, nullptr, 0, a.n_out};
+  return a.gated ? launch_by_rows<true>(a, p, stream) : launch_by_rows<false>(a, p, stream);
 }
 
 cudaError_t read_and_reset_expert_nvfp4_timeouts(unsigned int* count) {
