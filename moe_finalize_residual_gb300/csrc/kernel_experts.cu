@@ -100,6 +100,10 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     x.rows = n - at < part ? n - at : part;  // (not positive: the parts before it took all)
     x.chunks = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
   }
+  x.e = uniform(x.e);  // (called by whole warps)
+  x.row0 = uniform(x.row0);
+  x.rows = uniform(x.rows);
+  x.chunks = uniform(x.chunks);
   return x;
 }
 
@@ -136,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
   static_assert((4 * S::kStages + 5) * 8 <= kBarBytes, "barriers");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = Ctas == 2 ? cluster_ctarank() : 0;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = Ctas == 2 ? uniform(cluster_ctarank()) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -163,25 +167,25 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = *tmem_at;
-  const uint32_t tiles = D == kWeightGrad ? static_cast<uint32_t>(p.E) * p.tiles_m * p.tiles_n : static_cast<uint32_t>(first[p.E]) * p.tiles_m;
+  const uint32_t tmem = uniform(*tmem_at);
+  const uint32_t tiles = uniform(D == kWeightGrad ? static_cast<uint32_t>(p.E) * p.tiles_m * p.tiles_n : static_cast<uint32_t>(first[p.E]) * p.tiles_m);
   const uint32_t t0 = blockIdx.x / Ctas, dt = gridDim.x / Ctas;
 
   if (warp == 0) {
     // ---- copies
-    if (lane == 0) {
-      uint32_t s = 0, phase = 0;
-      bool ok = true;
-      for (uint32_t t = t0; t < tiles && ok; t += dt) {
-        const Tile x = tile_at<D, Ctas, BN>(p, first, t);
-        // B's boxes may reach behind the expert's last row: that only makes columns of D that are not stored
-        const int mine = (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit / Ctas;  // rows that this CTA copies, but for the boxes' ends
-        const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;  // one box for all of them, or several of 32
-        const int boxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kABytes + (D == kWeightGrad || whole ? S::kBBytes : boxes * kBoxRows * kDepth * 2);
-        for (int k = 0; k < x.chunks; k += kChunks) {
-          if (!(ok = wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, &g_expert_wait_timeouts))) break;
-          const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    for (uint32_t t = t0; t < tiles && ok; t += dt) {
+      const Tile x = tile_at<D, Ctas, BN>(p, first, t);
+      // B's boxes may reach behind the expert's last row: that only makes columns of D that are not stored
+      const int mine = (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit / Ctas;  // rows that this CTA copies, but for the boxes' ends
+      const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;  // one box for all of them, or several of 32
+      const int boxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = kABytes + (D == kWeightGrad || whole ? S::kBBytes : boxes * kBoxRows * kDepth * 2);
+      for (int k = 0; k < x.chunks; k += kChunks) {
+        if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
+        const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
+        if (elect_one()) {
           uint32_t bar = full0 + 8 * s;
           if (Ctas == 2 && D == kWeightGrad && x.rows < (k + n) * kDepth) {
             // the expert's last rows: each CTA of the pair sees its own copies land, and clears the lines behind them
@@ -221,13 +225,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
               }
             }
           }
-          if (++s == S::kStages) { s = 0; phase ^= 1; }
         }
+        __syncwarp();
+        if (++s == S::kStages) { s = 0; phase ^= 1; }
       }
-      if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
-        const uint64_t since = global_timer_ns();
-        while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
-      }
+    }
+    if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
+      const uint64_t since = global_timer_ns();
+      while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
     // ---- matrix instructions (of a pair: by its first CTA)
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           }
         }
         tmem_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             if (c >= n) break;

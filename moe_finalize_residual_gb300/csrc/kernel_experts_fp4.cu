@@ -81,6 +81,9 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
   const int at = (m - first[x.e]) * part;
   x.row0 = s.begin + at;
   x.rows = n - at < part ? n - at : part;
+  x.e = uniform(x.e);  // (called by whole warps)
+  x.row0 = uniform(x.row0);
+  x.rows = uniform(x.rows);
   return x;
 }
 
@@ -100,8 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
   volatile int* give_up = reinterpret_cast<volatile int*>(tmem_at + 1);
   int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
   static_assert((3 * S::kStages + 5) * 8 <= kBarBytes, "barriers");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = Ctas == 2 ? cluster_ctarank() : 0;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = Ctas == 2 ? uniform(cluster_ctarank()) : 0;
   unsigned int* const timeouts = &g_expert_nvfp4_wait_timeouts;
 
   if (threadIdx.x == 0) {
@@ -126,30 +129,30 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = *tmem_at;
-  const uint32_t tiles = static_cast<uint32_t>(first[p.E]) * p.tiles_m;
+  const uint32_t tmem = uniform(*tmem_at);
+  const uint32_t tiles = uniform(static_cast<uint32_t>(first[p.E]) * p.tiles_m);
   const uint32_t t0 = blockIdx.x / Ctas, dt = gridDim.x / Ctas;
   const int chunks = p.n_in / 64;  // instructions a tile, and columns of 512 bytes of the scales' tiles
 
   if (warp == 0) {
     // ---- copies
-    if (lane == 0) {
-      uint32_t s = 0, phase = 0;
-      bool ok = true;
-      for (uint32_t t = t0; t < tiles && ok; t += dt) {
-        const Tile x = tile_at<Gated, Ctas, BN>(p, first, t);
-        if (x.rows <= 0) continue;
-        const int mine = (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit / Ctas;
-        const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;
-        const int nboxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
-        const int sf_tile = x.m0 / 128 + rank;  // (not gated) of this CTA's lanes; behind the weights' last row there is none
-        const bool sfa = !Gated && sf_tile < p.sf_tiles;
-        const int sf_row = (x.e * p.sf_tiles + sf_tile) * chunks;
-        const uint32_t codes = kABytes + (whole ? S::kBBytes : nboxes * kBoxRows * 128);
-        const int sf_all = Gated ? 0 : Ctas == 2 && x.m0 / 128 + 1 < p.sf_tiles ? 2 : 1;  // of both CTAs
-        for (int k = 0; k < chunks; k += 4) {
-          if (!(ok = wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, timeouts))) break;
-          const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    for (uint32_t t = t0; t < tiles && ok; t += dt) {
+      const Tile x = tile_at<Gated, Ctas, BN>(p, first, t);
+      if (x.rows <= 0) continue;
+      const int mine = (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit / Ctas;
+      const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;
+      const int nboxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
+      const int sf_tile = x.m0 / 128 + rank;  // (not gated) of this CTA's lanes; behind the weights' last row there is none
+      const bool sfa = !Gated && sf_tile < p.sf_tiles;
+      const int sf_row = (x.e * p.sf_tiles + sf_tile) * chunks;
+      const uint32_t codes = kABytes + (whole ? S::kBBytes : nboxes * kBoxRows * 128);
+      const int sf_all = Gated ? 0 : Ctas == 2 && x.m0 / 128 + 1 < p.sf_tiles ? 2 : 1;  // of both CTAs
+      for (int k = 0; k < chunks; k += 4) {
+        if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, timeouts)))) break;
+        const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
+        if (elect_one()) {
           uint32_t bar = full0 + 8 * s;
           if (rank == 0) mbar_arrive_expect_tx(bar, Ctas * codes + sf_all * kSfaBytes);
           if constexpr (Ctas == 2) bar = cluster_addr(bar, 0);
@@ -164,13 +167,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
               tma_load_2d<Ctas>(b + i * kBoxRows * 128, &p.b_small, k * 32, x.row0 + rank * mine + i * kBoxRows, bar);
           }
           if (sfa) tma_load_2d<Ctas>(b + S::kBBytes, &p.sfa, 0, sf_row + k, bar);  // (may reach into the next tile's columns)
-          if (++s == S::kStages) { s = 0; phase ^= 1; }
         }
+        __syncwarp();
+        if (++s == S::kStages) { s = 0; phase ^= 1; }
       }
-      if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
-        const uint64_t since = global_timer_ns();
-        while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
-      }
+    }
+    if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
+      const uint64_t since = global_timer_ns();
+      while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
     }
   } else if (warp == 1) {
     // ---- matrix instructions (of a pair: by its first CTA)
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
           if (!(ok = __all_sync(0xffffffffu, wait_phase<1>(full0 + 8 * s, phase, give_up, timeouts) &&
                                                  wait_phase<Ctas>(sf0 + 8 * s, phase, give_up, timeouts)))) break;
           tmem_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t a = stage0 + s * S::kStage, b = a + kABytes, sfa = b + S::kBBytes, sfb = sfa + kSfaBytes;
             const uint64_t da = swizzled_desc(a, 1024, 16), db = swizzled_desc(b, 1024, 16);
             const uint32_t ta = tmem + 2 * BN + area * S::kSfColumns, tb = ta + kSfaBytes / 128;

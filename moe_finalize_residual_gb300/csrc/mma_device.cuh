@@ -103,6 +103,17 @@ __device__ __forceinline__ void cluster_sync() {
 // What this thread's loads and stores did to shared memory, before what tensor copies and tcgen05 do to it.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// A value that is the same in the whole warp, in a form that the compiler knows to be: the instructions for tensor copies and
+// tcgen05 take their operands from uniform registers, and moving each there costs more than small ones take.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Named barrier of `threads` threads of the CTA, and the conjunction of what they bring to it.
 __device__ __forceinline__ void named_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ bool named_all(int id, int threads, bool v) {
