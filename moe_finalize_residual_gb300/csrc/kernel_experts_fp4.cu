@@ -87,7 +87,9 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
   return x;
 }
 
-__device__ __forceinline__ void sts32(uint32_t dst, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts128(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
 template <bool Gated, int Ctas, int BN, typename T>
 __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_constant__ Params p) {
@@ -245,85 +247,66 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
     }
   } else {
     // ---- scales to put in order: row r of a block, chunk i of 64 values, to word r / 32 of line r % 32 of the chunk's 512
-    // bytes.  A warp takes every sixth stage, and loads the next one's before it waits for this one's place.
+    // bytes.  A warp takes every sixth stage.  It loads the next one's scales as soon as this one's are stored: not before, since
+    // the release that says so would wait for the loads.
     const bool wide = p.n_in % 256 == 0 && reinterpret_cast<uintptr_t>(p.sf) % 16 == 0;  // (a row's 16 scales of a stage on 16 bytes)
     const int line = p.n_in / 16;
-    struct {
-      uint32_t t;
-      int k;
+    uint32_t t = t0, stage = warp - kScaleWarp;
+    int k = 4 * static_cast<int>(stage);
+    for (bool ok = true;; stage += kScaleWarps, k += 4 * kScaleWarps) {
+      // the tile of the stage: over tiles that end before it
       Tile x;
-    } at = {t0, 0, {}};
-    bool more = true;
-    const auto advance = [&](int stages) {  // to the next but `stages` - 1 stage; over tiles without rows
-      at.k += 4 * stages;
-      while (at.t < tiles) {
-        at.x = tile_at<Gated, Ctas, BN>(p, first, at.t);
-        const int all = at.x.rows > 0 ? (chunks + 3) / 4 * 4 : 0;
-        if (at.k < all) return true;
-        at.k -= all;
-        at.t += dt;
+      bool more = false;
+      for (; t < tiles; t += dt) {
+        x = tile_at<Gated, Ctas, BN>(p, first, t);
+        const int all = x.rows > 0 ? (chunks + 3) / 4 * 4 : 0;
+        if ((more = k < all)) break;
+        k -= all;
       }
-      return false;
-    };
-    uint32_t w[2][BN / 32][4];
-    uint2 g[2][4], u[2][4];
-    const auto load = [&](int b) {
-      const int n = chunks - at.k < 4 ? chunks - at.k : 4;
+      if (!more || !ok) break;
+      const int n = chunks - k < 4 ? chunks - k : 4;
+      uint32_t w[(BN + 127) / 128 * 4][4];
 #pragma unroll
       for (int q = 0; q < BN / 32; ++q) {
         const int r = q * 32 + lane;
-        const uint8_t* src = p.sf + (static_cast<int64_t>(at.x.row0) + r) * line + at.k * 4;
+        const uint8_t* src = p.sf + (static_cast<int64_t>(x.row0) + r) * line + k * 4;
         if (wide) {
-          const uint4 v = r < at.x.rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-          w[b][q][0] = v.x; w[b][q][1] = v.y; w[b][q][2] = v.z; w[b][q][3] = v.w;
+          const uint4 v = r < x.rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[b][q][i] = r < at.x.rows && i < n ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0;
+          for (int i = 0; i < 4; ++i) w[q][i] = r < x.rows && i < n ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0;
         }
       }
+#pragma unroll
+      for (int q = BN / 32; q < (BN + 127) / 128 * 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[q][i] = 0;
+      uint2 g[4], h[4];
       if constexpr (Gated) {
-        // this CTA's gates are two neighbouring words of a tile's lines, the others two of another's
-        const int f0 = at.x.m0 + rank * (kTileM / 2);
-        const uint8_t* wsf = p.weight_sf + (static_cast<int64_t>(at.x.e) * p.sf_tiles + f0 / 128) * chunks * 512 + at.k * 512 + lane * 16 + f0 % 128 / 32 * 4;
-        const int64_t other = static_cast<int64_t>(p.n_out / 128) * chunks * 512;
+        // lane l of the block's lines is 8 gates, 8 others and so on: its words are the weights' rows c, c + 16, c + 32 and
+        // c + 48 from f0 on, which lie in the lines c and c + 16 of a tile, two neighbouring words each
+        const int f0 = x.m0 + rank * (kTileM / 2), f = f0 + (lane & 8 ? p.n_out : 0), c = lane / 16 * 8 + lane % 8;
+        const uint8_t* wsf = p.weight_sf + ((static_cast<int64_t>(x.e) * p.sf_tiles + f / 128) * chunks + k) * 512 + c * 16 + f0 % 128 / 32 * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          g[b][i] = i < n ? __ldg(reinterpret_cast<const uint2*>(wsf + i * 512)) : make_uint2(0, 0);
-          u[b][i] = i < n ? __ldg(reinterpret_cast<const uint2*>(wsf + other + i * 512)) : make_uint2(0, 0);
+          g[i] = i < n ? __ldg(reinterpret_cast<const uint2*>(wsf + i * 512)) : make_uint2(0, 0);
+          h[i] = i < n ? __ldg(reinterpret_cast<const uint2*>(wsf + i * 512 + 256)) : make_uint2(0, 0);
         }
       }
-    };
-    uint32_t stage = warp - kScaleWarp;
-    more = advance(static_cast<int>(stage));
-    if (more) load(0);
-    for (bool ok = true; more && ok;) {
+      const uint32_t s = stage % S::kStages, phase = stage / S::kStages & 1;
+      if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, timeouts)))) break;
+      const uint32_t sfa = stage0 + s * S::kStage + kABytes + S::kBBytes + lane * 16, sfb = sfa + kSfaBytes;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (!more || !ok) break;
-        more = advance(kScaleWarps);
-        if (more) load(b ^ 1);
-        const uint32_t s = stage % S::kStages, phase = stage / S::kStages & 1;
-        stage += kScaleWarps;
-        if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, timeouts)))) break;
-        const uint32_t sfa = stage0 + s * S::kStage + kABytes + S::kBBytes, sfb = sfa + kSfaBytes;
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int q = 0; q < BN / 32; ++q) sts32(sfb + (4 * (q / 4) + i) * 512 + lane * 16 + q % 4 * 4, w[b][q][i]);
-          if constexpr (Gated) {
-            // gate j (lane, and 32 + lane) is lane j / 8 * 16 + j % 8 of the tile, the other 8 further
-            const uint32_t a = sfa + i * 512 + (lane / 8 % 2 * 16 + lane % 8) * 16 + lane / 16 * 4;
-            sts32(a, g[b][i].x);
-            sts32(a + 8, g[b][i].y);
-            sts32(a + 128, u[b][i].x);
-            sts32(a + 136, u[b][i].y);
-          }
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (Ctas == 2) mbar_arrive_cluster(cluster_addr(sf0 + 8 * s, 0)); else mbar_arrive(sf0 + 8 * s);
-        }
+        for (int b = 0; b < S::kSfBlocks; ++b) sts128(sfb + (4 * b + i) * 512, w[4 * b][i], w[4 * b + 1][i], w[4 * b + 2][i], w[4 * b + 3][i]);
+        if constexpr (Gated) sts128(sfa + i * 512, g[i].x, h[i].x, g[i].y, h[i].y);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (Ctas == 2) mbar_arrive_cluster(cluster_addr(sf0 + 8 * s, 0)); else mbar_arrive(sf0 + 8 * s);
       }
     }
   }
