@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const __grid_const
 // NVFP4
 // ------------------------------------------------------------------------------------------------
 
+constexpr int kFp4Blocks = 152 * 8;  // CTAs at most: some turns of those that a GB300 holds at once
+
 struct Fp4Params {
   const uint8_t* x;   // quantize: read; dequantize: written
   uint8_t* codes;
@@ -96,94 +98,173 @@ struct Fp4Params {
   int32_t H, blocks, blocks_up, layout, tpr, act;
 };
 
-// Where this thread's row is: false if it has none.
+// Row i of all matrices'; `real` false behind a matrix's last row, `live` false for a row of no route too.
 struct Fp4Row {
   int64_t matrix, m, row;
+  bool real, live;
 };
-__device__ __forceinline__ bool fp4_row(const Fp4Params& p, Fp4Row& r) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.tpr) + threadIdx.x / p.tpr;
-  if (i >= p.total) return false;
+__device__ __forceinline__ Fp4Row fp4_row(const Fp4Params& p, int64_t i) {
+  Fp4Row r;
   r.matrix = i < p.rows_up ? 0 : i / p.rows_up;
   r.m = i - r.matrix * p.rows_up;
   r.row = r.matrix * p.rows + r.m;
-  return true;
+  r.real = r.m < p.rows;
+  r.live = r.real && (p.row_route == nullptr || p.row_route[r.row] >= 0);
+  return r;
 }
 
-// A thread takes blocks of 16 values.  The scale's bytes of four neighbouring blocks, one word of a tile, are written by
-// one thread.
+// Bytes into a matrix's scales of block k of a row: row_at(m) + block_at(k).
+__device__ __forceinline__ int64_t row_at(const Fp4Params& p, int64_t m) {
+  return p.layout == MFR_SF_ROW_MAJOR ? m * p.blocks : (m >> 7) * (static_cast<int64_t>((p.blocks + 3) >> 2) * 512) + (m & 31) * 16 + (m >> 5 & 3) * 4;
+}
+__device__ __forceinline__ int block_at(const Fp4Params& p, int k) { return p.layout == MFR_SF_ROW_MAJOR ? k : (k >> 2) * 512 + (k & 3); }
+
+// Eight E2M1 codes, nearest even, at most 6; the even value of a pair in the low half of its byte.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float2 v[4]) {
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+  return r;
+}
+
+// The largest magnitude of 8 values as they are stored, a NaN's bits if there is one: magnitudes order as their bits.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t largest(uint4 a) {
+  const uint32_t m = max_u16x2(max_u16x2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), max_u16x2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
+// A thread takes 8 values, two neighbouring ones a block, and two of its row's pieces at once.  Whole sectors go each way:
+// a block a thread, 32 bytes apart, was slower (H = 7168, 32768 rows: 210 us, then 134).  The scale's bytes of four neighbouring
+// blocks, one word of a tile, are written by one thread.
 template <typename T>
 __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const __grid_constant__ Fp4Params p) {
   pdl_launch_dependents();
   pdl_wait();
-  Fp4Row r;
-  if (!fp4_row(p, r)) return;  // (rows are whole warps')
   const float g = *p.scale;
-  const bool real = r.m < p.rows;
-  const bool live = real && (p.row_route == nullptr || p.row_route[r.row] >= 0);
-  for (int k0 = 0; k0 < p.blocks_up; k0 += p.tpr) {
-    const int k = k0 + threadIdx.x % p.tpr;
-    const bool here = real && k < p.blocks;
-    uint32_t sf = 0;
-    if (here) {
-      const uint8_t* x = p.x + r.row * p.x_stride + static_cast<int64_t>(k) * 32;
-      float v[16];
-      unpack8<T>(ldg16_if(x, live), v);
-      unpack8<T>(ldg16_if(x + 16, live), v + 8);
-      float amax = 0.0f;
-      bool nan = false;
+  const int lane_k = threadIdx.x % p.tpr, per = blockDim.x / p.tpr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / p.tpr;  // (rows are whole warps')
+  int base = 0;
+  if (i >= p.total) return;
+  Fp4Row r = fp4_row(p, i);
+  uint4 a[2];
+  const auto load = [&](uint4 v[2], const Fp4Row& row, int k0) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        amax = fmaxf(amax, fabsf(v[i]));
-        nan |= v[i] != v[i];
+    for (int u = 0; u < 2; ++u) v[u] = ldg16_if(p.x + row.row * p.x_stride + (k0 + u * p.tpr) * 16, row.live && k0 + u * p.tpr < 2 * p.blocks);
+  };
+  load(a, r, lane_k);
+  while (true) {
+    // the next pieces' loads are in flight while these are worked on
+    int64_t next = i;
+    int next_base = base + 2 * p.tpr;
+    if (next_base >= 2 * p.blocks_up) next_base = 0, next += step;
+    const bool more = next < p.total;
+    Fp4Row r1 = r;
+    uint4 a1[2];
+    if (more) {
+      if (next != i) r1 = fp4_row(p, next);
+      load(a1, r1, next_base + lane_k);
+    }
+    const int k0 = base + lane_k;
+    uint8_t* codes = p.codes + r.row * (p.H / 2);
+    uint8_t* to = p.sf + r.matrix * p.sf_bytes + row_at(p, r.m);
+    // of two neighbouring threads one finds the scale of their first block, the other that of their second
+    const bool odd = (threadIdx.x & 1) != 0;
+    uint32_t top = largest(a[0]), top1 = largest(a[1]);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+    const float amax = Act<T>::unpack(odd ? top1 : top).x;
+    // a block that holds a NaN gets the scale NaN: its codes cannot say so
+    uint32_t found = amax != amax ? 0x7fu : __nv_cvt_float_to_fp8(__fmul_rn(__fdiv_rn(amax, 6.0f), g), __NV_SATFINITE, __NV_E4M3);
+    if (!r.real || k0 + (odd ? p.tpr : 0) >= 2 * p.blocks) found = 0;
+    const float wide = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(found), __NV_E4M3)));
+    const float inverse = wide == 0.0f ? 0.0f : __fdiv_rn(g, wide);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = k0 + u * p.tpr;
+      const bool here = r.real && k < 2 * p.blocks;
+      uint32_t sf = __shfl_sync(0xffffffffu, found, u, 2);
+      const float es = __shfl_sync(0xffffffffu, inverse, u, 2);
+      const float2 es2 = make_float2(es, es);
+      const uint32_t w[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+      float2 y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(Act<T>::unpack(w[j]), es2);
+      if (here) *reinterpret_cast<uint32_t*>(codes + k * 4) = to_e2m1x8(y);
+      if (p.layout == MFR_SF_ROW_MAJOR) {
+        if (here && (k & 1) == 0) to[k >> 1] = static_cast<uint8_t>(sf);
+      } else {
+        sf |= __shfl_down_sync(0xffffffffu, sf, 2) << 8;
+        sf |= __shfl_down_sync(0xffffffffu, sf, 4) << 16;
+        if ((k & 7) == 0 && k < 2 * p.blocks_up) *reinterpret_cast<uint32_t*>(to + block_at(p, k >> 1)) = sf;
       }
-      // a block that holds a NaN gets the scale NaN: its codes cannot say so
-      sf = nan ? 0x7fu : __nv_cvt_float_to_fp8(__fmul_rn(__fdiv_rn(amax, 6.0f), g), __NV_SATFINITE, __NV_E4M3);
-      const float wide = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(sf), __NV_E4M3)));
-      const float es = wide == 0.0f ? 0.0f : __fdiv_rn(g, wide);
-      uint32_t c[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        c[i / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(__fmul_rn(v[2 * i], es), __fmul_rn(v[2 * i + 1], es)),
-                                                                   __NV_E2M1, cudaRoundNearest))
-                    << (8 * (i % 4));
-      *reinterpret_cast<uint2*>(p.codes + r.row * (p.H / 2) + static_cast<int64_t>(k) * 8) = make_uint2(c[0], c[1]);
     }
-    uint8_t* to = p.sf + r.matrix * p.sf_bytes;
-    if (p.layout == MFR_SF_ROW_MAJOR) {
-      if (here) to[r.m * p.blocks + k] = static_cast<uint8_t>(sf);
-    } else {
-      sf |= __shfl_down_sync(0xffffffffu, sf, 1) << 8;
-      sf |= __shfl_down_sync(0xffffffffu, sf, 2) << 16;
-      if ((k & 3) == 0 && k < p.blocks_up) *reinterpret_cast<uint32_t*>(to + sf_offset(r.m, k, p.H, p.layout)) = sf;
-    }
+    if (!more) break;
+    i = next;
+    base = next_base;
+    r = r1;
+    a[0] = a1[0];
+    a[1] = a1[1];
   }
+}
+
+// The values of four codes, in FP16, which holds them exactly.
+__device__ __forceinline__ void from_e2m1x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b8 b0, b1;\n .reg .b16 w;\n cvt.u16.u32 w, %2;\n mov.b16 {b0, b1}, w;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(512) nvfp4_dequantize_kernel(const __grid_constant__ Fp4Params p) {
   pdl_launch_dependents();
   pdl_wait();
-  Fp4Row r;
-  if (!fp4_row(p, r) || r.m >= p.rows) return;
   const float g = *p.scale;
-  const bool live = p.row_route == nullptr || p.row_route[r.row] >= 0;
-  const uint8_t* from = p.sf + r.matrix * p.sf_bytes;
-  for (int k = threadIdx.x % p.tpr; k < p.blocks; k += p.tpr) {
-    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (live) {
-      const uint2 c = *reinterpret_cast<const uint2*>(p.codes + r.row * (p.H / 2) + static_cast<int64_t>(k) * 8);
-      const uint8_t sf = from[sf_offset(r.m, k, p.H, p.layout)];
-      const float es = __fdiv_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(sf, __NV_E4M3))), g);
+  const int lane_k = threadIdx.x % p.tpr, per = blockDim.x / p.tpr;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / p.tpr; i < p.total; i += static_cast<int64_t>(gridDim.x) * per) {
+    const Fp4Row r = fp4_row(p, i);
+    const uint8_t* codes = p.codes + r.row * (p.H / 2);
+    const uint8_t* from = p.sf + r.matrix * p.sf_bytes + row_at(p, r.m);
+    uint8_t* x = const_cast<uint8_t*>(p.x) + r.row * p.x_stride;
+    for (int base = 0; base < 2 * p.blocks; base += 2 * p.tpr) {  // (by whole warps, for the shuffles)
+      const int k0 = base + lane_k;
+      uint32_t c[2], sf[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t pair = ((i < 4 ? c.x : c.y) >> (8 * (i % 4))) & 0xff;
-        const float2 v = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(pair), __NV_E2M1)));
-        w[i] = Act<T>::pack(__fmul_rn(v.x, es), __fmul_rn(v.y, es));
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + u * p.tpr;
+        const bool here = r.live && k < 2 * p.blocks;
+        c[u] = here ? __ldg(reinterpret_cast<const uint32_t*>(codes + k * 4)) : 0;
+        sf[u] = here ? __ldg(from + block_at(p, k >> 1)) : 0;
+      }
+      // (one division for the two blocks of two neighbouring threads)
+      const uint32_t of = (threadIdx.x & 1) != 0 ? sf[1] : sf[0];
+      const float quotient = __fdiv_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(of), __NV_E4M3))), g);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + u * p.tpr;
+        const float es = __shfl_sync(0xffffffffu, quotient, u, 2);
+        const float2 es2 = make_float2(es, es);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t h[2];
+          from_e2m1x4(c[u] >> (16 * i), h[0], h[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 v = __fmul2_rn(Act<__half>::unpack(h[j]), es2);
+            w[2 * i + j] = Act<T>::pack(v.x, v.y);
+          }
+        }
+        if (k < 2 * p.blocks) *reinterpret_cast<uint4*>(x + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    uint4* o = reinterpret_cast<uint4*>(const_cast<uint8_t*>(p.x) + r.row * p.x_stride + static_cast<int64_t>(k) * 32);
-    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -205,6 +286,13 @@ Fp4Params fp4_params(const mfr_nvfp4_args& a, bool padding) {
   p.blocks_up = tiles && padding ? (p.blocks + 3) / 4 * 4 : p.blocks;
   p.layout = a.sf_layout;
   return p;
+}
+
+// CTAs that stay for several rows: what a thread works out once (the divisions above all) is a third of its instructions when
+// it has one row.
+dim3 fp4_grid(const Fp4Params& p, const RowShape& s) {
+  const int64_t all = (p.total + s.rows - 1) / s.rows, most = kFp4Blocks;
+  return dim3(static_cast<unsigned>(all < most ? all : most));
 }
 
 }  // namespace
@@ -232,9 +320,9 @@ cudaError_t launch_swiglu_backward(const mfr_swiglu_backward_args& a, cudaStream
 
 cudaError_t launch_nvfp4_quantize(const mfr_nvfp4_args& a, cudaStream_t stream) {
   Fp4Params p = fp4_params(a, true);
-  const RowShape s = row_shape(p.blocks_up);
+  const RowShape s = row_shape(p.blocks_up);  // (two pieces a block, and two a thread)
   p.tpr = s.tpr;
-  const dim3 grid(static_cast<unsigned>((p.total + s.rows - 1) / s.rows));
+  const dim3 grid = fp4_grid(p, s);
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
   return a.act_dtype == MFR_BF16 ? launch_pdl(nvfp4_quantize_kernel<__nv_bfloat16>, grid, s.tpr * s.rows, 0, pdl, stream, p)
                                  : launch_pdl(nvfp4_quantize_kernel<__half>, grid, s.tpr * s.rows, 0, pdl, stream, p);
@@ -244,7 +332,7 @@ cudaError_t launch_nvfp4_dequantize(const mfr_nvfp4_args& a, cudaStream_t stream
   Fp4Params p = fp4_params(a, false);
   const RowShape s = row_shape(p.blocks);
   p.tpr = s.tpr;
-  const dim3 grid(static_cast<unsigned>((p.total + s.rows - 1) / s.rows));
+  const dim3 grid = fp4_grid(p, s);
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
   return a.act_dtype == MFR_BF16 ? launch_pdl(nvfp4_dequantize_kernel<__nv_bfloat16>, grid, s.tpr * s.rows, 0, pdl, stream, p)
                                  : launch_pdl(nvfp4_dequantize_kernel<__half>, grid, s.tpr * s.rows, 0, pdl, stream, p);
