@@ -97,7 +97,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     const int part = ((n + parts - 1) / parts + S::kUnit - 1) / S::kUnit * S::kUnit;
     const int at = (m - first[x.e]) * part;
     x.row0 = s.begin + at;
-    x.rows = n - at < part ? n - at : part;  // (not positive: the parts before it took all)
+    x.rows = at < 0 ? 0 : n - at < part ? n - at : part;  // (not positive: the parts before it took all)
     x.chunks = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
   }
   x.e = uniform(x.e);  // (called by whole warps)

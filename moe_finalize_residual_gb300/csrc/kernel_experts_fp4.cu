@@ -80,7 +80,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
   const int part = ((n + parts - 1) / parts + S::kUnit - 1) / S::kUnit * S::kUnit;
   const int at = (m - first[x.e]) * part;
   x.row0 = s.begin + at;
-  x.rows = n - at < part ? n - at : part;
+  x.rows = at < 0 ? 0 : n - at < part ? n - at : part;  // (not positive: the parts before it took all)
   x.e = uniform(x.e);  // (called by whole warps)
   x.row0 = uniform(x.row0);
   x.rows = uniform(x.rows);
