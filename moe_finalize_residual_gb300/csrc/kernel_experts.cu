@@ -24,8 +24,7 @@ namespace {
 
 enum Dir { kForward = 0, kGated = 1, kRowsGrad = 2, kWeightGrad = 3 };
 
-constexpr int kThreads = 256;
-constexpr int kEpilogueWarp = 4;                 // first of four
+constexpr int kEpilogueWarp = 4;                 // first of four, the weights' gradient: of two groups of four
 constexpr int kDepth = 64;                       // reduction values of a chunk: lines of 128 bytes
 constexpr int kChunks = 2;                       // chunks of a stage
 constexpr int kTileM = kExpertTileRows;          // rows of A of one CTA
@@ -51,9 +50,11 @@ struct Shape {
   static constexpr int kBRows = BN / Ctas;  // columns of D whose operand this CTA copies
   static constexpr int kBBytes = kBRows * kDepth * 2;
   static constexpr int kStage = kChunks * (kABytes + kBBytes);  // A's chunks, then B's
-  // results leave by two buffers: 128 lines of 128 bytes of the weights' gradient, or 32 rows of the tile's values
+  // results leave by two buffers: 128 lines of 128 bytes of the weights' gradient (one for each group of warps), or 32 rows of the tile's values
   static constexpr int kOutBytes = D == kWeightGrad ? kTileM * 128 : 32 * kTileM * 2;
   static constexpr int kStages = D == kWeightGrad ? 196608 / kStage : 204800 / kStage;
+  static constexpr int kGroups = D == kWeightGrad ? 2 : 1;  // groups of four warps that take results out
+  static constexpr int kThreads = 32 * (kEpilogueWarp + 4 * kGroups);
   static constexpr bool kALines = D == kRowsGrad || D == kWeightGrad;
   static constexpr bool kBLines = D == kWeightGrad;
   static constexpr int kFeatures = (D == kGated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
@@ -125,14 +126,14 @@ __device__ __forceinline__ void clear_lines(uint32_t stage, int chunk, int from)
 
 // T: the operands' type; O: that of D (FP32 for the weights' gradient alone).
 template <int D, int Ctas, int BN, typename T, typename O>
-__global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, Ctas, BN>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const uint32_t stage0 = smem_addr(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage + 2 * S::kOutBytes);
   const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * S::kStages;
-  // (the last two kinds: a pair's weights' gradient alone)
+  // (the next two kinds: the weights' gradient alone)
   const uint32_t tail0 = empty0 + 8 * S::kStages, ready0 = tail0 + 8 * S::kStages;
   const uint32_t dfull0 = ready0 + 8 * S::kStages, dempty0 = dfull0 + 16;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 4 * S::kStages + 4);
@@ -148,11 +149,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(tail0 + 8 * s, 1);
-      mbar_init(ready0 + 8 * s, 1);
+      mbar_init(ready0 + 8 * s, Ctas);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(dfull0 + 8 * i, 1);
-      mbar_init(dempty0 + 8 * i, 4 * Ctas);
+      mbar_init(dempty0 + 8 * i, 4 * S::kGroups * Ctas);
     }
     *give_up = 0;
     fence_mbar_init();
@@ -187,9 +188,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
         if (elect_one()) {
           uint32_t bar = full0 + 8 * s;
-          if (Ctas == 2 && D == kWeightGrad && x.rows < (k + n) * kDepth) {
-            // the expert's last rows: each CTA of the pair sees its own copies land, and clears the lines behind them
-            if (rank == 1) bar = tail0 + 8 * s;
+          if (D == kWeightGrad && x.rows < (k + n) * kDepth) {
+            // the expert's last rows: each CTA sees its own copies land, and clears the lines behind them
+            if (rank == 0) mbar_arrive(bar);
+            bar = tail0 + 8 * s;
             mbar_arrive_expect_tx(bar, n * bytes);
           } else {
             if (rank == 0) mbar_arrive_expect_tx(bar, n * Ctas * bytes);
@@ -237,40 +239,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   } else if (warp == 1) {
     // ---- matrix instructions (of a pair: by its first CTA)
     uint32_t s = 0, phase = 0, buf = 0, dphase = 0, tail_phase = 0;
-    bool ok = true;
+    bool ok = rank == 0;
     for (uint32_t t = t0; t < tiles && ok; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
       if (x.chunks == 0) continue;
-      const int last = x.rows - (x.chunks - 1) * kDepth;  // (weights' gradient) rows of the last chunk
       const int columns = D == kWeightGrad ? BN : (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit;
       const uint32_t idesc = f16_idesc(kIsBf16<T>, S::kALines, S::kBLines, kTileM * Ctas, columns);
-      if (rank != 0) {
-        // the pair's other CTA clears the lines of its own operands behind the expert's last row, and says so
-        if constexpr (D == kWeightGrad) {
-          const int n = x.chunks % kChunks == 0 ? kChunks : x.chunks % kChunks;  // chunks of the last stage
-          s = (s + (x.chunks - 1) / kChunks) % S::kStages;
-          if (last < kDepth) {
-            if (!(ok = __all_sync(0xffffffffu, wait_phase<1>(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
-            tail_phase ^= 1u << s;
-            clear_lines<S>(stage0 + s * S::kStage, n - 1, last);
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(ready0 + 8 * s, 0));
-          }
-          s = (s + 1) % S::kStages;
-        }
-        continue;
-      }
       if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
       tmem_fence_after();
       for (int k = 0; k < x.chunks; k += kChunks) {
         const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
         if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts)))) break;
         if constexpr (D == kWeightGrad) {
-          if (k + n == x.chunks && last < kDepth) {
-            clear_lines<S>(stage0 + s * S::kStage, n - 1, last);
-            if constexpr (Ctas == 2) {
-              if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
-              tail_phase ^= 1u << s;
-            }
+          if (k + n == x.chunks && x.rows % kDepth != 0) {
+            if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
+            tail_phase ^= 1u << s;
           }
         }
         tmem_fence_after();
@@ -293,6 +276,23 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       }
       if (buf ^= 1; buf == 0) dphase ^= 1;
     }
+  } else if (D == kWeightGrad && warp == 2) {
+    // ---- lines behind an expert's last row, cleared as soon as they land: stages before the instructions come to them
+    uint32_t s = 0, tail_phase = 0;
+    for (uint32_t t = t0; t < tiles; t += dt) {
+      const Tile x = tile_at<D, Ctas, BN>(p, first, t);
+      if (x.chunks == 0) continue;
+      s = (s + (x.chunks - 1) / kChunks) % S::kStages;  // the last stage, and its last chunk
+      if (x.rows % kDepth != 0) {
+        if (!__all_sync(0xffffffffu, wait_phase<1>(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts))) break;
+        tail_phase ^= 1u << s;
+        clear_lines<S>(stage0 + s * S::kStage, (x.chunks - 1) % kChunks, x.rows % kDepth);
+        if (lane == 0) {
+          if constexpr (Ctas == 2) mbar_arrive_cluster(cluster_addr(ready0 + 8 * s, 0)); else mbar_arrive(ready0 + 8 * s);
+        }
+      }
+      s = (s + 1) % S::kStages;
+    }
   } else if (warp < kEpilogueWarp) {
     // ---- rows of no expert
     if (D != kWeightGrad && p.zero_free) {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     }
   } else {
     // ---- finished accumulators
-    const int quarter = warp - kEpilogueWarp;
+    const int quarter = warp % 4, group = (warp - kEpilogueWarp) / 4, sync = 1 + group;
     uint32_t buf = 0, dphase = 0;
     int stored = 0;  // buffers so far
     for (uint32_t t = t0; t < tiles; t += dt) {
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const bool some = x.chunks > 0;
       if (some) {
         const bool ok = wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
-        if (!named_all(1, 128, ok)) break;  // (the four warps share their stores)
+        if (!named_all(sync, 128, ok)) break;  // (the four warps share their stores)
         tmem_fence_after();
       }
       const uint32_t d = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -321,46 +321,48 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         constexpr int kLine = 128 / sizeof(O);
         const int m0 = x.m0 + rank * kTileM;
         if (some || !p.accumulate) {
+          // (each group half of the columns, by a buffer of its own)
+          const uint32_t box = stage0 + S::kStages * S::kStage + group * S::kOutBytes;
+          const bool first_thread = threadIdx.x % 128 == 0;
 #pragma unroll 1
-          for (int c = 0; c < BN && x.n0 + c < p.n_n; c += kLine, ++stored) {
-            const uint32_t box = stage0 + S::kStages * S::kStage + (stored & 1) * S::kOutBytes;
-            if (threadIdx.x == kEpilogueWarp * 32) tma_store_wait_read<1>();  // the buffer's last box has left it
-            named_sync(1, 128);
+          for (int c = group * (BN / 2); c < (group + 1) * (BN / 2) && x.n0 + c < p.n_n; c += kLine) {
+            uint32_t v[kLine];
+            if (some) {
 #pragma unroll
-            for (int h = 0; h < kLine; h += 32) {
-              uint32_t v[32];
-              if (some) {
-                tmem_load32(d + c + h, v);
-                tmem_wait_load();
-              } else {
+              for (int h = 0; h < kLine; h += 32) tmem_load32(d + c + h, v + h);
+              tmem_wait_load();
+            } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0;
+              for (int i = 0; i < kLine; ++i) v[i] = 0;
+            }
+            if (first_thread) tma_store_wait_read<0>();  // the buffer's last box has left it
+            named_sync(sync, 128);
+            constexpr int kPiece = 16 / sizeof(O);  // values of 16 bytes, in the 128-byte swizzle
+#pragma unroll
+            for (int i = 0; i < kLine; i += kPiece) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(O) == 4)
+                  w[j] = v[i + j];
+                else
+                  w[j] = Act<T>::pack(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
               }
-              constexpr int kPiece = 16 / sizeof(O);  // values of 16 bytes, in the 128-byte swizzle
-#pragma unroll
-              for (int i = 0; i < 32; i += kPiece) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  if constexpr (sizeof(O) == 4)
-                    w[j] = v[i + j];
-                  else
-                    w[j] = Act<T>::pack(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
-                }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + r * 128 + ((((h + i) / kPiece) ^ (r & 7)) << 4)), "r"(w[0]),
-                             "r"(w[1]), "r"(w[2]), "r"(w[3])
-                             : "memory");
-              }
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + r * 128 + (((i / kPiece) ^ (r & 7)) << 4)), "r"(w[0]), "r"(w[1]),
+                           "r"(w[2]), "r"(w[3])
+                           : "memory");
             }
             fence_async_shared();
-            named_sync(1, 128);
-            if (threadIdx.x == kEpilogueWarp * 32 && m0 < p.n_m) {
-              if (p.accumulate)
-                tma_add_3d(&p.d, box, x.n0 + c, m0, x.e);
-              else
-                tma_store_3d(&p.d, box, x.n0 + c, m0, x.e);
+            named_sync(sync, 128);
+            if (first_thread) {
+              if (m0 < p.n_m) {
+                if (p.accumulate)
+                  tma_add_3d(&p.d, box, x.n0 + c, m0, x.e);
+                else
+                  tma_store_3d(&p.d, box, x.n0 + c, m0, x.e);
+              }
+              tma_store_commit();
             }
-            if (threadIdx.x == kEpilogueWarp * 32) tma_store_commit();
           }
         }
       } else {
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         if (buf ^= 1; buf == 0) dphase ^= 1;
       }
     }
-    if (D == kWeightGrad && threadIdx.x == kEpilogueWarp * 32) tma_store_wait();
+    if (D == kWeightGrad && threadIdx.x % 128 == 0) tma_store_wait();
   }
   __syncwarp();
   tmem_fence_before();
@@ -399,7 +401,7 @@ cudaError_t launch(Params& p, int64_t most_tiles, bool pdl, cudaStream_t stream)
   const int sms = sm_count() / Ctas * Ctas;
   if (sms == 0) return cudaErrorInvalidDevice;
   const int64_t want = most_tiles * Ctas;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(want < sms ? want : sms)), kThreads, S::kSmem, pdl, stream, p, Ctas);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(want < sms ? want : sms)), S::kThreads, S::kSmem, pdl, stream, p, Ctas);
 }
 
 CUtensorMapDataType map_type(int act) { return act == MFR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }
