@@ -11,7 +11,7 @@
 // and a decode step's few rows hardly anything beside the weights.
 //
 // A persistent CTA, or a pair of CTAs that share the columns' operand, takes tiles of 128 (256) weight rows x at most BN
-// rows.  One warp copies the operands in by tensor copies, 128 values of the reduction a stage; one thread issues the matrix
+// rows.  One warp copies the operands in by tensor copies, 64 values of the reduction a stage; one thread issues the matrix
 // instructions into one of two accumulators in tensor memory; four warps take finished accumulators out, round and store
 // them meanwhile.
 #include "experts_device.cuh"
@@ -25,8 +25,7 @@ namespace {
 enum Dir { kForward = 0, kGated = 1, kRowsGrad = 2, kWeightGrad = 3 };
 
 constexpr int kEpilogueWarp = 4;                 // first of four, the weights' gradient: of two groups of four
-constexpr int kDepth = 64;                       // reduction values of a chunk: lines of 128 bytes
-constexpr int kChunks = 2;                       // chunks of a stage
+constexpr int kDepth = 64;                       // reduction values of a stage: lines of 128 bytes
 constexpr int kTileM = kExpertTileRows;          // rows of A of one CTA
 constexpr int kABytes = kTileM * kDepth * 2;
 constexpr int kBoxRows = 32;                     // rows of a small box of B
@@ -49,7 +48,7 @@ template <int D, int Ctas, int BN>
 struct Shape {
   static constexpr int kBRows = BN / Ctas;  // columns of D whose operand this CTA copies
   static constexpr int kBBytes = kBRows * kDepth * 2;
-  static constexpr int kStage = kChunks * (kABytes + kBBytes);  // A's chunks, then B's
+  static constexpr int kStage = kABytes + kBBytes;
   // results leave by two buffers: 128 lines of 128 bytes of the weights' gradient (one for each group of warps), or 32 rows of the tile's values
   static constexpr int kOutBytes = D == kWeightGrad ? kTileM * 128 : 32 * kTileM * 2;
   static constexpr int kStages = D == kWeightGrad ? 196608 / kStage : 204800 / kStage;
@@ -70,7 +69,7 @@ struct Tile {
   int rows;   // its rows in the tile (weights' gradient: its rows)
   int m0;     // first value of the output row (weights' gradient: first row of D)
   int n0;     // weights' gradient: first column of D
-  int chunks; // of the reduction
+  int steps;  // stages of the reduction
 };
 
 template <int D, int Ctas, int BN>
@@ -86,7 +85,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     const RowSpan s = expert_rows(p.offsets, p.counts, x.e, p.R);
     x.row0 = s.begin;
     x.rows = s.end - s.begin;
-    x.chunks = (x.rows + kDepth - 1) / kDepth;
+    x.steps = (x.rows + kDepth - 1) / kDepth;
   } else {
     const int m = t / p.tiles_m;
     x.m0 = t % p.tiles_m * S::kFeatures;
@@ -99,27 +98,22 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     const int at = (m - first[x.e]) * part;
     x.row0 = s.begin + at;
     x.rows = at < 0 ? 0 : n - at < part ? n - at : part;  // (not positive: the parts before it took all)
-    x.chunks = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
+    x.steps = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
   }
   x.e = uniform(x.e);  // (called by whole warps)
   x.row0 = uniform(x.row0);
   x.rows = uniform(x.rows);
-  x.chunks = uniform(x.chunks);
+  x.steps = uniform(x.steps);
   return x;
 }
 
-// Zeros, by one warp, in the lines from `from` on of a stage's chunk whose operands' lines are steps of the reduction: they
-// hold rows behind the expert's last, which must not count.  In both operands, since 0 * NaN is NaN.
+// Zeros, by one warp, in the lines from `from` on of a stage whose operands' lines are steps of the reduction: they hold rows
+// behind the expert's last, which must not count.  In both operands, since 0 * NaN is NaN.
 template <typename S>
-__device__ __forceinline__ void clear_lines(uint32_t stage, int chunk, int from) {
+__device__ __forceinline__ void clear_lines(uint32_t stage, int from) {
   const int each = (kDepth - from) * 8;  // 16-byte pieces of a block of 64 columns
-  constexpr int kBlock = 64 * kDepth * 2, kABlocks = kTileM / 64;
-  const uint32_t a = stage + chunk * kABytes, b = stage + kChunks * kABytes + chunk * S::kBBytes;
-  for (int i = threadIdx.x & 31; i < (kABlocks + S::kBRows / 64) * each; i += 32) {
-    const int block = i / each;
-    const uint32_t at = (block < kABlocks ? a + block * kBlock : b + (block - kABlocks) * kBlock) + from * 128 + i % each * 16;
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-  }
+  for (int i = threadIdx.x & 31; i < S::kStage / (64 * kDepth * 2) * each; i += 32)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + i / each * (64 * kDepth * 2) + from * 128 + i % each * 16), "r"(0) : "memory");
   fence_async_shared();
   __syncwarp();
 }
@@ -183,48 +177,43 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
       const bool whole = S::kBRows <= kBoxRows || mine > S::kBRows / 2;  // one box for all of them, or several of 32
       const int boxes = whole ? 1 : (mine + kBoxRows - 1) / kBoxRows;
       const uint32_t bytes = kABytes + (D == kWeightGrad || whole ? S::kBBytes : boxes * kBoxRows * kDepth * 2);
-      for (int k = 0; k < x.chunks; k += kChunks) {
+      for (int k = 0; k < x.steps; ++k) {
         if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(empty0 + 8 * s, phase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
-        const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
         if (elect_one()) {
           uint32_t bar = full0 + 8 * s;
-          if (D == kWeightGrad && x.rows < (k + n) * kDepth) {
+          if (D == kWeightGrad && x.rows < (k + 1) * kDepth) {
             // the expert's last rows: each CTA sees its own copies land, and clears the lines behind them
             if (rank == 0) mbar_arrive(bar);
             bar = tail0 + 8 * s;
-            mbar_arrive_expect_tx(bar, n * bytes);
+            mbar_arrive_expect_tx(bar, bytes);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(bar, n * Ctas * bytes);
+            if (rank == 0) mbar_arrive_expect_tx(bar, Ctas * bytes);
             if constexpr (Ctas == 2) bar = cluster_addr(bar, 0);
           }
+          const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
+          const int r0 = k * kDepth;
+          if constexpr (D == kWeightGrad) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c >= n) break;
-            const uint32_t a = stage0 + s * S::kStage + c * kABytes, b = stage0 + s * S::kStage + kChunks * kABytes + c * S::kBBytes;
-            const int r0 = (k + c) * kDepth;
-            if constexpr (D == kWeightGrad) {
+            for (int i = 0; i < kTileM / 64; ++i)
+              tma_load_2d<Ctas>(a + i * 64 * kDepth * 2, &p.a, x.m0 + rank * kTileM + i * 64, x.row0 + r0, bar);
+#pragma unroll
+            for (int i = 0; i < S::kBRows / 64; ++i)
+              tma_load_2d<Ctas>(b + i * 64 * kDepth * 2, &p.b, x.n0 + rank * S::kBRows + i * 64, x.row0 + r0, bar);
+          } else {
+            if constexpr (D == kForward) {
+              tma_load_3d<Ctas>(a, &p.a, r0, x.m0 + rank * kTileM, x.e, bar);
+            } else if constexpr (D == kGated) {  // 8 rows of the gate, 8 of the others, and so on
+              tma_load_5d<Ctas>(a, &p.a, r0, 0, 0, (x.m0 + rank * (kTileM / 2)) / 8, x.e, bar);
+            } else {
 #pragma unroll
               for (int i = 0; i < kTileM / 64; ++i)
-                tma_load_2d<Ctas>(a + i * 64 * kDepth * 2, &p.a, x.m0 + rank * kTileM + i * 64, x.row0 + r0, bar);
-#pragma unroll
-              for (int i = 0; i < S::kBRows / 64; ++i)
-                tma_load_2d<Ctas>(b + i * 64 * kDepth * 2, &p.b, x.n0 + rank * S::kBRows + i * 64, x.row0 + r0, bar);
+                tma_load_3d<Ctas>(a + i * 64 * kDepth * 2, &p.a, x.m0 + rank * kTileM + i * 64, r0, x.e, bar);
+            }
+            if (S::kBRows <= kBoxRows || whole) {  // (p.b_small is there for larger tiles alone)
+              tma_load_2d<Ctas>(b, &p.b, r0, x.row0 + rank * mine, bar);
             } else {
-              if constexpr (D == kForward) {
-                tma_load_3d<Ctas>(a, &p.a, r0, x.m0 + rank * kTileM, x.e, bar);
-              } else if constexpr (D == kGated) {  // 8 rows of the gate, 8 of the others, and so on
-                tma_load_5d<Ctas>(a, &p.a, r0, 0, 0, (x.m0 + rank * (kTileM / 2)) / 8, x.e, bar);
-              } else {
-#pragma unroll
-                for (int i = 0; i < kTileM / 64; ++i)
-                  tma_load_3d<Ctas>(a + i * 64 * kDepth * 2, &p.a, x.m0 + rank * kTileM + i * 64, r0, x.e, bar);
-              }
-              if (S::kBRows <= kBoxRows || whole) {  // (p.b_small is there for larger tiles alone)
-                tma_load_2d<Ctas>(b, &p.b, r0, x.row0 + rank * mine, bar);
-              } else {
-                for (int i = 0; i < boxes; ++i)
-                  tma_load_2d<Ctas>(b + i * kBoxRows * kDepth * 2, &p.b_small, r0, x.row0 + rank * mine + i * kBoxRows, bar);
-              }
+              for (int i = 0; i < boxes; ++i)
+                tma_load_2d<Ctas>(b + i * kBoxRows * kDepth * 2, &p.b_small, r0, x.row0 + rank * mine + i * kBoxRows, bar);
             }
           }
         }
@@ -242,34 +231,29 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
     bool ok = rank == 0;
     for (uint32_t t = t0; t < tiles && ok; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
-      if (x.chunks == 0) continue;
+      if (x.steps == 0) continue;
       const int columns = D == kWeightGrad ? BN : (x.rows + S::kUnit - 1) / S::kUnit * S::kUnit;
       const uint32_t idesc = f16_idesc(kIsBf16<T>, S::kALines, S::kBLines, kTileM * Ctas, columns);
       if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(dempty0 + 8 * buf, dphase ^ 1, give_up, &g_expert_wait_timeouts)))) break;
       tmem_fence_after();
-      for (int k = 0; k < x.chunks; k += kChunks) {
-        const int n = x.chunks - k < kChunks ? x.chunks - k : kChunks;
+      for (int k = 0; k < x.steps; ++k) {
         if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(full0 + 8 * s, phase, give_up, &g_expert_wait_timeouts)))) break;
         if constexpr (D == kWeightGrad) {
-          if (k + n == x.chunks && x.rows % kDepth != 0) {
+          if (k + 1 == x.steps && x.rows % kDepth != 0) {
             if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(ready0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts)))) break;
             tail_phase ^= 1u << s;
           }
         }
         tmem_fence_after();
         if (elect_one()) {
+          const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
+          const uint64_t da = S::kALines ? swizzled_desc(a, 1024, 64 * kDepth * 2) : swizzled_desc(a, 1024, 16);
+          const uint64_t db = S::kBLines ? swizzled_desc(b, 1024, 64 * kDepth * 2) : swizzled_desc(b, 1024, 16);
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c >= n) break;
-            const uint32_t a = stage0 + s * S::kStage + c * kABytes, b = stage0 + s * S::kStage + kChunks * kABytes + c * S::kBBytes;
-            const uint64_t da = S::kALines ? swizzled_desc(a, 1024, 64 * kDepth * 2) : swizzled_desc(a, 1024, 16);
-            const uint64_t db = S::kBLines ? swizzled_desc(b, 1024, 64 * kDepth * 2) : swizzled_desc(b, 1024, 16);
-#pragma unroll
-            for (int i = 0; i < kDepth / 16; ++i)  // 16 values of the reduction: 32 bytes of a line, or 16 lines
-              mma_f16<Ctas>(tmem + buf * BN, da + i * (S::kALines ? 128 : 2), db + i * (S::kBLines ? 128 : 2), idesc, (k | c | i) != 0);
-          }
+          for (int i = 0; i < kDepth / 16; ++i)  // 16 values of the reduction: 32 bytes of a line, or 16 lines
+            mma_f16<Ctas>(tmem + buf * BN, da + i * (S::kALines ? 128 : 2), db + i * (S::kBLines ? 128 : 2), idesc, (k | i) != 0);
           mma_commit<Ctas>(empty0 + 8 * s);
-          if (k + n == x.chunks) mma_commit<Ctas>(dfull0 + 8 * buf);
+          if (k + 1 == x.steps) mma_commit<Ctas>(dfull0 + 8 * buf);
         }
         __syncwarp();
         if (++s == S::kStages) { s = 0; phase ^= 1; }
@@ -281,12 +265,12 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
     uint32_t s = 0, tail_phase = 0;
     for (uint32_t t = t0; t < tiles; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
-      if (x.chunks == 0) continue;
-      s = (s + (x.chunks - 1) / kChunks) % S::kStages;  // the last stage, and its last chunk
+      if (x.steps == 0) continue;
+      s = (s + x.steps - 1) % S::kStages;  // the last stage
       if (x.rows % kDepth != 0) {
         if (!__all_sync(0xffffffffu, wait_phase<1>(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts))) break;
         tail_phase ^= 1u << s;
-        clear_lines<S>(stage0 + s * S::kStage, (x.chunks - 1) % kChunks, x.rows % kDepth);
+        clear_lines<S>(stage0 + s * S::kStage, x.rows % kDepth);
         if (lane == 0) {
           if constexpr (Ctas == 2) mbar_arrive_cluster(cluster_addr(ready0 + 8 * s, 0)); else mbar_arrive(ready0 + 8 * s);
         }
@@ -308,7 +292,7 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
     int stored = 0;  // buffers so far
     for (uint32_t t = t0; t < tiles; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
-      const bool some = x.chunks > 0;
+      const bool some = x.steps > 0;
       if (some) {
         const bool ok = wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
         if (!named_all(sync, 128, ok)) break;  // (the four warps share their stores)
