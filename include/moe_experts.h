@@ -159,10 +159,15 @@ typedef struct {
   const int32_t* expert_counts;
   void* out;                     /* device [num_rows, n_out], 16-byte aligned                            */
   int64_t out_stride;
+  void* workspace;               /* device, 16-byte aligned, moe_expert_matmul_nvfp4_workspace_bytes bytes (NULL when that is 0) */
+  int64_t workspace_bytes;
   uint32_t flags;                /* MFR_FLAG_PDL, MFR_FLAG_ZERO_PADDING                                  */
 } mfr_expert_matmul_nvfp4_args;
 
 int moe_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args* args, struct CUstream_st* stream);
+
+/* Workspace bytes of moe_expert_matmul_nvfp4 (0 for few rows an expert). <0 on bad input. */
+int64_t moe_expert_matmul_nvfp4_workspace_bytes(int32_t E, int64_t num_rows, int32_t n_in);
 
 /* Waits of the products' kernels that ran out (about 2 s; none does unless something is broken) since the last call, on the
  * current device; synchronizes. */

@@ -171,6 +171,10 @@ int check_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args* a) {
   if (a->num_rows == 0) return MFR_OK;
   if (a->codes == nullptr || a->weight_codes == nullptr || !aligned(a->codes, 16) || !aligned(a->weight_codes, 16))
     return fail(MFR_ERR_INVALID_ARG, "codes or weight_codes is NULL or not 16-byte aligned");
+  const int64_t need = moe_expert_matmul_nvfp4_workspace_bytes(a->E, a->num_rows, a->n_in);
+  if (need < 0) return static_cast<int>(need);
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need || !aligned(a->workspace, 16)))
+    return fail(MFR_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", static_cast<ll>(need));
   if (a->sf == nullptr || a->weight_sf == nullptr || !aligned(a->sf, 4) || !aligned(a->weight_sf, 16))
     return fail(MFR_ERR_INVALID_ARG, "sf or weight_sf is NULL, sf not 4-byte or weight_sf not 16-byte aligned");
   return check_tensor("out", a->out, a->out_stride, a->n_out);
@@ -223,6 +227,16 @@ int moe_nvfp4_dequantize(const mfr_nvfp4_args* args, struct CUstream_st* stream)
   const int st = check_nvfp4(args);
   if (st != MFR_OK || args->rows == 0) return st;
   return enqueue_status(launch_nvfp4_dequantize(*args, stream), "moe_nvfp4_dequantize launch");
+}
+
+int64_t moe_expert_matmul_nvfp4_workspace_bytes(int32_t E, int64_t num_rows, int32_t n_in) {
+  int st;
+  if (E < 1 || E > MFR_MAX_EXPERTS) return fail(MFR_ERR_INVALID_ARG, "E = %d outside [1, %d]", E, MFR_MAX_EXPERTS);
+  if ((st = check_rows(num_rows)) != MFR_OK || (st = check_width("n_in", n_in, 64)) != MFR_OK) return st;
+  if (nvfp4_few_rows(num_rows, E)) return 0;
+  const int64_t blocks = expert_row_tiles(num_rows, E, kNvfp4Rows) * (n_in / 64) * 2;
+  if (blocks > INT32_MAX) return fail(MFR_ERR_INVALID_ARG, "%lld blocks of scales: 2^31 or more", static_cast<ll>(blocks));
+  return blocks * 512;
 }
 
 int moe_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args* args, struct CUstream_st* stream) {

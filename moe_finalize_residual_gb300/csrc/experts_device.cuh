@@ -90,6 +90,23 @@ __device__ __forceinline__ int tile_expert(const int* first, int E, int m) {
   return lo;
 }
 
+// The rows of tile number m: an expert's rows in equal parts, a multiple of `unit` but for the last, since a short last one would
+// use the weights' copies badly.
+struct RowPart {
+  int e, row0, rows;  // (rows not positive: the parts before it took all)
+};
+__device__ __forceinline__ RowPart row_part(const int* first, const int32_t* offsets, const int32_t* counts, int E, int R, int m, int unit) {
+  RowPart x;
+  x.e = tile_expert(first, E, m);
+  const RowSpan s = expert_rows(offsets, counts, x.e, R);
+  const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
+  const int part = ((n + parts - 1) / parts + unit - 1) / unit * unit;
+  const int at = (m - first[x.e]) * part;
+  x.row0 = s.begin + at;
+  x.rows = at < 0 ? 0 : n - at < part ? n - at : part;
+  return x;
+}
+
 // Zeros in the rows of no expert of an output with `bytes` (a multiple of 16) a row, by `nwarps` warps (this one is `w`).
 // Gap g lies behind the rows of expert g - 1; a warp looks at 32 gaps at a time.
 __device__ __forceinline__ void zero_free_rows(uint8_t* out, int64_t stride_bytes, int64_t bytes, const int32_t* offsets,

@@ -20,6 +20,12 @@ cudaError_t read_and_reset_expert_nvfp4_timeouts(unsigned int* count);
 constexpr int kExpertTileRows = 128;
 constexpr int64_t kExpertMaxTiles = int64_t{1} << 31;
 
+// The NVFP4 product of more than kNvfp4FewRows rows an expert takes tiles of kNvfp4Rows rows, whose scales a kernel before it puts
+// in order: for each tile and 64 values of the reduction two blocks of 128 rows' scales.
+constexpr int kNvfp4FewRows = 16;
+constexpr int kNvfp4Rows = 192;
+inline bool nvfp4_few_rows(int64_t R, int E) { return R <= int64_t{kNvfp4FewRows} * E; }
+
 // Tiles of `tile` rows that R rows of E experts fill at most.
 inline int64_t expert_row_tiles(int64_t R, int E, int tile) { return R / tile + (R < E ? R : E); }
 

@@ -90,14 +90,10 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     const int m = t / p.tiles_m;
     x.m0 = t % p.tiles_m * S::kFeatures;
     x.n0 = 0;
-    x.e = tile_expert(first, p.E, m);
-    const RowSpan s = expert_rows(p.offsets, p.counts, x.e, p.R);
-    // the expert's rows in equal parts: a short last one would use the weights' copies badly
-    const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
-    const int part = ((n + parts - 1) / parts + S::kUnit - 1) / S::kUnit * S::kUnit;
-    const int at = (m - first[x.e]) * part;
-    x.row0 = s.begin + at;
-    x.rows = at < 0 ? 0 : n - at < part ? n - at : part;  // (not positive: the parts before it took all)
+    const RowPart part = row_part(first, p.offsets, p.counts, p.E, p.R, m, S::kUnit);
+    x.e = part.e;
+    x.row0 = part.row0;
+    x.rows = part.rows;
     x.steps = x.rows > 0 ? (p.n_red + kDepth - 1) / kDepth : 0;
   }
   x.e = uniform(x.e);  // (called by whole warps)

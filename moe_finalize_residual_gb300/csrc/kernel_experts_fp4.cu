@@ -5,8 +5,10 @@
 // as its columns, persistent CTAs or pairs of them, operands by tensor copies, results through shared memory.  A stage is 256
 // values of the reduction.  The scales take a second way: tensor memory wants them in blocks of 128 rows x 4 scales, which
 // the issuing thread copies there from shared memory before each stage's instructions.  The weights' lie in such tiles and
-// come by tensor copies as they are; gated, where a tile's lanes are 8 gates and 8 others alternately, and for the rows, whose
-// scales are row-major since rows begin anywhere, six warps, a stage each in turn, put them in order.
+// come by tensor copies as they are; gated, where a tile's lanes are 8 gates and 8 others alternately, six warps, a stage each
+// in turn, put them in order.  The rows' scales are row-major, since rows begin anywhere.  With few rows the same warps gather
+// them; with many that took longer than the instructions (32 sectors a load; 105 us where 84 go without it), so a kernel
+// before this one writes them in tiles, once for all columns' tiles.
 #include "experts_device.cuh"
 
 namespace mfr {
@@ -28,7 +30,7 @@ constexpr int kBarBytes = 512;
 constexpr int kOutBytes = 32 * kTileM * 2;
 
 struct Params {
-  CUtensorMap a, b, b_small, sfa;  // (sfa: not gated, 512 bytes of 4 columns of a tile a row)
+  CUtensorMap a, b, b_small, sfa, sfb;  // (sfa: not gated; sfb: rows' scales in order; both 512 bytes a row)
   const int32_t* offsets;
   const int32_t* counts;
   const uint8_t* sf;         // rows' scales, row-major
@@ -46,6 +48,8 @@ template <bool Gated, int Ctas, int BN>
 struct Shape {
   static constexpr int kBRows = BN / Ctas;  // rows whose codes this CTA copies (their scales: all BN)
   static constexpr int kBBytes = kBRows * 128;
+  static constexpr bool kInOrder = Ctas == 2;         // the rows' scales are, in the workspace
+  static constexpr bool kGather = Gated || !kInOrder; // there are scales for the warps to put in order
   static constexpr int kSfBlocks = (BN + 127) / 128;  // blocks of 128 rows' scales
   static constexpr int kSfbBytes = kSfBlocks * 128 * kDepth / 16;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
@@ -74,13 +78,10 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
   Tile x;
   const int m = t / p.tiles_m;
   x.m0 = t % p.tiles_m * S::kFeatures;
-  x.e = tile_expert(first, p.E, m);
-  const RowSpan s = expert_rows(p.offsets, p.counts, x.e, p.R);
-  const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
-  const int part = ((n + parts - 1) / parts + S::kUnit - 1) / S::kUnit * S::kUnit;
-  const int at = (m - first[x.e]) * part;
-  x.row0 = s.begin + at;
-  x.rows = at < 0 ? 0 : n - at < part ? n - at : part;  // (not positive: the parts before it took all)
+  const RowPart part = row_part(first, p.offsets, p.counts, p.E, p.R, m, S::kUnit);
+  x.e = part.e;
+  x.row0 = part.row0;
+  x.rows = part.rows;
   x.e = uniform(x.e);  // (called by whole warps)
   x.row0 = uniform(x.row0);
   x.rows = uniform(x.rows);
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
         const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
         if (elect_one()) {
           uint32_t bar = full0 + 8 * s;
-          if (rank == 0) mbar_arrive_expect_tx(bar, Ctas * codes + sf_all * kSfaBytes);
+          if (rank == 0) mbar_arrive_expect_tx(bar, Ctas * (codes + (S::kInOrder ? S::kSfbBytes : 0)) + sf_all * kSfaBytes);
           if constexpr (Ctas == 2) bar = cluster_addr(bar, 0);
           if constexpr (Gated)
             tma_load_5d<Ctas>(a, &p.a, k * 32, 0, 0, (x.m0 + rank * (kTileM / 2)) / 8, x.e, bar);
@@ -169,6 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
               tma_load_2d<Ctas>(b + i * kBoxRows * 128, &p.b_small, k * 32, x.row0 + rank * mine + i * kBoxRows, bar);
           }
           if (sfa) tma_load_2d<Ctas>(b + S::kBBytes, &p.sfa, 0, sf_row + k, bar);  // (may reach into the next tile's columns)
+          if constexpr (S::kInOrder)
+            tma_load_2d<Ctas>(b + S::kBBytes + kSfaBytes, &p.sfb, 0, (static_cast<int>(t / p.tiles_m) * chunks + k) * S::kSfBlocks, bar);
         }
         __syncwarp();
         if (++s == S::kStages) { s = 0; phase ^= 1; }
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
         if (!(ok = __all_sync(0xffffffffu, wait_phase<Ctas>(dempty0 + 8 * buf, dphase ^ 1, give_up, timeouts)))) break;
         for (int k = 0; k < chunks; k += 4) {
           if (!(ok = __all_sync(0xffffffffu, wait_phase<1>(full0 + 8 * s, phase, give_up, timeouts) &&
-                                                 wait_phase<Ctas>(sf0 + 8 * s, phase, give_up, timeouts)))) break;
+                                                 (!S::kGather || wait_phase<Ctas>(sf0 + 8 * s, phase, give_up, timeouts))))) break;
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t a = stage0 + s * S::kStage, b = a + kABytes, sfa = b + S::kBBytes, sfb = sfa + kSfaBytes;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
               if (i >= n) break;
               tmem_copy_scales<Ctas>(ta + 4 * i, sfa + 512 * i);
 #pragma unroll
-              for (int j = 0; j < S::kSfBlocks; ++j) tmem_copy_scales<Ctas>(tb + 4 * (S::kSfBlocks * i + j), sfb + 512 * (4 * j + i));
+              for (int j = 0; j < S::kSfBlocks; ++j) tmem_copy_scales<Ctas>(tb + 4 * (S::kSfBlocks * i + j), sfb + 512 * (S::kSfBlocks * i + j));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
       }
       if (buf ^= 1; buf == 0) dphase ^= 1;
     }
-  } else {
+  } else if constexpr (S::kGather) {
     // ---- scales to put in order: row r of a block, chunk i of 64 values, to word r / 32 of line r % 32 of the chunk's 512
     // bytes.  A warp takes every sixth stage.  It loads the next one's scales as soon as this one's are stored: not before, since
     // the release that says so would wait for the loads.
@@ -265,23 +268,18 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
       }
       if (!more || !ok) break;
       const int n = chunks - k < 4 ? chunks - k : 4;
-      uint32_t w[(BN + 127) / 128 * 4][4];
-#pragma unroll
-      for (int q = 0; q < BN / 32; ++q) {
-        const int r = q * 32 + lane;
-        const uint8_t* src = p.sf + (static_cast<int64_t>(x.row0) + r) * line + k * 4;
+      uint32_t w[4];
+      if constexpr (!S::kInOrder) {  // at most 32 rows: the first word of each line
+        static_assert(S::kInOrder || BN == 32, "one row a lane");
+        const uint8_t* src = p.sf + (static_cast<int64_t>(x.row0) + lane) * line + k * 4;
         if (wide) {
-          const uint4 v = r < x.rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-          w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
+          const uint4 v = lane < x.rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[q][i] = r < x.rows && i < n ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0;
+          for (int i = 0; i < 4; ++i) w[i] = lane < x.rows && i < n ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0;
         }
       }
-#pragma unroll
-      for (int q = BN / 32; q < (BN + 127) / 128 * 4; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[q][i] = 0;
       uint2 g[4], h[4];
       if constexpr (Gated) {
         // lane l of the block's lines is 8 gates, 8 others and so on: its words are the weights' rows c, c + 16, c + 32 and
@@ -299,8 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
       const uint32_t sfa = stage0 + s * S::kStage + kABytes + S::kBBytes + lane * 16, sfb = sfa + kSfaBytes;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int b = 0; b < S::kSfBlocks; ++b) sts128(sfb + (4 * b + i) * 512, w[4 * b][i], w[4 * b + 1][i], w[4 * b + 2][i], w[4 * b + 3][i]);
+        if constexpr (!S::kInOrder) sts128(sfb + i * 512, w[i], 0, 0, 0);
         if constexpr (Gated) sts128(sfa + i * 512, g[i].x, h[i].x, g[i].y, h[i].y);
       }
       fence_async_shared();
@@ -316,6 +313,47 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
   if (warp == 2) {
     tmem_fence_after();
     tmem_free<Ctas>(tmem, 512);
+  }
+}
+
+// The rows' scales in the order of tensor memory: for each tile of kNvfp4Rows rows and each chunk of 64 values two blocks of 128
+// rows, row r's four scales in word r / 32 of line r % 32 of 16 bytes.  A CTA takes 16 chunks of a tile at a time, through shared
+// memory: rows in 64-byte pieces on one side, whole blocks on the other.  Rows of no tile get zeros.
+constexpr int kOrderThreads = 256, kOrderChunks = 16, kOrderRows = 256, kOrderPitch = kOrderChunks + 1;
+struct OrderParams {
+  const uint8_t* sf;
+  const int32_t* offsets;
+  const int32_t* counts;
+  int32_t E, R, chunks;
+  int32_t tiles;  // that the workspace holds: more than experts that share no rows fill
+  uint8_t* to;
+};
+__global__ void __launch_bounds__(kOrderThreads) order_scales_kernel(const __grid_constant__ OrderParams p) {
+  __shared__ uint32_t words[kOrderRows * kOrderPitch];
+  __shared__ int first[MFR_MAX_EXPERTS + 1 + 33];
+  pdl_launch_dependents();
+  pdl_wait();
+  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, kNvfp4Rows);
+  const int groups = (p.chunks + kOrderChunks - 1) / kOrderChunks;
+  const int64_t all = static_cast<int64_t>(first[p.E] < p.tiles ? first[p.E] : p.tiles) * groups;
+  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+    const int m = static_cast<int>(i / groups), c0 = static_cast<int>(i % groups) * kOrderChunks;
+    const RowPart x = row_part(first, p.offsets, p.counts, p.E, p.R, m, 32);
+    const int n = p.chunks - c0 < kOrderChunks ? p.chunks - c0 : kOrderChunks;
+    __syncthreads();  // (the last turn's words are read)
+#pragma unroll 4
+    for (int at = threadIdx.x; at < kOrderRows * kOrderChunks; at += kOrderThreads) {
+      const int r = at / kOrderChunks, c = at % kOrderChunks;
+      words[r * kOrderPitch + c] =
+          r < x.rows && c < n ? __ldg(reinterpret_cast<const uint32_t*>(p.sf + ((static_cast<int64_t>(x.row0) + r) * p.chunks + c0 + c) * 4)) : 0;
+    }
+    __syncthreads();
+    for (int at = threadIdx.x; at < n * 64; at += kOrderThreads) {
+      const int c = at / 64, b = at / 32 % 2, l = at % 32;
+      const uint32_t* w = words + (b * 128 + l) * kOrderPitch + c;
+      *reinterpret_cast<uint4*>(p.to + (((static_cast<int64_t>(m) * p.chunks + c0 + c) * 2 + b) * 32 + l) * 16) =
+          make_uint4(w[0], w[32 * kOrderPitch], w[64 * kOrderPitch], w[96 * kOrderPitch]);
+    }
   }
 }
 
@@ -347,8 +385,17 @@ cudaError_t launch_tile(const mfr_expert_matmul_nvfp4_args& a, Params& p, cudaSt
 // The tile by the rows that an expert has, as in kernel_experts.cu.
 template <bool Gated>
 cudaError_t launch_by_rows(const mfr_expert_matmul_nvfp4_args& a, Params& p, cudaStream_t stream) {
-  if (a.num_rows <= int64_t{16} * a.E) return launch_tile<Gated, 1, 32>(a, p, stream);
-  return launch_tile<Gated, 2, 192>(a, p, stream);
+  if (nvfp4_few_rows(a.num_rows, a.E)) return launch_tile<Gated, 1, 32>(a, p, stream);
+  const int chunks = a.n_in / 64;
+  const int64_t blocks = expert_row_tiles(a.num_rows, a.E, kNvfp4Rows) * chunks * 2;
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(blocks)}, strides[1] = {512};
+  const cuuint32_t box[2] = {128, 8};
+  cudaError_t e = encode_map(&p.sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, a.workspace, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (e != cudaSuccess) return e;
+  const OrderParams o = {p.sf, p.offsets, p.counts, p.E, p.R, chunks, static_cast<int32_t>(blocks / 2 / chunks), static_cast<uint8_t*>(a.workspace)};
+  const int64_t turns = blocks / 2 / chunks * ((chunks + kOrderChunks - 1) / kOrderChunks), most = int64_t{sm_count()} * 4;
+  e = launch_pdl(order_scales_kernel, dim3(static_cast<unsigned>(turns < most ? turns : most)), kOrderThreads, 0, (a.flags & MFR_FLAG_PDL) != 0, stream, o);
+  return e != cudaSuccess ? e : launch_tile<Gated, 2, kNvfp4Rows>(a, p, stream);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@ skips the tensors' checks; the library's own stay).  Gradients are explicit call
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import Optional, Tuple
 
@@ -19,7 +20,8 @@ from .layer import DTYPE, _I, _L, _P, _PDL, _U, _ZERO_PADDING, _check_tensor, _c
 
 __all__ = [
     "moe_expert_matmul", "moe_expert_matmul_backward", "moe_swiglu_backward", "nvfp4_quantize", "nvfp4_dequantize",
-    "nvfp4_sf_bytes", "moe_expert_matmul_nvfp4", "moe_expert_read_timeouts",
+    "nvfp4_sf_bytes", "moe_expert_matmul_nvfp4", "moe_expert_matmul_nvfp4_workspace_bytes",
+    "moe_expert_read_timeouts",
 ]
 
 _SF_LAYOUT = {"row_major": 0, "swizzled_128x4": 1}
@@ -54,7 +56,8 @@ class _CNvfp4(ctypes.Structure):
 class _CExpertMatmulNvfp4(ctypes.Structure):
     _fields_ = [("E", _I), ("n_in", _I), ("n_out", _I), ("out_dtype", _I), ("gated", _I), ("num_rows", _L), ("codes", _P),
                 ("sf", _P), ("weight_codes", _P), ("weight_sf", _P), ("alpha", _P), ("expert_offsets", _P),
-                ("expert_counts", _P), ("out", _P), ("out_stride", _L), ("flags", _U)]
+                ("expert_counts", _P), ("out", _P), ("out_stride", _L), ("workspace", _P), ("workspace_bytes", _L),
+                ("flags", _U)]
 
 
 _pack_matmul, _pack_matmul_backward, _pack_swiglu = map(_packer, (_CExpertMatmul, _CExpertMatmulBackward, _CSwigluBackward))
@@ -73,6 +76,8 @@ def _bind(lib, raise_status):
         f = getattr(lib, name)
         f.argtypes, f.restype = [_P, _P], ctypes.c_int
     lib.moe_expert_read_timeouts.argtypes, lib.moe_expert_read_timeouts.restype = [ctypes.POINTER(_U)], ctypes.c_int
+    f = lib.moe_expert_matmul_nvfp4_workspace_bytes
+    f.argtypes, f.restype = [_I, _L, _I], _L
     lib.moe_nvfp4_sf_bytes.argtypes, lib.moe_nvfp4_sf_bytes.restype = [_I, _L, _I, _I], _L
 
 
@@ -379,16 +384,32 @@ def nvfp4_dequantize(codes: torch.Tensor, sf: torch.Tensor, scale: torch.Tensor,
     return out
 
 
+def moe_expert_matmul_nvfp4_workspace_bytes(E: int, rows: int, n_in: int) -> int:
+    """Workspace of ``moe_expert_matmul_nvfp4`` (0 for few rows an expert)."""
+    try:
+        struct.pack("<iqi", E, rows, n_in)
+    except struct.error as e:
+        raise ValueError(f"a size is not an integer of its range: {e}") from None
+    n = _lib.moe_expert_matmul_nvfp4_workspace_bytes(E, rows, n_in)
+    if n < 0:
+        _raise_status(int(n))
+    return int(n)
+
+
+_nvfp4_space = functools.lru_cache(maxsize=1024)(lambda E, rows, n_in: moe_expert_matmul_nvfp4_workspace_bytes(E, rows, n_in))
+
+
 def moe_expert_matmul_nvfp4(codes: torch.Tensor, sf: torch.Tensor, weight_codes: torch.Tensor, weight_sf: torch.Tensor,
                             expert_offsets: torch.Tensor, expert_counts: Optional[torch.Tensor] = None, *,
                             alpha: Optional[torch.Tensor] = None, gated: bool = False, dtype: torch.dtype = torch.bfloat16,
-                            out: Optional[torch.Tensor] = None, pdl: bool = True,
+                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, pdl: bool = True,
                             stream: Optional[torch.cuda.Stream] = None, check: bool = True) -> torch.Tensor:
     """``moe_expert_matmul`` over NVFP4: rows ``codes`` ([R, n_in / 2] uint8) with row-major scales ``sf`` ([R, n_in / 16]) and
     weights ``weight_codes`` ([E, n, n_in / 2]) with their scales in tiles ``weight_sf``, all as ``nvfp4_quantize`` writes them
     (``moe_dispatch`` moves codes and row-major scales into expert order).  ``y = alpha[e] * sum (code * sf) * (code * sf)``, summed
     in FP32, before the gate and the one rounding to ``dtype`` (bf16 or fp16); ``alpha`` ([E] fp32, default ones) undoes the two
-    global scales: 1 / (rows' scale * weights' scale).  n_in is a multiple of 64 and, with ``gated``, n_out one of 128."""
+    global scales: 1 / (rows' scale * weights' scale).  n_in is a multiple of 64 and, with ``gated``, n_out one of 128.
+    ``workspace`` (uint8, ``moe_expert_matmul_nvfp4_workspace_bytes``) must not be shared by calls that may run at the same time."""
     if not all(isinstance(t, torch.Tensor) for t in (codes, sf, weight_codes, weight_sf)) or codes.dim() != 2 or weight_codes.dim() != 3:
         raise ValueError("codes must be [rows, n_in / 2] and weight_codes [E, n, n_in / 2], with their scales")
     index = codes.get_device()
@@ -414,9 +435,19 @@ def moe_expert_matmul_nvfp4(codes: torch.Tensor, sf: torch.Tensor, weight_codes:
         if alpha is not None and not _good(alpha, index, (E,), torch.float32):
             _check_tensor("alpha", alpha, codes.device, (E,), torch.float32)
         _check_tensor("out", out, codes.device, (R, n_out), _ACT, contiguous=False)
+    if workspace is not None:
+        if check:
+            _check_tensor("workspace", workspace, codes.device, None, torch.uint8)
+        space = workspace.numel()
+    else:
+        space = _nvfp4_space(E, R, n_in)
+        if space:
+            workspace = torch.empty(space, dtype=torch.uint8, device=codes.device)
+            allocated.append(workspace)
     args = _pack_matmul_nvfp4(E, n_in, n_out, DTYPE[out.dtype], 1 if gated else 0, R, codes.data_ptr(), sf.data_ptr(),
                               weight_codes.data_ptr(), weight_sf.data_ptr(), _ptr(alpha), expert_offsets.data_ptr(),
-                              _ptr(expert_counts), *_row_tensor("out", out, index, (R, n_out), out.dtype, check), flags)
+                              _ptr(expert_counts), *_row_tensor("out", out, index, (R, n_out), out.dtype, check),
+                              _ptr(workspace) if space else 0, space, flags)
     _enqueue(_lib.moe_expert_matmul_nvfp4, args, index, stream, allocated)
     return out
 

@@ -36,7 +36,7 @@ def _structs(x):
 def test_every_declared_symbol_is_exported_and_bound(mfr):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b(moe_\w+)\s*\(", text))
-    assert len(names) == 8, names
+    assert len(names) == 9, names
     lib = ctypes.CDLL(mfr.library_path())
     for n in names:
         assert hasattr(lib, n), n
@@ -83,7 +83,7 @@ def _args(mfr, call):
                                   row_route=p(3), d_gate_up=p(4), d_gate_up_stride=256, out=p(5), out_stride=128, flags=1)
     if call == "moe_expert_matmul_nvfp4":
         return X._CExpertMatmulNvfp4(E=8, n_in=128, n_out=128, out_dtype=0, gated=1, num_rows=1000, codes=p(1), sf=p(2), weight_codes=p(3),
-                                     weight_sf=p(4), alpha=p(5), expert_offsets=p(6), expert_counts=p(7), out=p(8), out_stride=128, flags=5)
+                                     weight_sf=p(4), alpha=p(5), expert_offsets=p(6), expert_counts=p(7), out=p(8), out_stride=128, workspace=p(9), workspace_bytes=1 << 24, flags=5)
     return X._CNvfp4(matrices=2, rows=100, H=64, act_dtype=0, sf_layout=1, x=p(1), x_stride=64, scale=p(2), row_route=p(3), codes=p(4),
                      sf=p(5), flags=1)
 
@@ -113,7 +113,7 @@ BAD = {
     "moe_expert_matmul_nvfp4": COMMON + [
         dict(n_in=96), dict(n_out=64), dict(out_dtype=2), dict(gated=-1), dict(codes=None), dict(codes=0x10008), dict(sf=None), dict(sf=0x20002),
         dict(weight_codes=None), dict(weight_codes=0x30008), dict(weight_sf=None), dict(weight_sf=0x40008), dict(alpha=0x50002), dict(out=None),
-        dict(out=0x80008), dict(out_stride=120)],
+        dict(out=0x80008), dict(out_stride=120), dict(workspace=None), dict(workspace=0x90008), dict(workspace_bytes=1000)],
     "moe_nvfp4_quantize": NVFP4,
     "moe_nvfp4_dequantize": NVFP4,
 }
@@ -161,6 +161,16 @@ def test_scale_bytes(mfr):
     for args in ((1, 64, "tiles"), (1 << 64, 64), (1, 1 << 40)):
         with pytest.raises(ValueError):
             mfr.nvfp4_sf_bytes(*args)
+
+
+def test_nvfp4_workspace_bytes(mfr):
+    assert mfr.moe_expert_matmul_nvfp4_workspace_bytes(8, 128, 64) == 0
+    assert mfr.moe_expert_matmul_nvfp4_workspace_bytes(8, 1000, 128) == (1000 // 192 + 8) * 2 * 2 * 512
+    for args in ((0, 8, 64), (8, -1, 64), (8, 8, 96), (8, (1 << 31) - 1, 65536)):
+        with pytest.raises(mfr.MoEFinalizeError):
+            mfr.moe_expert_matmul_nvfp4_workspace_bytes(*args)
+    with pytest.raises(ValueError):
+        mfr.moe_expert_matmul_nvfp4_workspace_bytes(1 << 40, 8, 64)
 
 
 def test_cpu_tensors_and_wrong_shapes_are_refused(mfr):

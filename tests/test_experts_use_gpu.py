@@ -98,7 +98,12 @@ def test_wrong_offsets_touch_no_row_outside(mfr):
                               torch.tensor(cnt, dtype=torch.int32).cuda(), out=guard[40:80])
         mfr.moe_expert_matmul_backward(d.cuda(), x.cuda(), w.cuda().expand(2, 64, 64).contiguous(), torch.tensor(off, dtype=torch.int32).cuda(),
                                        torch.tensor(cnt, dtype=torch.int32).cuda(), d_rows=guard[40:80])
-        assert (guard[:40] == 7).all() and (guard[80:] == 7).all()
+        codes, sf = torch.zeros(40, 32, dtype=torch.uint8).cuda(), torch.zeros(40, 4, dtype=torch.uint8).cuda()
+        wc, ws = torch.zeros(2, 64, 32, dtype=torch.uint8).cuda(), torch.zeros(2, 512, dtype=torch.uint8).cuda()
+        space = torch.full((mfr.moe_expert_matmul_nvfp4_workspace_bytes(2, 40, 64) + 4096,), 9, dtype=torch.uint8).cuda()
+        mfr.moe_expert_matmul_nvfp4(codes, sf, wc, ws, torch.tensor(off, dtype=torch.int32).cuda(), torch.tensor(cnt, dtype=torch.int32).cuda(),
+                                    out=guard[40:80], workspace=space)
+        assert (guard[:40] == 7).all() and (guard[80:] == 7).all() and (space[-4096:] == 9).all()
 
 
 def test_elements_behind_two_to_the_31(mfr):
