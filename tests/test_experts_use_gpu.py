@@ -92,18 +92,20 @@ def test_no_rows_at_all(mfr):
 def test_wrong_offsets_touch_no_row_outside(mfr):
     """Device data that contradicts the call is cut to its rows; what is written behind them shows in the guard."""
     x, w, d, _, _ = _case([40], 64, 64, 4)
-    guard = torch.full((120, 64), 7.0, dtype=HF).cuda()
     for off, cnt in (([-5, 30, 1000], [1000, 1000]), ([2000000000, 2147483647, 5], [2147483647, -3]), ([10, 5, 0], [-1, 2])):
+        guard = torch.full((120, 64), 7.0, dtype=HF).cuda()
         mfr.moe_expert_matmul(x.cuda(), w.cuda().expand(2, 64, 64).contiguous(), torch.tensor(off, dtype=torch.int32).cuda(),
                               torch.tensor(cnt, dtype=torch.int32).cuda(), out=guard[40:80])
         mfr.moe_expert_matmul_backward(d.cuda(), x.cuda(), w.cuda().expand(2, 64, 64).contiguous(), torch.tensor(off, dtype=torch.int32).cuda(),
                                        torch.tensor(cnt, dtype=torch.int32).cuda(), d_rows=guard[40:80])
-        codes, sf = torch.zeros(40, 32, dtype=torch.uint8).cuda(), torch.zeros(40, 4, dtype=torch.uint8).cuda()
+        assert (guard[:40] == 7).all() and (guard[80:] == 7).all()
+        codes, sf = torch.zeros(60, 32, dtype=torch.uint8).cuda(), torch.zeros(60, 4, dtype=torch.uint8).cuda()
         wc, ws = torch.zeros(2, 64, 32, dtype=torch.uint8).cuda(), torch.zeros(2, 512, dtype=torch.uint8).cuda()
-        space = torch.full((mfr.moe_expert_matmul_nvfp4_workspace_bytes(2, 40, 64) + 4096,), 9, dtype=torch.uint8).cuda()
+        space = torch.full((mfr.moe_expert_matmul_nvfp4_workspace_bytes(2, 60, 64) + 4096,), 9, dtype=torch.uint8).cuda()
+        assert space.numel() > 4096
         mfr.moe_expert_matmul_nvfp4(codes, sf, wc, ws, torch.tensor(off, dtype=torch.int32).cuda(), torch.tensor(cnt, dtype=torch.int32).cuda(),
-                                    out=guard[40:80], workspace=space)
-        assert (guard[:40] == 7).all() and (guard[80:] == 7).all() and (space[-4096:] == 9).all()
+                                    out=guard[40:100], workspace=space)
+        assert (guard[:40] == 7).all() and (guard[100:] == 7).all() and (space[-4096:] == 9).all()
 
 
 def test_elements_behind_two_to_the_31(mfr):
