@@ -14,6 +14,11 @@
 // rows.  One warp copies the operands in by tensor copies, 64 values of the reduction a stage; one thread issues the matrix
 // instructions into one of two accumulators in tensor memory; four warps take finished accumulators out, round and store
 // them meanwhile.
+//
+// What bounds it, on GB300: with few rows HBM (64 tokens of 256 experts, top-8, 1024 x 6144 weights: 375 us, every weight read
+// once); with many the tensor pipe, 92 % busy (8 experts of 768 rows, 7168 x 4096: 211 us, 1.70 PFLOP/s), beside copies of 64 bytes a
+// cycle and SM, which alone take 0.8 of that; the weights' gradient its results beside those copies (64 experts of 384 rows,
+// 4096 x 4096: 721 us; 530 without stores, 404 without results).
 #include "experts_device.cuh"
 
 namespace mfr {

@@ -9,6 +9,10 @@
 // in turn, put them in order.  The rows' scales are row-major, since rows begin anywhere.  With few rows the same warps gather
 // them; with many that took longer than the instructions (32 sectors a load; 105 us where 84 go without it), so a kernel
 // before this one writes them in tiles, once for all columns' tiles.
+//
+// What bounds it, on GB300: with few rows HBM (16 tokens of 256 experts, top-8, 7168 x 2048 weights: 123.5 us, the floor); with many
+// the stages' turnaround, 0.35 us (8 experts of 768 rows, 7168 x 4096: 78 us, 4.6 PFLOP/s), gated the weights' scales on top of
+// it (99 us).
 #include "experts_device.cuh"
 
 namespace mfr {

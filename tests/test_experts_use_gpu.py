@@ -68,6 +68,30 @@ def test_many_rows_an_expert(mfr, n_in, n_out):
         assert torch.equal(dw[e], (d[s].double().T @ x[s].double()).half())
 
 
+@pytest.mark.parametrize("most", [3, 70])
+def test_as_many_experts_as_there_may_be(mfr, most):
+    g = torch.Generator().manual_seed(most)
+    counts = torch.randint(0, most, (1024,), generator=g)
+    counts[::7] = 0
+    counts = counts.tolist()
+    x, w, d, off, cnt = _case(counts, 64, 64, most)
+    args = [t.cuda() for t in (d, x, w, off, cnt)]
+    out = mfr.moe_expert_matmul(*args[1:]).cpu()
+    dx, dw = (t.cpu() for t in mfr.moe_expert_matmul_backward(*args))
+    assert torch.equal(out, _want(x, w, off, counts).half())
+    assert torch.equal(dx, _want(d, w.transpose(1, 2), off, counts).half())
+    of = torch.repeat_interleave(torch.arange(1024), torch.tensor(counts))
+    want = torch.zeros(1024, 64 * 64, dtype=torch.float64).index_add_(0, of, (d.double()[:, :, None] * x.double()[:, None, :]).flatten(1))
+    assert torch.equal(dw, want.view(1024, 64, 64).half())
+    # the same values in NVFP4: codes of whole numbers, every scale one
+    code = torch.tensor([12, 10, 0, 2, 4], dtype=torch.uint8)  # of -2 .. 2
+    pack = lambda t: (lambda c: c[..., 0::2] | (c[..., 1::2] << 4))(code[(t.double() + 2).long()])  # noqa: E731
+    ones = torch.full((1024, 128 * 4), 0x38, dtype=torch.uint8)
+    q = mfr.moe_expert_matmul_nvfp4(pack(x).cuda(), torch.full((x.shape[0], 4), 0x38, dtype=torch.uint8).cuda(), pack(w).cuda(), ones.cuda(),
+                                    *args[3:], dtype=HF).cpu()
+    assert torch.equal(q, out)
+
+
 def test_without_counts_every_row_up_to_the_next_expert(mfr):
     x, w, d, off, _ = _case([8, 0, 40], 64, 64, 3)
     args = [t.cuda() for t in (x, w, off)]
