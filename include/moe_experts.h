@@ -64,7 +64,7 @@ int moe_expert_matmul(const mfr_expert_matmul_args* args, struct CUstream_st* st
 /* The gradients of the product without the gate, given that of its output:
  *   d_rows[r, i]      = round(sum_n d_out[r, n] * weight[e, n, i])
  *   d_weight[e, n, i] = round(sum over the rows r of e of d_out[r, n] * rows[r, i])      0 for an expert of no rows
- * With accumulate (FP32 only), d_weight gets the sum added to it. */
+ * With accumulate (FP32 only), d_weight gets the sum added to it (magnitudes below 2^-126 count as 0). */
 typedef struct {
   int32_t E;
   int32_t n_in, n_out;

@@ -1,8 +1,8 @@
 // The elementwise operators between the experts' products: the gradient of the gate, NVFP4 quantisation and its inverse.
 // All are bound by memory: every input is read once and every output written once, 32 to 48 bytes a thread in flight.
 // A row is taken by `tpr` threads of a CTA (whole warps), so that no thread divides by a row's length.
-// Measured on GB300, 32768 rows: the gate's gradient of 2048 values 123 us (0.96 of the copy bandwidth); 7168 values to NVFP4 132 us
-// and back 108 (floor 89 each), both held up by their instructions (72 % of the issue slots).
+// Measured on GB300, 32768 rows: the gate's gradient of 2048 values 123 us (0.96 of the copy bandwidth); 7168 values to NVFP4 112 us
+// and back 110 (floor 89 each), both held up by their instructions.
 #include "experts_launch.h"
 
 namespace mfr {
@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const __grid_const
 // NVFP4
 // ------------------------------------------------------------------------------------------------
 
+constexpr int kPieces = 4;           // of 8 values, that a thread has in flight
 constexpr int kFp4Blocks = 152 * 8;  // CTAs at most: some turns of those that a GB300 holds at once
 
 struct Fp4Params {
@@ -143,8 +144,8 @@ __device__ __forceinline__ uint32_t largest(uint4 a) {
   return max(m & 0xffffu, m >> 16);
 }
 
-// A thread takes 8 values, two neighbouring ones a block, and two of its row's pieces at once.  Whole sectors go each way:
-// a block a thread, 32 bytes apart, was slower (H = 7168, 32768 rows: 210 us, with two rows a thread 134; 132 so).  The scale's bytes of four neighbouring
+// A thread takes 8 values, two neighbouring ones a block, and four of its row's pieces at once.  Whole sectors go each way:
+// a block a thread, 32 bytes apart, was slower (H = 7168, 32768 rows: 210 us; with two rows a thread 134; two pieces a thread 132; 112 so).  The scale's bytes of four neighbouring
 // blocks, one word of a tile, are written by one thread.
 template <typename T>
 __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const __grid_constant__ Fp4Params p) {
@@ -157,20 +158,20 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const __grid_consta
   int base = 0;
   if (i >= p.total) return;
   Fp4Row r = fp4_row(p, i);
-  uint4 a[2];
-  const auto load = [&](uint4 v[2], const Fp4Row& row, int k0) {
+  uint4 a[kPieces];
+  const auto load = [&](uint4 v[kPieces], const Fp4Row& row, int k0) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) v[u] = ldg16_if(p.x + row.row * p.x_stride + (k0 + u * p.tpr) * 16, row.live && k0 + u * p.tpr < 2 * p.blocks);
+    for (int u = 0; u < kPieces; ++u) v[u] = ldg16_if(p.x + row.row * p.x_stride + (k0 + u * p.tpr) * 16, row.live && k0 + u * p.tpr < 2 * p.blocks);
   };
   load(a, r, lane_k);
   while (true) {
     // the next pieces' loads are in flight while these are worked on
     int64_t next = i;
-    int next_base = base + 2 * p.tpr;
+    int next_base = base + kPieces * p.tpr;
     if (next_base >= 2 * p.blocks_up) next_base = 0, next += step;
     const bool more = next < p.total;
     Fp4Row r1 = r;
-    uint4 a1[2];
+    uint4 a1[kPieces];
     if (more) {
       if (next != i) r1 = fp4_row(p, next);
       load(a1, r1, next_base + lane_k);
@@ -178,43 +179,46 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const __grid_consta
     const int k0 = base + lane_k;
     uint8_t* codes = p.codes + r.row * (p.H / 2);
     uint8_t* to = p.sf + r.matrix * p.sf_bytes + row_at(p, r.m);
-    // of two neighbouring threads one finds the scale of their first block, the other that of their second
     const bool odd = (threadIdx.x & 1) != 0;
-    uint32_t top = largest(a[0]), top1 = largest(a[1]);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-    const float amax = Act<T>::unpack(odd ? top1 : top).x;
-    // a block that holds a NaN gets the scale NaN: its codes cannot say so
-    uint32_t found = amax != amax ? 0x7fu : __nv_cvt_float_to_fp8(__fmul_rn(__fdiv_rn(amax, 6.0f), g), __NV_SATFINITE, __NV_E4M3);
-    if (!r.real || k0 + (odd ? p.tpr : 0) >= 2 * p.blocks) found = 0;
-    const float wide = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(found), __NV_E4M3)));
-    const float inverse = wide == 0.0f ? 0.0f : __fdiv_rn(g, wide);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = k0 + u * p.tpr;
-      const bool here = r.real && k < 2 * p.blocks;
-      uint32_t sf = __shfl_sync(0xffffffffu, found, u, 2);
-      const float es = __shfl_sync(0xffffffffu, inverse, u, 2);
-      const float2 es2 = make_float2(es, es);
-      const uint32_t w[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
-      float2 y[4];
+    for (int v = 0; v < kPieces; v += 2) {
+      // of two neighbouring threads one finds the scale of their first block, the other that of their second
+      uint32_t top = largest(a[v]), top1 = largest(a[v + 1]);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+      const float amax = Act<T>::unpack(odd ? top1 : top).x;
+      // a block that holds a NaN gets the scale NaN: its codes cannot say so
+      uint32_t found = amax != amax ? 0x7fu : __nv_cvt_float_to_fp8(__fmul_rn(__fdiv_rn(amax, 6.0f), g), __NV_SATFINITE, __NV_E4M3);
+      if (!r.real || k0 + (odd ? v + 1 : v) * p.tpr >= 2 * p.blocks) found = 0;
+      const float wide = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(found), __NV_E4M3)));
+      const float inverse = wide == 0.0f ? 0.0f : __fdiv_rn(g, wide);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(Act<T>::unpack(w[j]), es2);
-      if (here) *reinterpret_cast<uint32_t*>(codes + k * 4) = to_e2m1x8(y);
-      if (p.layout == MFR_SF_ROW_MAJOR) {
-        if (here && (k & 1) == 0) to[k >> 1] = static_cast<uint8_t>(sf);
-      } else {
-        sf |= __shfl_down_sync(0xffffffffu, sf, 2) << 8;
-        sf |= __shfl_down_sync(0xffffffffu, sf, 4) << 16;
-        if ((k & 7) == 0 && k < 2 * p.blocks_up) *reinterpret_cast<uint32_t*>(to + block_at(p, k >> 1)) = sf;
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + (v + u) * p.tpr;
+        const bool here = r.real && k < 2 * p.blocks;
+        uint32_t sf = __shfl_sync(0xffffffffu, found, u, 2);
+        const float es = __shfl_sync(0xffffffffu, inverse, u, 2);
+        const float2 es2 = make_float2(es, es);
+        const uint32_t w[4] = {a[v + u].x, a[v + u].y, a[v + u].z, a[v + u].w};
+        float2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(Act<T>::unpack(w[j]), es2);
+        if (here) *reinterpret_cast<uint32_t*>(codes + k * 4) = to_e2m1x8(y);
+        if (p.layout == MFR_SF_ROW_MAJOR) {
+          if (here && (k & 1) == 0) to[k >> 1] = static_cast<uint8_t>(sf);
+        } else {
+          sf |= __shfl_down_sync(0xffffffffu, sf, 2) << 8;
+          sf |= __shfl_down_sync(0xffffffffu, sf, 4) << 16;
+          if ((k & 7) == 0 && k < 2 * p.blocks_up) *reinterpret_cast<uint32_t*>(to + block_at(p, k >> 1)) = sf;
+        }
       }
     }
     if (!more) break;
     i = next;
     base = next_base;
     r = r1;
-    a[0] = a1[0];
-    a[1] = a1[1];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) a[u] = a1[u];
   }
 }
 
@@ -236,36 +240,39 @@ __global__ void __launch_bounds__(512) nvfp4_dequantize_kernel(const __grid_cons
     const uint8_t* codes = p.codes + r.row * (p.H / 2);
     const uint8_t* from = p.sf + r.matrix * p.sf_bytes + row_at(p, r.m);
     uint8_t* x = const_cast<uint8_t*>(p.x) + r.row * p.x_stride;
-    for (int base = 0; base < 2 * p.blocks; base += 2 * p.tpr) {  // (by whole warps, for the shuffles)
+    for (int base = 0; base < 2 * p.blocks; base += kPieces * p.tpr) {  // (by whole warps, for the shuffles)
       const int k0 = base + lane_k;
-      uint32_t c[2], sf[2];
+      uint32_t c[kPieces], sf[kPieces];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kPieces; ++u) {
         const int k = k0 + u * p.tpr;
         const bool here = r.live && k < 2 * p.blocks;
         c[u] = here ? __ldg(reinterpret_cast<const uint32_t*>(codes + k * 4)) : 0;
         sf[u] = here ? __ldg(from + block_at(p, k >> 1)) : 0;
       }
-      // (one division for the two blocks of two neighbouring threads)
-      const uint32_t of = (threadIdx.x & 1) != 0 ? sf[1] : sf[0];
-      const float quotient = __fdiv_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(of), __NV_E4M3))), g);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int k = k0 + u * p.tpr;
-        const float es = __shfl_sync(0xffffffffu, quotient, u, 2);
-        const float2 es2 = make_float2(es, es);
-        uint32_t w[4];
+      for (int v = 0; v < kPieces; v += 2) {
+        // (one division for the two blocks of two neighbouring threads)
+        const uint32_t of = (threadIdx.x & 1) != 0 ? sf[v + 1] : sf[v];
+        const float quotient = __fdiv_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(of), __NV_E4M3))), g);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t h[2];
-          from_e2m1x4(c[u] >> (16 * i), h[0], h[1]);
+        for (int u = 0; u < 2; ++u) {
+          const int k = k0 + (v + u) * p.tpr;
+          const float es = __shfl_sync(0xffffffffu, quotient, u, 2);
+          const float2 es2 = make_float2(es, es);
+          uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float2 v = __fmul2_rn(Act<__half>::unpack(h[j]), es2);
-            w[2 * i + j] = Act<T>::pack(v.x, v.y);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t h[2];
+            from_e2m1x4(c[v + u] >> (16 * i), h[0], h[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 y = __fmul2_rn(Act<__half>::unpack(h[j]), es2);
+              w[2 * i + j] = Act<T>::pack(y.x, y.y);
+            }
           }
+          if (k < 2 * p.blocks) *reinterpret_cast<uint4*>(x + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (k < 2 * p.blocks) *reinterpret_cast<uint4*>(x + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
@@ -323,7 +330,7 @@ cudaError_t launch_swiglu_backward(const mfr_swiglu_backward_args& a, cudaStream
 
 cudaError_t launch_nvfp4_quantize(const mfr_nvfp4_args& a, cudaStream_t stream) {
   Fp4Params p = fp4_params(a, true);
-  const RowShape s = row_shape(p.blocks_up);  // (two pieces a block, and two a thread)
+  const RowShape s = row_shape((2 * p.blocks_up + kPieces - 1) / kPieces);
   p.tpr = s.tpr;
   const dim3 grid = fp4_grid(p, s);
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
@@ -333,7 +340,7 @@ cudaError_t launch_nvfp4_quantize(const mfr_nvfp4_args& a, cudaStream_t stream) 
 
 cudaError_t launch_nvfp4_dequantize(const mfr_nvfp4_args& a, cudaStream_t stream) {
   Fp4Params p = fp4_params(a, false);
-  const RowShape s = row_shape(p.blocks);
+  const RowShape s = row_shape((2 * p.blocks + kPieces - 1) / kPieces);
   p.tpr = s.tpr;
   const dim3 grid = fp4_grid(p, s);
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
