@@ -166,18 +166,22 @@ struct RowsOut {
   int32_t n;
 };
 
-// One CTA's part of a finished tile, by the 128 threads of the epilogue: 128 lanes of tensor memory at `d` (this warp's
-// quarter), the values f0.. of the rows row0 .. row0 + rows - 1, a column each, times `alpha`.  Gated, the lanes hold 8 gates,
-// their 8 others, and so on.  A thread has one value of 32 rows; through shared memory (two buffers of 8 KB at `boxes`),
-// where 16 (gated: 8) threads find 16 bytes each of a row: storing from the registers, 2 bytes a thread, took 10 us a tile of
-// 256 rows, more than most reductions, and this 3.4.
+// Four warps that take finished accumulators out together: kOutGroups of them share a tile, each with a buffer of its own.
+constexpr int kOutGroups = 2;
+constexpr int kOutBytes = 32 * 128 * 2;  // a buffer: 32 rows of 128 values
+
+// One CTA's part of a finished tile, by the 128 threads of group `group`: 128 lanes of tensor memory at `d` (this warp's
+// quarter), the values f0.. of the rows row0 .. row0 + rows_all - 1, a column each, times `alpha`.  Gated, the lanes hold 8 gates,
+// their 8 others, and so on.  A thread has one value of 32 rows; through shared memory, where 16 (gated: 8) threads find 16
+// bytes each of a row: storing from the registers, 2 bytes a thread, took 10 us a tile of 256 rows, more than most reductions,
+// and this 3.4 by one group.  The groups take 32 rows in turn, which matters where the reduction is short.
 template <typename T, bool Gated>
-__device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, int f0, float alpha, const RowsOut& to, uint8_t* boxes, int& stored) {
+__device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, int f0, float alpha, const RowsOut& to, uint8_t* box, int group) {
   constexpr int kLanes = 128, kLine = (Gated ? kLanes / 2 : kLanes) * 2;  // bytes of a row in this CTA's tile
-  const int r = threadIdx.x % kLanes;
+  const int r = threadIdx.x % kLanes, sync = 1 + group;
   const int64_t at = static_cast<int64_t>(f0) * 2;
 #pragma unroll 1
-  for (int c = 0; c < rows_all; c += 32) {
+  for (int c = group * 32; c < rows_all; c += kOutGroups * 32) {
     uint32_t w[32];
     tmem_load32(d + c, w);
     tmem_wait_load();
@@ -186,35 +190,32 @@ __device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, i
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * alpha;
     const int rows = rows_all - c < 32 ? rows_all - c : 32;
     const int64_t row = static_cast<int64_t>(row0) + c;
+    named_sync(sync, 128);  // the buffer's last rows are read
     if constexpr (Gated) {
       // lanes 0..7 of each 16 and 8..15 exchange, and each of the two computes every second row
       const int f = r / 16 * 8 + r % 8;
       const bool upper = (r & 8) != 0;
       if (to.gate_up != nullptr) {
-        uint8_t* box = boxes + (stored++ & 1) * (32 * kLanes * 2);
 #pragma unroll
         for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kLanes + (upper ? kLanes / 2 : 0) + f] = to_act<T>(v[j]);
-        named_sync(1, 128);
+        named_sync(sync, 128);
         store_rows<kLine>(to.gate_up + row * to.gate_up_stride + at, to.gate_up_stride, box, 2 * kLine, rows, to.n - f0);
         store_rows<kLine>(to.gate_up + row * to.gate_up_stride + at + static_cast<int64_t>(to.n) * 2, to.gate_up_stride, box + kLine, 2 * kLine, rows,
                           to.n - f0);
+        named_sync(sync, 128);
       }
-      uint8_t* box = boxes + (stored++ & 1) * (32 * kLanes * 2);
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
         const float y = swiglu(upper ? other : v[j], upper ? v[j + 1] : other);
         reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kLanes / 2) + f] = to_act<T>(y);
       }
-      named_sync(1, 128);
-      store_rows<kLine>(to.out + row * to.out_stride + at, to.out_stride, box, kLine, rows, to.n - f0);
     } else {
-      uint8_t* box = boxes + (stored++ & 1) * (32 * kLanes * 2);
 #pragma unroll
       for (int j = 0; j < 32; ++j) reinterpret_cast<T*>(box)[j * kLanes + r] = to_act<T>(v[j]);
-      named_sync(1, 128);
-      store_rows<kLine>(to.out + row * to.out_stride + at, to.out_stride, box, kLine, rows, to.n - f0);
     }
+    named_sync(sync, 128);
+    store_rows<kLine>(to.out + row * to.out_stride + at, to.out_stride, box, kLine, rows, to.n - f0);
   }
 }
 

@@ -12,8 +12,8 @@
 //
 // A persistent CTA, or a pair of CTAs that share the columns' operand, takes tiles of 128 (256) weight rows x at most BN
 // rows.  One warp copies the operands in by tensor copies, 64 values of the reduction a stage; one thread issues the matrix
-// instructions into one of two accumulators in tensor memory; four warps take finished accumulators out, round and store
-// them meanwhile.
+// instructions into one of two accumulators in tensor memory; two groups of four warps take finished accumulators out, round and
+// store them meanwhile.
 //
 // What bounds it, on GB300: with few rows HBM (64 tokens of 256 experts, top-8, 1024 x 6144 weights: 375 us, every weight read
 // once); with many the tensor pipe, 92 % busy (8 experts of 768 rows, 7168 x 4096: 211 us, 1.70 PFLOP/s), beside copies of 64 bytes a
@@ -29,7 +29,8 @@ namespace {
 
 enum Dir { kForward = 0, kGated = 1, kRowsGrad = 2, kWeightGrad = 3 };
 
-constexpr int kEpilogueWarp = 4;                 // first of four, the weights' gradient: of two groups of four
+constexpr int kEpilogueWarp = 4;                 // first of kOutGroups groups of four
+constexpr int kThreads = 32 * (kEpilogueWarp + 4 * kOutGroups);
 constexpr int kDepth = 64;                       // reduction values of a stage: lines of 128 bytes
 constexpr int kTileM = kExpertTileRows;          // rows of A of one CTA
 constexpr int kABytes = kTileM * kDepth * 2;
@@ -54,18 +55,16 @@ struct Shape {
   static constexpr int kBRows = BN / Ctas;  // columns of D whose operand this CTA copies
   static constexpr int kBBytes = kBRows * kDepth * 2;
   static constexpr int kStage = kABytes + kBBytes;
-  // results leave by two buffers: 128 lines of 128 bytes of the weights' gradient (one for each group of warps), or 32 rows of the tile's values
-  static constexpr int kOutBytes = D == kWeightGrad ? kTileM * 128 : 32 * kTileM * 2;
+  // results leave by a buffer for each group of warps: 128 lines of 128 bytes of the weights' gradient, or 32 rows of the tile's values
+  static constexpr int kOut = D == kWeightGrad ? kTileM * 128 : kOutBytes;
   static constexpr int kStages = D == kWeightGrad ? 196608 / kStage : 204800 / kStage;
-  static constexpr int kGroups = D == kWeightGrad ? 2 : 1;  // groups of four warps that take results out
-  static constexpr int kThreads = 32 * (kEpilogueWarp + 4 * kGroups);
   static constexpr bool kALines = D == kRowsGrad || D == kWeightGrad;
   static constexpr bool kBLines = D == kWeightGrad;
   static constexpr int kFeatures = (D == kGated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
   static constexpr int kUnit = Ctas == 1 ? 16 : 32;  // an instruction's columns are a multiple
   // what one CTA holds besides the stages: the barriers and, but for the weights' gradient, the experts' first tiles
   static constexpr int kFixed = kBarBytes + (D == kWeightGrad ? 0 : (MFR_MAX_EXPERTS + 1 + 33) * 4);
-  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kOutBytes + kFixed;
+  static constexpr int kSmem = 1024 + kStages * kStage + kOutGroups * kOut + kFixed;
 };
 
 struct Tile {
@@ -121,12 +120,12 @@ __device__ __forceinline__ void clear_lines(uint32_t stage, int from) {
 
 // T: the operands' type; O: that of D (FP32 for the weights' gradient alone).
 template <int D, int Ctas, int BN, typename T, typename O>
-__global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, Ctas, BN>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const uint32_t stage0 = smem_addr(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage + 2 * S::kOutBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage + kOutGroups * S::kOut);
   const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * S::kStages;
   // (the next two kinds: the weights' gradient alone)
   const uint32_t tail0 = empty0 + 8 * S::kStages, ready0 = tail0 + 8 * S::kStages;
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(dfull0 + 8 * i, 1);
-      mbar_init(dempty0 + 8 * i, 4 * S::kGroups * Ctas);
+      mbar_init(dempty0 + 8 * i, 4 * kOutGroups * Ctas);
     }
     *give_up = 0;
     fence_mbar_init();
@@ -290,7 +289,6 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
     // ---- finished accumulators
     const int quarter = warp % 4, group = (warp - kEpilogueWarp) / 4, sync = 1 + group;
     uint32_t buf = 0, dphase = 0;
-    int stored = 0;  // buffers so far
     for (uint32_t t = t0; t < tiles; t += dt) {
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
       const bool some = x.steps > 0;
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
         const int m0 = x.m0 + rank * kTileM;
         if (some || !p.accumulate) {
           // (each group half of the columns, by a buffer of its own)
-          const uint32_t box = stage0 + S::kStages * S::kStage + group * S::kOutBytes;
+          const uint32_t box = stage0 + S::kStages * S::kStage + group * S::kOut;
           const bool first_thread = threadIdx.x % 128 == 0;
 #pragma unroll 1
           for (int c = group * (BN / 2); c < (group + 1) * (BN / 2) && x.n0 + c < p.n_n; c += kLine) {
@@ -351,7 +349,8 @@ __global__ void __launch_bounds__(Shape<D, Ctas, BN>::kThreads, 1) expert_kernel
           }
         }
       } else {
-        store_tile<T, D == kGated>(d, x.rows, x.row0, x.m0 + rank * (S::kFeatures / Ctas), 1.0f, p.to, smem + S::kStages * S::kStage, stored);
+        store_tile<T, D == kGated>(d, x.rows, x.row0, x.m0 + rank * (S::kFeatures / Ctas), 1.0f, p.to, smem + S::kStages * S::kStage + group * S::kOut,
+                                     group);
       }
       if (some) {
         tmem_fence_before();
@@ -386,7 +385,7 @@ cudaError_t launch(Params& p, int64_t most_tiles, bool pdl, cudaStream_t stream)
   const int sms = sm_count() / Ctas * Ctas;
   if (sms == 0) return cudaErrorInvalidDevice;
   const int64_t want = most_tiles * Ctas;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(want < sms ? want : sms)), S::kThreads, S::kSmem, pdl, stream, p, Ctas);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(want < sms ? want : sms)), kThreads, S::kSmem, pdl, stream, p, Ctas);
 }
 
 CUtensorMapDataType map_type(int act) { return act == MFR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }

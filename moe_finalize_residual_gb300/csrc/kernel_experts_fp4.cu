@@ -21,17 +21,16 @@ __device__ unsigned int g_expert_nvfp4_wait_timeouts = 0;
 
 namespace {
 
-constexpr int kThreads = 448;
-constexpr int kEpilogueWarp = 4;  // first of four
-constexpr int kScaleWarp = 8;     // first of six
+constexpr int kEpilogueWarp = 4;  // first of kOutGroups groups of four
+constexpr int kScaleWarp = kEpilogueWarp + 4 * kOutGroups;
 constexpr int kScaleWarps = 6;
+constexpr int kThreads = 32 * (kScaleWarp + kScaleWarps);
 constexpr int kDepth = 256;       // reduction values of a stage: lines of 128 bytes
 constexpr int kTileM = kExpertTileRows;
 constexpr int kABytes = kTileM * 128;
 constexpr int kSfaBytes = kTileM * kDepth / 16;
 constexpr int kBoxRows = 32;      // rows of a box of B
 constexpr int kBarBytes = 512;
-constexpr int kOutBytes = 32 * kTileM * 2;
 
 struct Params {
   CUtensorMap a, b, b_small, sfa, sfb;  // (sfa: not gated; sfb: rows' scales in order; both 512 bytes a row)
@@ -59,7 +58,7 @@ struct Shape {
   static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
   static constexpr int kStage = (kStageBytes + 1023) / 1024 * 1024;
   static constexpr int kStages = 209920 / kStage;
-  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kOutBytes + kBarBytes + (MFR_MAX_EXPERTS + 1 + 33) * 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kOutGroups * kOutBytes + kBarBytes + (MFR_MAX_EXPERTS + 1 + 33) * 4;
   static constexpr int kFeatures = (Gated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
   static constexpr int kUnit = Ctas == 1 ? 16 : 32;
   // tensor-memory columns: two accumulators, then areas of a stage's scales, 4 bytes a lane and column
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
   uint8_t* smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const uint32_t stage0 = smem_addr(smem);
   uint8_t* boxes = smem + S::kStages * S::kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + 2 * kOutBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + kOutGroups * kOutBytes);
   const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * S::kStages, sf0 = empty0 + 8 * S::kStages;
   const uint32_t dfull0 = sf0 + 8 * S::kStages, dempty0 = dfull0 + 16;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 3 * S::kStages + 4);
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(dfull0 + 8 * i, 1);
-      mbar_init(dempty0 + 8 * i, 4 * Ctas);
+      mbar_init(dempty0 + 8 * i, 4 * kOutGroups * Ctas);
     }
     *give_up = 0;
     fence_mbar_init();
@@ -234,17 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
       zero_free_rows(p.to.out, p.to.out_stride, static_cast<int64_t>(p.n_out) * 2, p.offsets, p.counts, p.E, p.R, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
   } else if (warp < kScaleWarp) {
     // ---- finished accumulators
-    const int quarter = warp - kEpilogueWarp;
+    const int quarter = warp % 4, group = (warp - kEpilogueWarp) / 4;
     uint32_t buf = 0, dphase = 0;
-    int stored = 0;
     for (uint32_t t = t0; t < tiles; t += dt) {
       const Tile x = tile_at<Gated, Ctas, BN>(p, first, t);
       if (x.rows <= 0) continue;
       const float alpha = p.alpha == nullptr ? 1.0f : p.alpha[x.e];
-      if (!named_all(1, 128, wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, timeouts))) break;  // (the four warps share their stores)
+      if (!named_all(1 + group, 128, wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, timeouts))) break;  // (the four warps share their stores)
       tmem_fence_after();
       store_tile<T, Gated>(tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16), x.rows, x.row0, x.m0 + rank * (S::kFeatures / Ctas), alpha,
-                           p.to, boxes, stored);
+                           p.to, boxes + group * kOutBytes, group);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) {
