@@ -174,7 +174,7 @@ constexpr int kOutBytes = 32 * 128 * 2;  // a buffer: 32 rows of 128 values
 // quarter), the values f0.. of the rows row0 .. row0 + rows_all - 1, a column each, times `alpha`.  Gated, the lanes hold 8 gates,
 // their 8 others, and so on.  A thread has one value of 32 rows; through shared memory, where 16 (gated: 8) threads find 16
 // bytes each of a row: storing from the registers, 2 bytes a thread, took 10 us a tile of 256 rows, more than most reductions,
-// and this 3.4 by one group.  The groups take 32 rows in turn, which matters where the reduction is short.
+// and this 3.4 by one group.  The groups take 32 rows in turn, which gains a tenth where the reduction is short.
 template <typename T, bool Gated>
 __device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, int f0, float alpha, const RowsOut& to, uint8_t* box, int group) {
   constexpr int kLanes = 128, kLine = (Gated ? kLanes / 2 : kLanes) * 2;  // bytes of a row in this CTA's tile
@@ -184,7 +184,7 @@ __device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, i
   for (int c = group * 32; c < rows_all; c += kOutGroups * 32) {
     uint32_t w[32];
     tmem_load32(d + c, w);
-    tmem_wait_load();
+    tmem_wait_load(w);
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * alpha;

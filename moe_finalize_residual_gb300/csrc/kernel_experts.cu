@@ -18,7 +18,7 @@
 // What bounds it, on GB300: with few rows HBM (64 tokens of 256 experts, top-8, 1024 x 6144 weights: 375 us, every weight read
 // once); with many the tensor pipe, 92 % busy (8 experts of 768 rows, 7168 x 4096: 211 us, 1.70 PFLOP/s), beside copies of 64 bytes a
 // cycle and SM, which alone take 0.8 of that; the weights' gradient its results beside those copies (64 experts of 384 rows,
-// 4096 x 4096: 721 us; 530 without stores, 404 without results).
+// 4096 x 4096: 720 to 750 us; 530 without stores, 404 without results).
 #include "experts_device.cuh"
 
 namespace mfr {
@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             if (some) {
 #pragma unroll
               for (int h = 0; h < kLine; h += 32) tmem_load32(d + c + h, v + h);
-              tmem_wait_load();
+              tmem_wait_load(v);
+              if constexpr (kLine == 64) tmem_after_wait(v + 32);
             } else {
 #pragma unroll
               for (int i = 0; i < kLine; ++i) v[i] = 0;
