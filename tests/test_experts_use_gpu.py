@@ -403,3 +403,59 @@ def test_refusals_on_the_gpu(mfr):
         with pytest.raises(mfr.MoEFinalizeError):
             call()
     torch.cuda.synchronize()
+
+
+def _nvfp4_large(seed):
+    """A case whose rows' scales take the workspace, and its result."""
+    g = torch.Generator().manual_seed(seed)
+    counts, n_in, n = [130, 0, 250, 41], 320, 136
+    off, R = ref.order(counts)
+    codes, wc = (torch.randint(0, 256, s, generator=g, dtype=torch.uint8) for s in ((R, n_in // 2), (4, n, n_in // 2)))
+    sf, ws = (torch.randint(40, 60, s, generator=g, dtype=torch.uint8) for s in ((R, n_in // 16), (4, 256 * (n_in // 16))))
+    return [t.cuda() for t in (codes, sf, wc, ws, off, torch.tensor(counts, dtype=torch.int32))]
+
+
+def test_nvfp4_on_other_streams_and_without_programmatic_launch(mfr):
+    args = _nvfp4_large(1)
+    assert mfr.moe_expert_matmul_nvfp4_workspace_bytes(4, args[0].shape[0], 320) > 0
+    want = mfr.moe_expert_matmul_nvfp4(*args, pdl=False)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [mfr.moe_expert_matmul_nvfp4(*args, stream=streams[i % 2], pdl=i % 3 > 0) for i in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    x, w, d, off, cnt = (t.cuda() for t in _case([300, 5, 0, 250], 136, 264, 2))
+    for call in (lambda p: mfr.moe_expert_matmul(x, w, off, cnt, pdl=p), lambda p: mfr.moe_expert_matmul_backward(d, x, w, off, cnt, pdl=p)[0],
+                 lambda p: mfr.moe_swiglu_backward(x[:, :64], d[:, :128], pdl=p)[0], lambda p: mfr.nvfp4_quantize(d[:, :256], torch.ones(1).cuda(), pdl=p)[0]):
+        assert torch.equal(call(True), call(False))
+
+
+def test_two_graphs_at_once(mfr):
+    """Two captured graphs, each with the workspace that its call allocated, replayed beside each other."""
+    cases = [_nvfp4_large(s) for s in (3, 4)]
+    wants = [mfr.moe_expert_matmul_nvfp4(*c) for c in cases]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for c, s in zip(cases, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append([mfr.moe_expert_matmul_nvfp4(*c) for _ in range(3)])
+        graphs.append(g)
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for held, w in zip(outs, wants) for o in held)
+
+
+def test_a_workspace_that_is_passed_in(mfr):
+    args = _nvfp4_large(5)
+    need = mfr.moe_expert_matmul_nvfp4_workspace_bytes(4, args[0].shape[0], 320)
+    space = torch.full((need + 512,), 0x7f, dtype=torch.uint8).cuda()  # scales that are not numbers, where it is not written
+    assert torch.equal(mfr.moe_expert_matmul_nvfp4(*args, workspace=space), mfr.moe_expert_matmul_nvfp4(*args))
+    assert (space[need:] == 0x7f).all()
+    with pytest.raises(mfr.MoEFinalizeError):
+        mfr.moe_expert_matmul_nvfp4(*args, workspace=space[:need - 1])
+    with pytest.raises(ValueError):
+        mfr.moe_expert_matmul_nvfp4(*args, workspace=space.cpu())
