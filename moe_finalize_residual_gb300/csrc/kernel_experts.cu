@@ -18,7 +18,7 @@
 // What bounds it, on GB300: with few rows HBM (64 tokens of 256 experts, top-8, 1024 x 6144 weights: 375 us, every weight read
 // once); with many the tensor pipe, 92 % busy (8 experts of 768 rows, 7168 x 4096: 211 us, 1.70 PFLOP/s), beside copies of 64 bytes a
 // cycle and SM, which alone take 0.8 of that; the weights' gradient its results beside those copies (64 experts of 384 rows,
-// 4096 x 4096: 720 to 750 us; 530 without stores, 404 without results).
+// 4096 x 4096: 645 us; by pairs 720 to 750, of it 530 without stores and 404 without results).
 #include "experts_device.cuh"
 
 namespace mfr {
@@ -111,9 +111,11 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
 // behind the expert's last, which must not count.  In both operands, since 0 * NaN is NaN.
 template <typename S>
 __device__ __forceinline__ void clear_lines(uint32_t stage, int from) {
-  const int each = (kDepth - from) * 8;  // 16-byte pieces of a block of 64 columns
-  for (int i = threadIdx.x & 31; i < S::kStage / (64 * kDepth * 2) * each; i += 32)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + i / each * (64 * kDepth * 2) + from * 128 + i % each * 16), "r"(0) : "memory");
+  constexpr int kBlock = 64 * kDepth * 2;  // bytes of 64 columns, line by line
+#pragma unroll
+  for (int block = 0; block < S::kStage / kBlock; ++block)
+    for (int at = from * 128 + (threadIdx.x & 31) * 16; at < kBlock; at += 512)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + block * kBlock + at), "r"(0) : "memory");
   fence_async_shared();
   __syncwarp();
 }
@@ -494,7 +496,12 @@ cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, 
   p.n_m = a.n_out;
   p.n_n = a.n_in;
   p.accumulate = a.accumulate;
-  return a.n_out > kTileM ? launch_weights<2>(a, p, stream) : launch_weights<1>(a, p, stream);
+  // A pair's tiles cost more of a turnaround and fewer copies.  Measured, 32 experts of 4096 x 4096: 128 rows each 181 us by one CTA
+  // a tile and 311 by pairs, 256 rows 248 and 354, 384 to 483 rows 436 and 437, 512 rows 408 and 391, 768 rows 563 and 492.  The rows
+  // of the call are a little more than the experts', by their alignment.  (With at most 128 rows of weights the pair's second CTA
+  // would have none.)
+  const bool pair = a.num_rows >= int64_t{512} * a.E && a.n_out > kTileM;
+  return pair ? launch_weights<2>(a, p, stream) : launch_weights<1>(a, p, stream);
 }
 
 cudaError_t read_and_reset_expert_timeouts(unsigned int* count) {

@@ -53,16 +53,18 @@ def test_strided_rows_weights_and_outputs(mfr):
         assert torch.equal(dw.cpu()[e], (d[s].double().T @ x[s].double()).half())
 
 
-@pytest.mark.parametrize("n_in,n_out", [(264, 512), (512, 24)])
-def test_many_rows_an_expert(mfr, n_in, n_out):
-    """Several tiles of rows, by pairs of CTAs, with experts of one row and of none between."""
-    counts = [700, 0, 523, 1, 256, 257]
+@pytest.mark.parametrize("n_in,n_out", [(264, 512), (512, 24), (136, 264)])
+@pytest.mark.parametrize("counts", [[700, 0, 523, 1, 256, 257], [1100, 1, 523], [1024, 640], [0, 2051]])
+def test_many_rows_an_expert(mfr, counts, n_in, n_out):
+    """Several tiles of rows, by pairs of CTAs (the weights' gradient in all but the first), with experts of one row and of none."""
     x, w, d, off, cnt = _case(counts, n_in, n_out, 2)
     args = [t.cuda() for t in (d, x, w, off, cnt)]
     out = mfr.moe_expert_matmul(*args[1:]).cpu()
     dx, dw = (t.cpu() for t in mfr.moe_expert_matmul_backward(*args))
+    _, dw32 = mfr.moe_expert_matmul_backward(*args[:2], None, *args[3:], want_d_rows=False, d_weight=torch.full(w.shape, 3.0).cuda(), accumulate=True)
     want = _want(x, w, off, counts)
     assert want.abs().max() <= 2048 and torch.equal(out, want.half())
+    assert torch.equal(dw32.cpu() - 3, dw.float()) and dw.abs().max() <= 2048 and (dw[torch.tensor(counts) == 0] == 0).all()
     for e, s in ref.spans(off, counts):
         assert torch.equal(dx[s], (d[s].double() @ w[e].double()).half())
         assert torch.equal(dw[e], (d[s].double().T @ x[s].double()).half())
