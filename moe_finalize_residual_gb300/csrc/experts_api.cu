@@ -72,7 +72,7 @@ int check_matmul(const mfr_expert_matmul_args* a) {
   if (a == nullptr) return fail(MFR_ERR_INVALID_ARG, "args is NULL");
   int st;
   if ((st = check_experts(a->E, a->num_rows, a->expert_offsets, a->expert_counts)) != MFR_OK || (st = check_width("n_in", a->n_in, 8)) != MFR_OK ||
-      (st = check_width("n_out", a->n_out, 8)) != MFR_OK || (st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING)) != MFR_OK)
+      (st = check_width("n_out", a->n_out, 8)) != MFR_OK || (st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING | MFR_FLAG_TEST_STREAM_TIMEOUT)) != MFR_OK)
     return st;
   if (!act(a->act_dtype)) return fail(MFR_ERR_UNSUPPORTED, "act_dtype %d: only MFR_BF16 and MFR_FP16", a->act_dtype);
   if (a->gated != 0 && a->gated != 1) return fail(MFR_ERR_INVALID_ARG, "gated = %d is not 0 or 1", a->gated);
@@ -91,7 +91,7 @@ int check_matmul_backward(const mfr_expert_matmul_backward_args* a) {
   if (a == nullptr) return fail(MFR_ERR_INVALID_ARG, "args is NULL");
   int st;
   if ((st = check_experts(a->E, a->num_rows, a->expert_offsets, a->expert_counts)) != MFR_OK || (st = check_width("n_in", a->n_in, 8)) != MFR_OK ||
-      (st = check_width("n_out", a->n_out, 8)) != MFR_OK || (st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING)) != MFR_OK)
+      (st = check_width("n_out", a->n_out, 8)) != MFR_OK || (st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING | MFR_FLAG_TEST_STREAM_TIMEOUT)) != MFR_OK)
     return st;
   if (!act(a->act_dtype)) return fail(MFR_ERR_UNSUPPORTED, "act_dtype %d: only MFR_BF16 and MFR_FP16", a->act_dtype);
   if (a->d_weight_dtype != a->act_dtype && a->d_weight_dtype != MFR_FP32)
@@ -162,7 +162,7 @@ int check_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args* a) {
   int st;
   if ((st = check_experts(a->E, a->num_rows, a->expert_offsets, a->expert_counts)) != MFR_OK || (st = check_width("n_in", a->n_in, 64)) != MFR_OK ||
       (st = check_width("n_out", a->n_out, a->gated == 1 ? 128 : 8)) != MFR_OK ||
-      (st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING)) != MFR_OK)
+      (st = check_flags(a->flags, MFR_FLAG_PDL | MFR_FLAG_ZERO_PADDING | MFR_FLAG_TEST_STREAM_TIMEOUT)) != MFR_OK)
     return st;
   if (!act(a->out_dtype)) return fail(MFR_ERR_UNSUPPORTED, "out_dtype %d: only MFR_BF16 and MFR_FP16", a->out_dtype);
   if (a->gated != 0 && a->gated != 1) return fail(MFR_ERR_INVALID_ARG, "gated = %d is not 0 or 1", a->gated);

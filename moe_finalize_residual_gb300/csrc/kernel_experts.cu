@@ -47,6 +47,7 @@ struct Params {
   int32_t n_n;         // the weights' gradient: columns of D
   int32_t tiles_m, tiles_n;  // row tiles of D; the weights' gradient: column tiles
   int32_t zero_free, accumulate;
+  int32_t test_extra;  // arrivals that a stage's barrier expects and that never come (1 only under the failure-detection test hook)
   RowsOut to;          // (but for the weights' gradient)
 };
 
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, 1 + p.test_extra);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(tail0 + 8 * s, 1);
       mbar_init(ready0 + 8 * s, Ctas);
@@ -437,6 +438,7 @@ cudaError_t launch_expert_matmul(const mfr_expert_matmul_args& a, cudaStream_t s
   p.n_red = a.n_in;
   p.n_m = a.n_out;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
+  p.test_extra = (a.flags & MFR_FLAG_TEST_STREAM_TIMEOUT) != 0;
   p.to = {static_cast<uint8_t*>(a.out), a.out_stride * 2, static_cast<uint8_t*>(a.gate_up), a.gate_up_stride * 2, a.n_out};
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
   return a.gated ? launch_by_rows<kGated>(a.act_dtype, a.num_rows, a.E, a.rows, a.rows_stride, p, pdl, stream)
@@ -455,6 +457,7 @@ cudaError_t launch_expert_rows_grad(const mfr_expert_matmul_backward_args& a, cu
   p.n_red = a.n_out;
   p.n_m = a.n_in;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
+  p.test_extra = (a.flags & MFR_FLAG_TEST_STREAM_TIMEOUT) != 0;
   p.to = {static_cast<uint8_t*>(a.d_rows), a.d_rows_stride * 2, nullptr, 0, a.n_in};
   return launch_by_rows<kRowsGrad>(a.act_dtype, a.num_rows, a.E, a.d_out, a.d_out_stride, p, (a.flags & MFR_FLAG_PDL) != 0, stream);
 }
@@ -496,6 +499,7 @@ cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, 
   p.n_m = a.n_out;
   p.n_n = a.n_in;
   p.accumulate = a.accumulate;
+  p.test_extra = (a.flags & MFR_FLAG_TEST_STREAM_TIMEOUT) != 0;
   // A pair's tiles cost more of a turnaround and fewer copies.  Measured, 32 experts of 4096 x 4096: 128 rows each 181 us by one CTA
   // a tile and 311 by pairs, 256 rows 248 and 354, 384 to 483 rows 436 and 437, 512 rows 408 and 391, 768 rows 563 and 492.  The rows
   // of the call are a little more than the experts', by their alignment.  (With at most 128 rows of weights the pair's second CTA

@@ -44,6 +44,7 @@ struct Params {
   int32_t tiles_m;
   int32_t sf_tiles;          // tiles of 128 weight rows an expert
   int32_t zero_free;
+  int32_t test_extra;        // as in kernel_experts.cu
   RowsOut to;
 };
 
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);    // the copies' bytes
+      mbar_init(full0 + 8 * s, 1 + p.test_extra);  // the copies' bytes
       mbar_init(sf0 + 8 * s, Ctas);   // the scales that the warps put in order
       mbar_init(empty0 + 8 * s, 1);
     }
@@ -331,6 +332,7 @@ struct OrderParams {
   uint8_t* to;
 };
 __global__ void __launch_bounds__(kOrderThreads) order_scales_kernel(const __grid_constant__ OrderParams p) {
+  static_assert(kNvfp4Rows > 128 && kNvfp4Rows <= kOrderRows, "two blocks of rows");
   __shared__ uint32_t words[kOrderRows * kOrderPitch];
   __shared__ int first[MFR_MAX_EXPERTS + 1 + 33];
   pdl_launch_dependents();
@@ -426,6 +428,7 @@ cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cu
   p.n_in = a.n_in;
   p.n_out = a.n_out;
   p.zero_free = (a.flags & MFR_FLAG_ZERO_PADDING) != 0;
+  p.test_extra = (a.flags & MFR_FLAG_TEST_STREAM_TIMEOUT) != 0;
   p.to = {static_cast<uint8_t*>(a.out), a.out_stride * 2, nullptr, 0, a.n_out};
   return a.gated ? launch_by_rows<true>(a, p, stream) : launch_by_rows<false>(a, p, stream);
 }

@@ -461,3 +461,31 @@ def test_a_workspace_that_is_passed_in(mfr):
         mfr.moe_expert_matmul_nvfp4(*args, workspace=space[:need - 1])
     with pytest.raises(ValueError):
         mfr.moe_expert_matmul_nvfp4(*args, workspace=space.cpu())
+
+
+@pytest.mark.parametrize("rows", [3, 700])
+@pytest.mark.parametrize("call", ["product", "rows", "weights", "nvfp4"])
+def test_a_wait_that_runs_out_is_counted(mfr, call, rows):
+    """A barrier that expects one arrival more than come: the call ends after its limit, is counted, and the next one is right."""
+    X, timeout = mfr.experts, mfr.MFR_FLAG_TEST_STREAM_TIMEOUT
+    x, w, d, off, cnt = (t.cuda() for t in _case([rows], 128, 256, 20))
+    dx, dw, out = torch.empty_like(x), torch.empty_like(w), torch.empty_like(d)
+    ptr = lambda *ts: [t.data_ptr() for t in ts]  # noqa: E731
+    codes, wc, ws = (torch.zeros(*s, dtype=torch.uint8).cuda() for s in ((rows, 64), (1, 256, 64), (1, 256 * 8)))
+    sf, space = torch.zeros(rows, 8, dtype=torch.uint8).cuda(), torch.zeros(1 << 20, dtype=torch.uint8).cuda()
+    if call == "product":
+        f, args = "moe_expert_matmul", X._pack_matmul(1, 128, 256, 1, 0, rows, x.data_ptr(), 128, w.data_ptr(), 128, 256 * 128, *ptr(off, cnt, out), 256, 0, 0, timeout)
+    elif call == "nvfp4":
+        f, args = "moe_expert_matmul_nvfp4", X._pack_matmul_nvfp4(1, 128, 256, 1, 0, rows, *ptr(codes, sf, wc, ws), 0, *ptr(off, cnt, out), 256, space.data_ptr(), 1 << 20, timeout)
+    else:
+        f, args = "moe_expert_matmul_backward", X._pack_matmul_backward(
+            1, 128, 256, 1, 1, 0, rows, x.data_ptr(), 128, w.data_ptr(), 128, 256 * 128, d.data_ptr(), 256, *ptr(off, cnt),
+            dx.data_ptr() if call == "rows" else 0, 128, dw.data_ptr() if call == "weights" else 0, timeout)
+    assert mfr.moe_expert_read_timeouts() == 0
+    assert getattr(mfr.raw_library(), f)(args, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert mfr.moe_expert_read_timeouts() > 0 and mfr.moe_expert_read_timeouts() == 0
+    assert torch.equal(mfr.moe_expert_matmul(x, w, off, cnt).cpu(), _want(x.cpu(), w.cpu(), off.cpu(), [rows]).half())
+    got = mfr.moe_expert_matmul_backward(d, x, w, off, cnt)
+    assert torch.equal(got[0].cpu(), (d.double() @ w[0].double()).half().cpu()) and torch.equal(got[1][0].cpu(), (d.double().T @ x.double()).half().cpu())
+    assert mfr.moe_expert_read_timeouts() == 0
