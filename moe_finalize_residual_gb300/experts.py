@@ -103,6 +103,12 @@ def _weight(t, index, act, check):
     return E, n, n_in, (t.data_ptr(), row, s[0] if E > 1 else n * row)
 
 
+def _act_tensor(name, t, index, shape):
+    """A tensor of either 16-bit type, its rows apart or not."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in _ACT and t.get_device() == index and t.shape == shape):
+        _check_tensor(name, t, torch.device("cuda", index), shape, _ACT, contiguous=False)
+
+
 def _first(name, t, check):
     """Device index and type of the call's first tensor, which the others follow."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -377,7 +383,7 @@ def nvfp4_dequantize(codes: torch.Tensor, sf: torch.Tensor, scale: torch.Tensor,
         if index < 0:
             _check_tensor("codes", codes, codes.device, None, torch.uint8)
         _check_nvfp4(codes, sf, scale, row_route, index, lead, rows, H, layout, matrices)
-        _check_tensor("out", out, codes.device, (*lead, H), _ACT, contiguous=False)
+        _act_tensor("out", out, index, (*lead, H))
     args = _pack_nvfp4(matrices, rows, H, DTYPE[out.dtype], layout, *_x("out", out, index, matrices, rows, H, check), scale.data_ptr(),
                        _ptr(row_route), codes.data_ptr(), sf.data_ptr(), _PDL if pdl else 0)
     _enqueue(_lib.moe_nvfp4_dequantize, args, index, stream, allocated)
@@ -434,7 +440,7 @@ def moe_expert_matmul_nvfp4(codes: torch.Tensor, sf: torch.Tensor, weight_codes:
         _check_order(expert_offsets, expert_counts, index, E)
         if alpha is not None and not _good(alpha, index, (E,), torch.float32):
             _check_tensor("alpha", alpha, codes.device, (E,), torch.float32)
-        _check_tensor("out", out, codes.device, (R, n_out), _ACT, contiguous=False)
+        _act_tensor("out", out, index, (R, n_out))
     if workspace is not None:
         if check:
             _check_tensor("workspace", workspace, codes.device, None, torch.uint8)
