@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include "experts_launch.h"
+#include "gate_device.cuh"
 #include "mma_device.cuh"
 
 namespace mfr {
@@ -128,10 +129,6 @@ __device__ __forceinline__ void zero_free_rows(uint8_t* out, int64_t stride_byte
     }
   }
 }
-
-// g / (1 + exp(-g)) * u.  The quotient is 0 below g = -87, where it is smaller than 1e-35 (the fast division's largest divisor
-// is 2^126).
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // ------------------------------------------------------------------------------------------------
 // Results

@@ -4,6 +4,7 @@
 // Measured on GB300, 32768 rows: the gate's gradient of 2048 values 123 us (0.96 of the copy bandwidth); 7168 values to NVFP4 112 us
 // and back 110 (floor 89 each), both held up by their instructions.
 #include "experts_launch.h"
+#include "gate_device.cuh"
 
 namespace mfr {
 namespace {
@@ -71,12 +72,12 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const __grid_const
       float a[2], b[2], c[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // the logistic function of g; where exp(-g) is infinite it is 0
-        const float s = __frcp_rn(1.0f + __expf(-g[i + j]));
-        const float sg = g[i + j] * s;
-        a[j] = d[i + j] * u[i + j] * (s * (1.0f + (g[i + j] - sg)));
-        b[j] = d[i + j] * sg;
-        c[j] = sg * u[i + j];
+        const float G = g[i + j], U = u[i + j], D = d[i + j];
+        const Logistic p = logistic(G);
+        const float sg = G * p.m * p.r;  // (times m: g / (1 + exp(-g)))
+        a[j] = scaled_product(D, U, p.m, p.m * (p.r * (1.0f + (G - sg * p.m))));
+        b[j] = sg * (D * p.m);
+        c[j] = sg * (U * p.m);
       }
       dg[i / 2] = Act<T>::pack(a[0], a[1]);
       du[i / 2] = Act<T>::pack(b[0], b[1]);

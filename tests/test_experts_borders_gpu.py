@@ -1,0 +1,81 @@
+"""The experts' products where they can go wrong: gates far below zero."""
+import pytest
+import torch
+
+import experts_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def mfr():
+    import moe_finalize_residual_gb300 as m
+    yield m
+    torch.cuda.synchronize()
+    assert m.moe_expert_read_timeouts() == 0
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# The gate
+# ----------------------------------------------------------------------------------------------------------------
+
+def _spread(g, *shape):
+    """BF16 values of either sign over most of the type's range."""
+    sign = 1.0 - 2.0 * torch.randint(0, 2, shape, generator=g)
+    return (sign * torch.exp((torch.rand(*shape, generator=g) * 2 - 1) * 86)).to(BF)
+
+
+def _gates(g, *shape):
+    """Gates whose exponential halves stay normal numbers in FP32, most of them below zero."""
+    return (torch.rand(*shape, generator=g) * 200 - 168).to(BF)
+
+
+def _near(name, got, want, rel):
+    """One rounding to BF16 of a value that is off by at most ``rel`` of it, below the type's normal numbers by one of them, and
+    infinite where the value may round beyond the largest."""
+    got, off, tiny = got.double(), rel * want.abs(), 2.0 ** -126
+    top = torch.finfo(BF).max
+    beyond = want.abs() + off > top
+    assert (torch.isfinite(got) | beyond).all(), f"{name} is not finite"
+    assert ((got == torch.sign(want) * float("inf")) | ((got - want).abs() <= off + 2.0 ** -8 * (want.abs() + off)) | ~beyond).all(), name
+    bad = ~beyond & ((got - want).abs() > off + 2.0 ** -8 * (want.abs() + off) + tiny)
+    assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} off"
+
+
+def _logistic(g):
+    return torch.where(g >= 0, 1 / (1 + torch.exp(-g)), torch.exp(g) / (1 + torch.exp(g)))
+
+
+@pytest.mark.parametrize("rows", [8, 64])
+def test_the_gate_of_large_negative_values(mfr, rows):
+    """Rows with a single one pick out the weights, so the gate's inputs are the weights' BF16 values: its output is g / (1 + exp(-g)) * u
+    wherever that is a normal number, however small the quotient alone is."""
+    F, n_in = 128, 64
+    g = torch.Generator().manual_seed(rows)
+    gate, up = _gates(g, F, n_in), _spread(g, F, n_in)
+    gate[0, :8] = torch.tensor([-87.0, -87.5, -88.0, -88.5, -89.0, -95.0, -104.0, -1e4]).to(BF)
+    up[0, :8] = torch.tensor([1e33, 1e33, 1e33, 1e33, 1e35, 1e38, 1e38, 1e38]).to(BF)
+    x = torch.eye(n_in)[torch.arange(rows) % n_in].to(BF)
+    off, cnt = torch.tensor([0, rows], dtype=torch.int32).cuda(), torch.tensor([rows], dtype=torch.int32).cuda()
+    out = mfr.moe_expert_matmul(x.cuda(), torch.cat([gate, up])[None].cuda(), off, cnt, gated=True).cpu()
+    a, b = gate.double().T[:rows], up.double().T[:rows]
+    # the exponential of half the gate, twice: 2^-22 each, and 0.75 |g| * 2^-23 by the rounding of its argument; a few operations
+    _near("out", out, a * _logistic(a) * b, (a.abs() + 8) * 2.0 ** -23)
+
+
+def test_the_gates_gradient_of_large_negative_values(mfr):
+    R, F = 40, 512
+    g = torch.Generator().manual_seed(3)
+    gate, up, d = _gates(g, R, F), _spread(g, R, F), _spread(g, R, F)
+    gate[0, :8] = torch.tensor([-87.5, -88.5, -89.0, -95.0, -115.0, -60.0, -1e4, -150.0]).to(BF)
+    up[0, :8] = torch.tensor([1e33, 1e33, 1e35, 1e38, 3e38, 1e20, 1e38, 1e37]).to(BF)
+    d[0, :8] = torch.tensor([1.0, 1.0, 1e-3, 1e10, 1e-25, 1e20, 1e38, 1e37]).to(BF)
+    d_x, y = (t.cpu() for t in mfr.moe_swiglu_backward(d.cuda(), torch.cat([gate, up], 1).cuda()))
+    a, b, e = gate.double(), up.double(), d.double()
+    p, rel = _logistic(a), (a.abs() + 8) * 2.0 ** -23
+    _near("act", y, a * p * b, rel)
+    _near("d_up", d_x[:, F:], e * a * p, rel)
+    # 1 + g (1 - p) has a zero; its error is relative to its terms
+    slope = 1 + a * (1 - p)
+    _near("d_gate", d_x[:, :F], e * b * p * slope, rel * (1 + 2 * a.abs()) / slope.abs())
