@@ -28,6 +28,7 @@ extern "C" {
 #endif
 
 #define MFR_MAX_EXPERT_WIDTH 65536
+#define MFR_MAX_EXPERT_ROWS 2147482624 /* 2^31 - 1024: rows of a product, in whole tiles of any kernel */
 
 /* ---------------------------------------------------------------------------------------------------- */
 /* 16-bit products                                                                                        */
@@ -44,7 +45,7 @@ typedef struct {
   int32_t n_in, n_out;           /* multiples of 8, 8..MFR_MAX_EXPERT_WIDTH                              */
   int32_t act_dtype;             /* MFR_BF16 or MFR_FP16, of every tensor here                           */
   int32_t gated;                 /* 0 or 1                                                              */
-  int64_t num_rows;              /* rows of `rows` and `out`, 0 <= num_rows < 2^31                        */
+  int64_t num_rows;              /* rows of `rows` and `out`, 0..MFR_MAX_EXPERT_ROWS                      */
   const void* rows;              /* device [num_rows, n_in], 16-byte aligned                             */
   int64_t rows_stride;           /* elements from row to row, a multiple of 8, >= n_in                    */
   const void* weight;            /* device [E, n_out or 2 * n_out, n_in], 16-byte aligned                 */

@@ -34,6 +34,13 @@ int check_rows(int64_t rows) {
   return MFR_OK;
 }
 
+// Rows in expert order: the kernels round their numbers up to whole tiles in 32 bits.
+int check_expert_rows(int64_t rows) {
+  if (rows < 0 || rows > MFR_MAX_EXPERT_ROWS)
+    return fail(MFR_ERR_INVALID_ARG, "num_rows = %lld outside [0, %lld]", static_cast<ll>(rows), static_cast<ll>(MFR_MAX_EXPERT_ROWS));
+  return MFR_OK;
+}
+
 // A tensor of rows: its pointer and the distance of its rows in elements.
 int check_tensor(const char* name, const void* p, int64_t stride, int64_t width) {
   if (p == nullptr || !aligned(p, 16)) return fail(MFR_ERR_INVALID_ARG, "%s is NULL or not 16-byte aligned", name);
@@ -45,7 +52,7 @@ int check_tensor(const char* name, const void* p, int64_t stride, int64_t width)
 
 int check_experts(int E, int64_t num_rows, const int32_t* offsets, const int32_t* counts) {
   if (E < 1 || E > MFR_MAX_EXPERTS) return fail(MFR_ERR_INVALID_ARG, "E = %d outside [1, %d]", E, MFR_MAX_EXPERTS);
-  const int st = check_rows(num_rows);
+  const int st = check_expert_rows(num_rows);
   if (st != MFR_OK) return st;
   if (offsets == nullptr || !aligned(offsets, 4) || !aligned(counts, 4))
     return fail(MFR_ERR_INVALID_ARG, "expert_offsets is NULL, or it or expert_counts not 4-byte aligned");
@@ -232,7 +239,7 @@ int moe_nvfp4_dequantize(const mfr_nvfp4_args* args, struct CUstream_st* stream)
 int64_t moe_expert_matmul_nvfp4_workspace_bytes(int32_t E, int64_t num_rows, int32_t n_in) {
   int st;
   if (E < 1 || E > MFR_MAX_EXPERTS) return fail(MFR_ERR_INVALID_ARG, "E = %d outside [1, %d]", E, MFR_MAX_EXPERTS);
-  if ((st = check_rows(num_rows)) != MFR_OK || (st = check_width("n_in", n_in, 64)) != MFR_OK) return st;
+  if ((st = check_expert_rows(num_rows)) != MFR_OK || (st = check_width("n_in", n_in, 64)) != MFR_OK) return st;
   if (nvfp4_few_rows(num_rows, E)) return 0;
   const int64_t blocks = expert_row_tiles(num_rows, E, kNvfp4Rows) * (n_in / 64) * 2;
   if (blocks > INT32_MAX) return fail(MFR_ERR_INVALID_ARG, "%lld blocks of scales: 2^31 or more", static_cast<ll>(blocks));

@@ -101,7 +101,7 @@ __device__ __forceinline__ RowPart row_part(const int* first, const int32_t* off
   x.e = tile_expert(first, E, m);
   const RowSpan s = expert_rows(offsets, counts, x.e, R);
   const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
-  const int part = ((n + parts - 1) / parts + unit - 1) / unit * unit;
+  const int part = static_cast<int>((static_cast<uint32_t>(n) + parts - 1) / parts + unit - 1) / unit * unit;  // (n + parts may pass 2^31)
   const int at = (m - first[x.e]) * part;
   x.row0 = s.begin + at;
   x.rows = at < 0 ? 0 : n - at < part ? n - at : part;

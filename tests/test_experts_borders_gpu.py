@@ -1,4 +1,4 @@
-"""The experts' products where they can go wrong: gates far below zero."""
+"""The experts' products where they can go wrong: gates far below zero, as many rows as a call takes."""
 import pytest
 import torch
 
@@ -79,3 +79,36 @@ def test_the_gates_gradient_of_large_negative_values(mfr):
     # 1 + g (1 - p) has a zero; its error is relative to its terms
     slope = 1 + a * (1 - p)
     _near("d_gate", d_x[:, :F], e * b * p * slope, rel * (1 + 2 * a.abs()) / slope.abs())
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Rows
+# ----------------------------------------------------------------------------------------------------------------
+
+def _room(gb):
+    """Skips where so many GB are not free."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gb << 30:
+        pytest.skip(f"{gb} GB of device memory are wanted")
+
+
+def _count(t):
+    """Elements that are not zero, a piece at a time."""
+    return sum(int(torch.count_nonzero(p)) for p in t.split(1 << 27))
+
+
+def test_the_most_rows_there_may_be(mfr):
+    """One expert of as many rows as a call takes: the first, the last and some between hold values, the others zeros."""
+    R, n = (1 << 31) - 1024, 8
+    _room(90)
+    g = torch.Generator().manual_seed(4)
+    at = torch.cat([torch.arange(300), torch.randint(300, R - 300, (400,), generator=g).unique(), torch.arange(R - 300, R)]).cuda()
+    x, y = torch.zeros(R, n, dtype=HF, device="cuda"), torch.empty(R, n, dtype=HF, device="cuda")
+    some, w = torch.randint(1, 3, (at.numel(), n), generator=g).to(HF).cuda(), torch.randint(1, 3, (1, n, n), generator=g).to(HF).cuda()
+    x[at] = some
+    off, cnt = torch.tensor([0, R], dtype=torch.int32).cuda(), torch.tensor([R], dtype=torch.int32).cuda()
+    for product, want in ((lambda: mfr.moe_expert_matmul(x, w, off, cnt, out=y), some.double() @ w[0].double().T),
+                          (lambda: mfr.moe_expert_matmul_backward(x, None, w, off, cnt, d_rows=y, want_d_weight=False), some.double() @ w[0].double())):
+        y.fill_(1.0)
+        product()
+        assert torch.equal(y[at].double(), want) and _count(y) == want.numel()
