@@ -13,7 +13,8 @@
  * expert e has the rows expert_offsets[e] .. expert_offsets[e] + expert_counts[e] - 1 (without counts: up to
  * expert_offsets[e + 1]), any number of them, none included.  The other rows belong to no expert: they are not used,
  * whatever they hold, and their output rows are left as they were, or set to zero under MFR_FLAG_ZERO_PADDING.
- * Offsets and counts are device data: they are cut to [0, num_rows], and experts must not share rows.
+ * Offsets and counts are device data: they are cut to [0, num_rows].  Experts come in the order of their rows and must not share any:
+ * where they do, no row outside is touched and rows' products take no more tiles than num_rows rows fill, but what is written is not defined.
  *
  * Products are of the stored values, exactly, and summed in FP32 by the tensor cores; what is rounded to 16 bits is
  * rounded once.  Every result is the same from run to run.

@@ -47,34 +47,36 @@ __device__ __forceinline__ RowSpan expert_rows(const int32_t* offsets, const int
   return s;
 }
 
-// first[e] = the tiles of `tile` rows of the experts before e, e = 0..E, by all threads of the CTA; `scratch` holds 33 ints.
-__device__ __forceinline__ void count_tiles(int* first, int* scratch, const int32_t* offsets, const int32_t* counts, int E, int R, int tile) {
+// first[e] = the tiles of `tile` rows of the experts before e, e = 0..E, by all threads of the CTA; `scratch` holds 32 ints.  At most
+// `most` of them, what R rows fill (below 2^31): where experts share rows the sums could be E times that.
+__device__ __forceinline__ void count_tiles(int* first, int* scratch, const int32_t* offsets, const int32_t* counts, int E, int R, int tile, int most) {
   const int n = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int per = (E + n - 1) / n;
-  int sum = 0;
+  const auto add = [most](int a, int b) { return static_cast<int>(min(static_cast<uint32_t>(a) + b, static_cast<uint32_t>(most))); };
+  const auto tiles = [&](int e) {
+    const RowSpan s = expert_rows(offsets, counts, e, R);
+    return (s.end - s.begin + tile - 1) / tile;
+  };
+  int upto = 0;  // the sum up to this thread's experts
   for (int i = 0; i < per; ++i) {
     const int e = t * per + i;
-    if (e < E) {
-      const RowSpan s = expert_rows(offsets, counts, e, R);
-      sum += (s.end - s.begin + tile - 1) / tile;
-    }
+    if (e < E) upto = add(upto, tiles(e));
   }
-  int before = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += v;
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto = add(upto, v);
   }
-  if (lane == 31) scratch[warp] = before;
+  if (lane == 31) scratch[warp] = upto;
+  int at = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) at = 0;
   __syncthreads();
-  int at = before - sum;
-  for (int w = 0; w < warp; ++w) at += scratch[w];
+  for (int w = 0; w < warp; ++w) at = add(at, scratch[w]);
   for (int i = 0; i < per; ++i) {
     const int e = t * per + i;
     if (e < E) {
-      const RowSpan s = expert_rows(offsets, counts, e, R);
       first[e] = at;
-      at += (s.end - s.begin + tile - 1) / tile;
+      at = add(at, tiles(e));
     }
   }
   if (t == n - 1) first[E] = at;
@@ -91,17 +93,18 @@ __device__ __forceinline__ int tile_expert(const int* first, int E, int m) {
   return lo;
 }
 
-// The rows of tile number m: an expert's rows in equal parts, a multiple of `unit` but for the last, since a short last one would
-// use the weights' copies badly.
+// The rows of tile number m, at most `tile`: an expert's rows in equal parts, a multiple of `unit` but for the last, since a short last
+// one would use the weights' copies badly.
 struct RowPart {
   int e, row0, rows;  // (rows not positive: the parts before it took all)
 };
-__device__ __forceinline__ RowPart row_part(const int* first, const int32_t* offsets, const int32_t* counts, int E, int R, int m, int unit) {
+__device__ __forceinline__ RowPart row_part(const int* first, const int32_t* offsets, const int32_t* counts, int E, int R, int m, int tile, int unit) {
   RowPart x;
   x.e = tile_expert(first, E, m);
   const RowSpan s = expert_rows(offsets, counts, x.e, R);
   const int parts = first[x.e + 1] - first[x.e], n = s.end - s.begin;
-  const int part = static_cast<int>((static_cast<uint32_t>(n) + parts - 1) / parts + unit - 1) / unit * unit;  // (n + parts may pass 2^31)
+  const int equal = static_cast<int>((static_cast<uint32_t>(n) + parts - 1) / parts + unit - 1) / unit * unit;  // (n + parts may pass 2^31)
+  const int part = equal < tile ? equal : tile;  // (fewer parts than it takes: experts share rows)
   const int at = (m - first[x.e]) * part;
   x.row0 = s.begin + at;
   x.rows = at < 0 ? 0 : n - at < part ? n - at : part;

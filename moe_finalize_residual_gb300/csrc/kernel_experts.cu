@@ -46,6 +46,7 @@ struct Params {
   int32_t n_m;         // values of an output row, as in `to` (the weights' gradient: rows of D)
   int32_t n_n;         // the weights' gradient: columns of D
   int32_t tiles_m, tiles_n;  // row tiles of D; the weights' gradient: column tiles
+  int32_t row_tiles;   // tiles of the rows in expert order, at most (but for the weights' gradient)
   int32_t zero_free, accumulate;
   int32_t test_extra;  // arrivals that a stage's barrier expects and that never come (1 only under the failure-detection test hook)
   RowsOut to;          // (but for the weights' gradient)
@@ -64,7 +65,7 @@ struct Shape {
   static constexpr int kFeatures = (D == kGated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
   static constexpr int kUnit = Ctas == 1 ? 16 : 32;  // an instruction's columns are a multiple
   // what one CTA holds besides the stages: the barriers and, but for the weights' gradient, the experts' first tiles
-  static constexpr int kFixed = kBarBytes + (D == kWeightGrad ? 0 : (MFR_MAX_EXPERTS + 1 + 33) * 4);
+  static constexpr int kFixed = kBarBytes + (D == kWeightGrad ? 0 : (MFR_MAX_EXPERTS + 1 + 32) * 4);
   static constexpr int kSmem = 1024 + kStages * kStage + kOutGroups * kOut + kFixed;
 };
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
     const int m = t / p.tiles_m;
     x.m0 = t % p.tiles_m * S::kFeatures;
     x.n0 = 0;
-    const RowPart part = row_part(first, p.offsets, p.counts, p.E, p.R, m, S::kUnit);
+    const RowPart part = row_part(first, p.offsets, p.counts, p.E, p.R, m, BN, S::kUnit);
     x.e = part.e;
     x.row0 = part.row0;
     x.rows = part.rows;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   pdl_launch_dependents();
   pdl_wait();
   if constexpr (D != kWeightGrad)
-    count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, BN);
+    count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, BN, p.row_tiles);
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   tmem_fence_after();
@@ -402,7 +403,8 @@ cudaError_t launch_rows(int act, int64_t R, int E, const void* rows, int64_t row
   if (e == cudaSuccess && S::kBRows > kBoxRows) e = encode_rows(&p.b_small, map_type(act), rows, p.n_red, R, rows_stride * 2, kDepth, kBoxRows);
   if (e != cudaSuccess) return e;
   p.tiles_m = (p.n_m + S::kFeatures - 1) / S::kFeatures;
-  const int64_t tiles = expert_row_tiles(R, E, BN) * p.tiles_m;
+  p.row_tiles = static_cast<int32_t>(expert_row_tiles(R, E, BN));
+  const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.tiles_m;
   return act == MFR_BF16 ? launch<D, Ctas, BN, __nv_bfloat16, __nv_bfloat16>(p, tiles, pdl, stream)
                          : launch<D, Ctas, BN, __half, __half>(p, tiles, pdl, stream);
 }

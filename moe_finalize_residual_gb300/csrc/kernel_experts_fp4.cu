@@ -42,6 +42,7 @@ struct Params {
   int32_t E, R;
   int32_t n_in, n_out;
   int32_t tiles_m;
+  int32_t row_tiles;         // tiles of the rows, at most
   int32_t sf_tiles;          // tiles of 128 weight rows an expert
   int32_t zero_free;
   int32_t test_extra;        // as in kernel_experts.cu
@@ -59,7 +60,7 @@ struct Shape {
   static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
   static constexpr int kStage = (kStageBytes + 1023) / 1024 * 1024;
   static constexpr int kStages = 209920 / kStage;
-  static constexpr int kSmem = 1024 + kStages * kStage + kOutGroups * kOutBytes + kBarBytes + (MFR_MAX_EXPERTS + 1 + 33) * 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kOutGroups * kOutBytes + kBarBytes + (MFR_MAX_EXPERTS + 1 + 32) * 4;
   static constexpr int kFeatures = (Gated ? kTileM / 2 : kTileM) * Ctas;  // values of an output row in a tile
   static constexpr int kUnit = Ctas == 1 ? 16 : 32;
   // tensor-memory columns: two accumulators, then areas of a stage's scales, 4 bytes a lane and column
@@ -82,7 +83,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* first, uint3
   Tile x;
   const int m = t / p.tiles_m;
   x.m0 = t % p.tiles_m * S::kFeatures;
-  const RowPart part = row_part(first, p.offsets, p.counts, p.E, p.R, m, S::kUnit);
+  const RowPart part = row_part(first, p.offsets, p.counts, p.E, p.R, m, BN, S::kUnit);
   x.e = part.e;
   x.row0 = part.row0;
   x.rows = part.rows;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
   if (warp == 2) tmem_alloc<Ctas>(smem_addr(tmem_at), 512);
   pdl_launch_dependents();
   pdl_wait();
-  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, BN);
+  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, BN, p.row_tiles);
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
   tmem_fence_after();
@@ -328,21 +329,21 @@ struct OrderParams {
   const int32_t* offsets;
   const int32_t* counts;
   int32_t E, R, chunks;
-  int32_t tiles;  // that the workspace holds: more than experts that share no rows fill
+  int32_t tiles;  // of the rows, at most: the workspace holds so many
   uint8_t* to;
 };
 __global__ void __launch_bounds__(kOrderThreads) order_scales_kernel(const __grid_constant__ OrderParams p) {
   static_assert(kNvfp4Rows > 128 && kNvfp4Rows <= kOrderRows, "two blocks of rows");
   __shared__ uint32_t words[kOrderRows * kOrderPitch];
-  __shared__ int first[MFR_MAX_EXPERTS + 1 + 33];
+  __shared__ int first[MFR_MAX_EXPERTS + 1 + 32];
   pdl_launch_dependents();
   pdl_wait();
-  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, kNvfp4Rows);
+  count_tiles(first, first + MFR_MAX_EXPERTS + 1, p.offsets, p.counts, p.E, p.R, kNvfp4Rows, p.tiles);
   const int groups = (p.chunks + kOrderChunks - 1) / kOrderChunks;
-  const int64_t all = static_cast<int64_t>(first[p.E] < p.tiles ? first[p.E] : p.tiles) * groups;
+  const int64_t all = static_cast<int64_t>(first[p.E]) * groups;
   for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
     const int m = static_cast<int>(i / groups), c0 = static_cast<int>(i % groups) * kOrderChunks;
-    const RowPart x = row_part(first, p.offsets, p.counts, p.E, p.R, m, 32);
+    const RowPart x = row_part(first, p.offsets, p.counts, p.E, p.R, m, kNvfp4Rows, 32);
     const int n = p.chunks - c0 < kOrderChunks ? p.chunks - c0 : kOrderChunks;
     __syncthreads();  // (the last turn's words are read)
 #pragma unroll 4
@@ -381,7 +382,8 @@ cudaError_t launch_tile(const mfr_expert_matmul_nvfp4_args& a, Params& p, cudaSt
   if (e == cudaSuccess && S::kBRows > kBoxRows) e = encode_rows(&p.b_small, type, a.codes, line, a.num_rows, line, 128, kBoxRows);
   if (e != cudaSuccess) return e;
   p.tiles_m = (a.n_out + S::kFeatures - 1) / S::kFeatures;
-  const int64_t tiles = expert_row_tiles(a.num_rows, a.E, BN) * p.tiles_m;
+  p.row_tiles = static_cast<int32_t>(expert_row_tiles(a.num_rows, a.E, BN));
+  const int64_t tiles = static_cast<int64_t>(p.row_tiles) * p.tiles_m;
   const bool pdl = (a.flags & MFR_FLAG_PDL) != 0;
   return a.out_dtype == MFR_BF16 ? launch<Gated, Ctas, BN, __nv_bfloat16>(p, tiles, pdl, stream) : launch<Gated, Ctas, BN, __half>(p, tiles, pdl, stream);
 }

@@ -1,4 +1,5 @@
-"""The experts' products where they can go wrong: gates far below zero, as many rows as a call takes."""
+"""The experts' products where they can go wrong: gates far below zero, as many rows as a call takes, experts that share
+rows."""
 import pytest
 import torch
 
@@ -112,3 +113,25 @@ def test_the_most_rows_there_may_be(mfr):
         y.fill_(1.0)
         product()
         assert torch.equal(y[at].double(), want) and _count(y) == want.numel()
+
+
+def test_experts_that_share_all_rows_end(mfr):
+    """Offsets that give every expert every row: the tiles that 1024 experts would fill pass 2^32, those that the call works on are
+    no more than its rows fill."""
+    E, R, n = 1024, 1 << 29, 8
+    _room(40)
+    off, cnt = torch.zeros(E + 1, dtype=torch.int32).cuda(), torch.full((E,), R, dtype=torch.int32).cuda()
+    x, y = torch.zeros(R, n, dtype=HF, device="cuda"), torch.full((R + 1, n), 7.0, dtype=HF, device="cuda")
+    w = torch.ones(E, n, n, dtype=HF).cuda()
+    mfr.moe_expert_matmul(x, w, off, cnt, out=y[:R])
+    mfr.moe_expert_matmul_backward(x, None, w, off, cnt, d_rows=y[:R], want_d_weight=False)
+    assert (y[R] == 7).all() and mfr.moe_expert_read_timeouts() == 0
+    del x, y
+    R = 1 << 25
+    cnt.fill_(R)
+    codes, sf = torch.zeros(R, 32, dtype=torch.uint8, device="cuda"), torch.zeros(R, 4, dtype=torch.uint8, device="cuda")
+    y = torch.full((R + 1, n), 7.0, dtype=BF, device="cuda")
+    space = torch.full((mfr.moe_expert_matmul_nvfp4_workspace_bytes(E, R, 64) + 4096,), 9, dtype=torch.uint8, device="cuda")
+    mfr.moe_expert_matmul_nvfp4(codes, sf, torch.zeros(E, n, 32, dtype=torch.uint8).cuda(), torch.zeros(E, 512, dtype=torch.uint8).cuda(), off, cnt,
+                                out=y[:R], workspace=space)
+    assert (y[R] == 7).all() and (space[-4096:] == 9).all() and mfr.moe_expert_read_timeouts() == 0
