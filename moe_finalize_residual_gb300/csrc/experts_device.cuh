@@ -33,6 +33,14 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   }
 }
 
+// Once a wait has run out: what this CTA's copies and matrix instructions in flight read and write stays theirs for 20 ms, in which
+// they end.  By the warps that issued them, before the CTA (of a pair: before both) gives up its memory.
+__device__ __forceinline__ void drain(volatile int* give_up) {
+  if (!*give_up) return;
+  const uint64_t since = global_timer_ns();
+  while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
+}
+
 // The rows of expert e, cut to [0, R]: whatever the device data says, no row outside is touched.
 struct RowSpan {
   int begin, end;

@@ -225,10 +225,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         if (++s == S::kStages) { s = 0; phase ^= 1; }
       }
     }
-    if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
-      const uint64_t since = global_timer_ns();
-      while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
-    }
   } else if (warp == 1) {
     // ---- matrix instructions (of a pair: by its first CTA)
     uint32_t s = 0, phase = 0, buf = 0, dphase = 0, tail_phase = 0;
@@ -368,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     }
     if (D == kWeightGrad && threadIdx.x % 128 == 0) tma_store_wait();
   }
+  if (warp < 2) drain(give_up);
   __syncwarp();
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();

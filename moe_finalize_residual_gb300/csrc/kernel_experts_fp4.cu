@@ -182,10 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
         if (++s == S::kStages) { s = 0; phase ^= 1; }
       }
     }
-    if (!ok) {  // copies in flight write this CTA's memory: they get 20 ms to land
-      const uint64_t since = global_timer_ns();
-      while (global_timer_ns() - since < 20000000ull) __nanosleep(1000);
-    }
   } else if (warp == 1) {
     // ---- matrix instructions (of a pair: by its first CTA)
     if (rank == 0) {
@@ -311,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_nvfp4_kernel(const __grid_
       }
     }
   }
+  if (warp < 2) drain(give_up);
   __syncwarp();
   tmem_fence_before();
   if constexpr (Ctas == 2) cluster_sync(); else __syncthreads();
