@@ -13,18 +13,26 @@ namespace mfr {
 constexpr uint64_t kExpertWaitNs = 2000000000ull;
 
 // Bounded wait on an mbarrier phase: false if the CTA is giving up or the limit (about 2 s) ran out; that is counted, and
-// starts the giving up.
+// starts the giving up.  Where the wait is for a whole reduction, which may well take longer, `progress` counts its stages, and the
+// limit starts again when it changes.
 // Ctas 2: of arrivals from both CTAs of a pair.
 template <int Ctas>
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* give_up, unsigned int* timeouts) {
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* give_up, unsigned int* timeouts,
+                                           const volatile uint32_t* progress = nullptr) {
   const auto arrived = [&] { return Ctas == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity); };
   if (arrived()) return true;
-  const uint64_t t0 = global_timer_ns();
+  uint64_t t0 = global_timer_ns();
+  uint32_t seen = progress != nullptr ? *progress : 0;
   for (uint32_t it = 1;; ++it) {
     if (arrived()) return true;
     if ((it & 15u) == 0) {
       if (*give_up) return false;
-      if (global_timer_ns() - t0 > kExpertWaitNs) {
+      const uint64_t now = global_timer_ns();
+      if (progress != nullptr && *progress != seen) {
+        seen = *progress;
+        t0 = now;
+      }
+      if (now - t0 > kExpertWaitNs) {
         atomicAdd(timeouts, 1u);
         *give_up = 1;
         return false;

@@ -136,8 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   const uint32_t dfull0 = ready0 + 8 * S::kStages, dempty0 = dfull0 + 16;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + 4 * S::kStages + 4);
   volatile int* give_up = reinterpret_cast<volatile int*>(tmem_at + 1);
+  // stages whose copies this CTA has issued: the weights' gradient alone, whose reductions are as long as an expert has rows
+  volatile uint32_t* progress = D == kWeightGrad ? tmem_at + 2 : nullptr;
   int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
-  static_assert((4 * S::kStages + 5) * 8 <= kBarBytes, "barriers");
+  static_assert((4 * S::kStages + 6) * 8 <= kBarBytes, "barriers");
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = Ctas == 2 ? uniform(cluster_ctarank()) : 0;
@@ -154,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       mbar_init(dempty0 + 8 * i, 4 * kOutGroups * Ctas);
     }
     *give_up = 0;
+    if constexpr (D == kWeightGrad) *progress = 0;
     fence_mbar_init();
     tma_prefetch_map(&p.a);
     tma_prefetch_map(&p.b);
@@ -197,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           const uint32_t a = stage0 + s * S::kStage, b = a + kABytes;
           const int r0 = k * kDepth;
           if constexpr (D == kWeightGrad) {
+            *progress = *progress + 1;
 #pragma unroll
             for (int i = 0; i < kTileM / 64; ++i)
               tma_load_2d<Ctas>(a + i * 64 * kDepth * 2, &p.a, x.m0 + rank * kTileM + i * 64, x.row0 + r0, bar);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       if (x.steps == 0) continue;
       s = (s + x.steps - 1) % S::kStages;  // the last stage
       if (x.rows % kDepth != 0) {
-        if (!__all_sync(0xffffffffu, wait_phase<1>(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts))) break;
+        if (!__all_sync(0xffffffffu, wait_phase<1>(tail0 + 8 * s, tail_phase >> s & 1, give_up, &g_expert_wait_timeouts, progress))) break;
         tail_phase ^= 1u << s;
         clear_lines<S>(stage0 + s * S::kStage, x.rows % kDepth);
         if (lane == 0) {
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const Tile x = tile_at<D, Ctas, BN>(p, first, t);
       const bool some = x.steps > 0;
       if (some) {
-        const bool ok = wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts);
+        const bool ok = wait_phase<Ctas>(dfull0 + 8 * buf, dphase, give_up, &g_expert_wait_timeouts, progress);
         if (!named_all(sync, 128, ok)) break;  // (the four warps share their stores)
         tmem_fence_after();
       }

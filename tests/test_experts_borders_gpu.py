@@ -1,5 +1,5 @@
 """The experts' products where they can go wrong: gates far below zero, as many rows as a call takes, experts that share
-rows."""
+rows, reductions longer than a wait."""
 import pytest
 import torch
 
@@ -135,3 +135,21 @@ def test_experts_that_share_all_rows_end(mfr):
     mfr.moe_expert_matmul_nvfp4(codes, sf, torch.zeros(E, n, 32, dtype=torch.uint8).cuda(), torch.zeros(E, 512, dtype=torch.uint8).cuda(), off, cnt,
                                 out=y[:R], workspace=space)
     assert (y[R] == 7).all() and (space[-4096:] == 9).all() and mfr.moe_expert_read_timeouts() == 0
+
+
+@pytest.mark.parametrize("n_out", [8, 136])
+def test_a_reduction_that_takes_longer_than_a_wait(mfr, n_out):
+    """The weights' gradient of an expert of so many rows is at work on one tile for more than the 2 s of a wait (64 rows are four
+    instructions of at least 128 cycles each), by one CTA and by a pair."""
+    R, n_in = 640_000_001, 8
+    _room(20 + R * (n_in + n_out) * 2 // (1 << 30))
+    g = torch.Generator().manual_seed(n_out)
+    at = torch.cat([torch.arange(100), torch.randint(100, R - 100, (300,), generator=g).unique(), torch.arange(R - 100, R)]).cuda()
+    x, d = torch.zeros(R, n_in, dtype=HF, device="cuda"), torch.zeros(R, n_out, dtype=HF, device="cuda")
+    some, grad = torch.randint(-2, 3, (at.numel(), n_in), generator=g).to(HF).cuda(), torch.randint(-2, 3, (at.numel(), n_out), generator=g).to(HF).cuda()
+    x[at], d[at] = some, grad
+    off, cnt = torch.tensor([0, R], dtype=torch.int32).cuda(), torch.tensor([R], dtype=torch.int32).cuda()
+    _, dw = mfr.moe_expert_matmul_backward(d, x, None, off, cnt, want_d_rows=False, d_weight_dtype=F32)
+    torch.cuda.synchronize()
+    assert mfr.moe_expert_read_timeouts() == 0
+    assert torch.equal(dw[0].double(), grad.double().T @ some.double())
