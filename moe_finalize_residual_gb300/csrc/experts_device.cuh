@@ -220,11 +220,23 @@ __device__ __forceinline__ void store_tile(uint32_t d, int rows_all, int row0, i
                           to.n - f0);
         named_sync(sync, 128);
       }
+      // (the general form for all of them takes the NVFP4 prompt 776 us for 756; a branch a value the one token's product 35.9 for 35.3)
+      bool far = false;
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
-        const float y = swiglu(upper ? other : v[j], upper ? v[j + 1] : other);
-        reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kLanes / 2) + f] = to_act<T>(y);
+        const float gate = upper ? other : v[j];
+        far |= j < rows && gate < kNearGate;
+        reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kLanes / 2) + f] = to_act<T>(swiglu_near(gate, upper ? v[j + 1] : other));
+      }
+      if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 1], 8);
+          const float gate = upper ? other : v[j];
+          // (only they: a row's results do not depend on its neighbours')
+          if (gate < kNearGate) reinterpret_cast<T*>(box)[(j + (upper ? 1 : 0)) * (kLanes / 2) + f] = to_act<T>(swiglu(gate, upper ? v[j + 1] : other));
+        }
       }
     } else {
 #pragma unroll

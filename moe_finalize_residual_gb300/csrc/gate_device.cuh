@@ -17,7 +17,14 @@ __device__ __forceinline__ Logistic logistic(float g) {
   return p;
 }
 
-// g / (1 + exp(-g)) * u.
+// g / (1 + exp(-g)) * u; the first form from kNearGate on, where the quotient stays inside FP32's normal numbers.
+constexpr float kNearGate = -80.0f;
+__device__ __forceinline__ float swiglu_near(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950409f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
 __device__ __forceinline__ float swiglu(float g, float u) {
   const Logistic p = logistic(g);
   return g * p.m * p.r * (u * p.m);

@@ -65,6 +65,18 @@ def test_the_gate_of_large_negative_values(mfr, rows):
     _near("out", out, a * _logistic(a) * b, (a.abs() + 8) * 2.0 ** -23)
 
 
+def test_gates_below_the_border_leave_their_neighbours_alone(mfr):
+    """A row's results are the same beside rows with gates far below zero."""
+    g = torch.Generator().manual_seed(5)
+    x, w = torch.randn(64, 64, generator=g).to(BF), torch.randn(1, 256, 64, generator=g).to(BF)
+    off, cnt = torch.tensor([0, 64], dtype=torch.int32).cuda(), torch.tensor([64], dtype=torch.int32).cuda()
+    plain = mfr.moe_expert_matmul(x.cuda(), w.cuda(), off, cnt, gated=True)
+    beside = x.clone()
+    beside[::2] = 100 * x[::2]  # gates of either sign, to -3000
+    out = mfr.moe_expert_matmul(beside.cuda(), w.cuda(), off, cnt, gated=True)
+    assert torch.equal(out[1::2], plain[1::2]) and (x[::2].float() @ w[0, :128].float().T * 100).min() < -1000
+
+
 def test_the_gates_gradient_of_large_negative_values(mfr):
     R, F = 40, 512
     g = torch.Generator().manual_seed(3)
