@@ -172,8 +172,8 @@ int moe_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args* args, struct CUs
 int64_t moe_expert_matmul_nvfp4_workspace_bytes(int32_t E, int64_t num_rows, int32_t n_in);
 
 /* Waits of the products' kernels that ran out (about 2 s without a step of a reduction; none does unless something is broken) since
- * the last call, on the current device; synchronizes.  A call with such a wait ends and leaves its outputs unfinished.  Test hook:
- * under MFR_FLAG_TEST_STREAM_TIMEOUT the products' waits for their operands run out. */
+ * the last call, on the current device, which is synchronized: every stream's calls count.  A call with such a wait ends and leaves its
+ * outputs unfinished.  Test hook: under MFR_FLAG_TEST_STREAM_TIMEOUT the products' waits for their operands run out. */
 int moe_expert_read_timeouts(uint32_t* count);
 
 #ifdef __cplusplus

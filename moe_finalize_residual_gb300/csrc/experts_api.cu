@@ -1,6 +1,7 @@
 // C ABI of the experts' products (moe_experts.h): argument validation (nothing is enqueued on error), size queries and
 // dispatch to the kernels.
 #include <climits>
+#include <mutex>
 
 #include "experts_launch.h"
 #include "mfr_launch.h"
@@ -254,11 +255,22 @@ int moe_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args* args, struct CUs
 
 int moe_expert_read_timeouts(uint32_t* count) {
   if (count == nullptr) return fail(MFR_ERR_INVALID_ARG, "count is NULL");
+  // The device's counters only grow, so that no wait of a running kernel is lost; what was read last is kept here.
+  constexpr int kDevices = 64;
+  static std::mutex lock;
+  static uint32_t known[kDevices] = {};
+  const std::lock_guard<std::mutex> hold(lock);
+  int dev = 0;
   unsigned int c = 0, q = 0;
-  cudaError_t e = read_and_reset_expert_timeouts(&c);
-  if (e == cudaSuccess) e = read_and_reset_expert_nvfp4_timeouts(&q);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= kDevices) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();  // (the copies below wait for no stream that does not block)
+  if (e == cudaSuccess) e = read_expert_timeouts(&c);
+  if (e == cudaSuccess) e = read_expert_nvfp4_timeouts(&q);
   if (e != cudaSuccess) return fail(MFR_ERR_CUDA, "reading the timeout counters: %s", cudaGetErrorString(e));
-  *count = c + q;
+  const uint32_t all = c + q;
+  *count = all >= known[dev] ? all - known[dev] : all;  // (fewer: the device was reset)
+  known[dev] = all;
   return MFR_OK;
 }
 

@@ -13,8 +13,8 @@ cudaError_t launch_swiglu_backward(const mfr_swiglu_backward_args& a, cudaStream
 cudaError_t launch_nvfp4_quantize(const mfr_nvfp4_args& a, cudaStream_t stream);
 cudaError_t launch_nvfp4_dequantize(const mfr_nvfp4_args& a, cudaStream_t stream);
 cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cudaStream_t stream);
-cudaError_t read_and_reset_expert_timeouts(unsigned int* count);
-cudaError_t read_and_reset_expert_nvfp4_timeouts(unsigned int* count);
+cudaError_t read_expert_timeouts(unsigned int* count);
+cudaError_t read_expert_nvfp4_timeouts(unsigned int* count);
 
 // Rows of an operand that one CTA's tile spans, and the most tiles of a call (tile numbers are 32-bit).
 constexpr int kExpertTileRows = 128;

@@ -511,11 +511,6 @@ cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, 
   return pair ? launch_weights<2>(a, p, stream) : launch_weights<1>(a, p, stream);
 }
 
-cudaError_t read_and_reset_expert_timeouts(unsigned int* count) {
-  cudaError_t e = cudaMemcpyFromSymbol(count, g_expert_wait_timeouts, sizeof(unsigned int));
-  if (e != cudaSuccess || *count == 0) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(g_expert_wait_timeouts, &zero, sizeof(unsigned int));
-}
+cudaError_t read_expert_timeouts(unsigned int* count) { return cudaMemcpyFromSymbol(count, g_expert_wait_timeouts, sizeof(unsigned int)); }
 
 }  // namespace mfr

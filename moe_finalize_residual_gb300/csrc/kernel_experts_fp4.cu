@@ -432,11 +432,6 @@ cudaError_t launch_expert_matmul_nvfp4(const mfr_expert_matmul_nvfp4_args& a, cu
   return a.gated ? launch_by_rows<true>(a, p, stream) : launch_by_rows<false>(a, p, stream);
 }
 
-cudaError_t read_and_reset_expert_nvfp4_timeouts(unsigned int* count) {
-  cudaError_t e = cudaMemcpyFromSymbol(count, g_expert_nvfp4_wait_timeouts, sizeof(unsigned int));
-  if (e != cudaSuccess || *count == 0) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(g_expert_nvfp4_wait_timeouts, &zero, sizeof(unsigned int));
-}
+cudaError_t read_expert_nvfp4_timeouts(unsigned int* count) { return cudaMemcpyFromSymbol(count, g_expert_nvfp4_wait_timeouts, sizeof(unsigned int)); }
 
 }  // namespace mfr

@@ -459,7 +459,8 @@ def moe_expert_matmul_nvfp4(codes: torch.Tensor, sf: torch.Tensor, weight_codes:
 
 
 def moe_expert_read_timeouts() -> int:
-    """Waits of the products' kernels that ran out since the last call, on the current device (0 unless something is broken)."""
+    """Waits of the products' kernels that ran out since the last call, on the current device and any of its streams (0 unless
+    something is broken).  Synchronizes the device."""
     n = _U(0)
     status = _lib.moe_expert_read_timeouts(ctypes.byref(n))
     if status != 0:

@@ -1,5 +1,5 @@
 """The experts' products where they can go wrong: gates far below zero, as many rows as a call takes, experts that share
-rows, reductions longer than a wait."""
+rows, reductions longer than a wait, waits on other streams."""
 import pytest
 import torch
 
@@ -165,3 +165,25 @@ def test_a_reduction_that_takes_longer_than_a_wait(mfr, n_out):
     torch.cuda.synchronize()
     assert mfr.moe_expert_read_timeouts() == 0
     assert torch.equal(dw[0].double(), grad.double().T @ some.double())
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Waits
+# ----------------------------------------------------------------------------------------------------------------
+
+def test_a_wait_that_runs_out_on_another_stream_is_counted(mfr):
+    """The count waits for every stream of the device: the call may still be running."""
+    X, rows = mfr.experts, 40
+    x, w = torch.ones(rows, 64, dtype=HF).cuda(), torch.ones(1, 64, 64, dtype=HF).cuda()
+    off, cnt, out = torch.tensor([0, rows], dtype=torch.int32).cuda(), torch.tensor([rows], dtype=torch.int32).cuda(), torch.empty(rows, 64, dtype=HF).cuda()
+    args = X._pack_matmul(1, 64, 64, 1, 0, rows, x.data_ptr(), 64, w.data_ptr(), 64, 64 * 64, off.data_ptr(), cnt.data_ptr(), out.data_ptr(), 64, 0, 0,
+                          mfr.MFR_FLAG_TEST_STREAM_TIMEOUT)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert mfr.moe_expert_read_timeouts() == 0
+    assert mfr.raw_library().moe_expert_matmul(args, side.cuda_stream) == 0
+    first = mfr.moe_expert_read_timeouts()
+    torch.cuda.synchronize()
+    again = mfr.moe_expert_read_timeouts()
+    assert first > 0 and again == 0
+    assert torch.equal(mfr.moe_expert_matmul(x, w, off, cnt), torch.full((rows, 64), 64.0, dtype=HF).cuda())
