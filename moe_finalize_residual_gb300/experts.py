@@ -83,7 +83,10 @@ def _bind(lib, raise_status):
 
 def _row_tensor(name, t, index, shape, act, check):
     """Pointer and row stride of a tensor [rows, n] whose rows may be apart."""
-    s = t.stride()
+    try:
+        s = t.stride()
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
     if check and not (t.dtype is act and t.get_device() == index and t.shape == shape and (s[1] == 1 or shape[1] == 1)):
         _check_tensor(name, t, torch.device("cuda", index), shape, act, contiguous=False)
         raise ValueError(f"the values of a row must be contiguous in {name}")
@@ -95,7 +98,10 @@ def _weight(t, index, act, check):
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError("weight must be [E, n, n_in]")
     E, n, n_in = t.shape
-    s = t.stride()
+    try:
+        s = t.stride()
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
     if check and not (t.dtype is act and t.get_device() == index and s[2] == 1):
         _check_tensor("weight", t, torch.device("cuda", index), None, act, contiguous=False)
         raise ValueError("the values of a row must be contiguous in weight")
@@ -187,9 +193,10 @@ def moe_expert_matmul_backward(d_out: torch.Tensor, rows: Optional[torch.Tensor]
         raise ValueError("accumulate needs a d_weight to add to")
     if want_d_rows and weight is None or want_d_weight and rows is None or rows is None and weight is None:
         raise ValueError("d_rows needs weight, and d_weight needs rows")
-    if check and expert_offsets is None:
-        raise ValueError("expert_offsets must be a tensor")
-    E = expert_offsets.shape[0] - 1
+    try:
+        E = expert_offsets.shape[0] - 1
+    except (AttributeError, IndexError):
+        raise ValueError("expert_offsets must be a tensor [E + 1]") from None
     w, x = (0, 0, 0), (0, 0)
     if weight is not None:
         We, Wn, n_in, w = _weight(weight, index, act, check)
@@ -217,7 +224,7 @@ def moe_expert_matmul_backward(d_out: torch.Tensor, rows: Optional[torch.Tensor]
             d_weight = torch.empty(E, n_out, n_in, dtype=dw_type, device=d_out.device)
             allocated.append(d_weight)
         else:
-            dw_type = d_weight.dtype
+            dw_type = getattr(d_weight, "dtype", None)
             if check and (d_weight_dtype is not None and dw_type is not d_weight_dtype
                           or not _good(d_weight, index, (E, n_out, n_in), dw_type)
                           or dw_type is not act and dw_type is not torch.float32):
@@ -339,6 +346,8 @@ def nvfp4_quantize(x: torch.Tensor, scale: torch.Tensor, *, sf_layout: str = "ro
     "swizzled_128x4" tiles of 128 rows x 4 blocks, for each matrix, with zeros behind its last row and block.
     ``moe_expert_matmul_nvfp4`` reads rows of the first kind and weights of the second.  With ``row_route`` rows of no route are
     not read and get zeros."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a tensor")
     matrices, rows, H = _matrices(x.shape)
     index, layout = x.get_device(), _choice(_SF_LAYOUT, "sf_layout", sf_layout)
     lead = tuple(x.shape[:-1])
@@ -367,6 +376,8 @@ def nvfp4_dequantize(codes: torch.Tensor, sf: torch.Tensor, scale: torch.Tensor,
                      check: bool = True) -> torch.Tensor:
     """The values that ``nvfp4_quantize``'s (or the finalize's) codes and scales stand for: ``code * (sf / scale)``, rounded to
     ``dtype`` (bf16 or fp16).  With ``row_route`` rows of no route are not read and get zeros."""
+    if not isinstance(codes, torch.Tensor):
+        raise ValueError("codes must be a tensor")
     matrices, rows, half = _matrices(codes.shape)
     H = 2 * half
     index, layout = codes.get_device(), _choice(_SF_LAYOUT, "sf_layout", sf_layout)

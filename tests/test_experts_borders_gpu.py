@@ -187,3 +187,24 @@ def test_a_wait_that_runs_out_on_another_stream_is_counted(mfr):
     again = mfr.moe_expert_read_timeouts()
     assert first > 0 and again == 0
     assert torch.equal(mfr.moe_expert_matmul(x, w, off, cnt), torch.full((rows, 64), 64.0, dtype=HF).cuda())
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Refusals
+# ----------------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("no_tensor", [3, [1.0], "rows"])
+def test_what_is_no_tensor_is_refused(mfr, no_tensor):
+    x, w, o = torch.zeros(4, 64, dtype=BF).cuda(), torch.zeros(2, 128, 64, dtype=BF).cuda(), torch.zeros(3, dtype=torch.int32).cuda()
+    d = torch.zeros(4, 128, dtype=BF).cuda()
+    t = no_tensor
+    for call in (lambda: mfr.moe_expert_matmul(x, w, o, out=t), lambda: mfr.moe_expert_matmul(x, w, o, gated=True, gate_up=t),
+                 lambda: mfr.moe_expert_matmul(x, w, t), lambda: mfr.moe_expert_matmul(x, w, o, t),
+                 lambda: mfr.moe_expert_matmul_backward(d, x, w, t), lambda: mfr.moe_expert_matmul_backward(d, x, w, o, t),
+                 lambda: mfr.moe_expert_matmul_backward(d, x, w, o[0]), lambda: mfr.moe_expert_matmul_backward(d, t, w, o),
+                 lambda: mfr.moe_expert_matmul_backward(d, x, w, o, d_rows=t), lambda: mfr.moe_expert_matmul_backward(d, x, w, o, d_weight=t),
+                 lambda: mfr.moe_swiglu_backward(t, d), lambda: mfr.moe_swiglu_backward(x, d, d_gate_up=t),
+                 lambda: mfr.moe_swiglu_backward(x, d, act=t), lambda: mfr.moe_swiglu_backward(x, d, row_route=t),
+                 lambda: mfr.nvfp4_quantize(x, t), lambda: mfr.nvfp4_quantize(x, d, codes=t)):
+        with pytest.raises(ValueError):
+            call()

@@ -52,3 +52,11 @@ def test_the_most_rows_of_a_workspace(mfr):
     assert mfr.moe_expert_matmul_nvfp4_workspace_bytes(8, MOST_ROWS, 64) == (MOST_ROWS // 192 + 8) * 2 * 512
     with pytest.raises(mfr.MoEFinalizeError):
         mfr.moe_expert_matmul_nvfp4_workspace_bytes(8, MOST_ROWS + 1, 64)
+
+
+@pytest.mark.parametrize("no_tensor", [None, 3, [1.0]])
+def test_what_is_no_tensor_is_refused(mfr, no_tensor):
+    u8, s = torch.zeros(4, 32, dtype=torch.uint8), torch.ones(1)
+    for call in (lambda: mfr.nvfp4_quantize(no_tensor, s), lambda: mfr.nvfp4_dequantize(no_tensor, u8, s)):
+        with pytest.raises(ValueError):
+            call()
