@@ -678,7 +678,8 @@ int moe_finalize_gather_floor_launch(const int32_t* idx, const void* rows, int64
 int moe_finalize_read_timeouts(uint32_t* count) {
   if (count == nullptr) return fail(MFR_ERR_INVALID_ARG, "count is NULL");
   unsigned int c = 0, cc = 0, cb = 0;
-  cudaError_t e = read_and_reset_timeouts(&c);
+  cudaError_t e = cudaDeviceSynchronize();  // (the copies below wait for no stream that does not block)
+  if (e == cudaSuccess) e = read_and_reset_timeouts(&c);
   if (e == cudaSuccess) e = read_and_reset_cluster_timeouts(&cc);
   if (e == cudaSuccess) e = read_and_reset_bulk_timeouts(&cb);
   if (e != cudaSuccess) return fail(MFR_ERR_CUDA, "reading the timeout counters: %s", cudaGetErrorString(e));
