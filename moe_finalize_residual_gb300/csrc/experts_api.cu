@@ -60,11 +60,12 @@ int check_experts(int E, int64_t num_rows, const int32_t* offsets, const int32_t
   return MFR_OK;
 }
 
-// `rows` tiles' rows, `width` columns: tile numbers are 32-bit.
+// Tile numbers are 32-bit.
 int check_tiles(int64_t tiles) {
   if (tiles >= kExpertMaxTiles) return fail(MFR_ERR_INVALID_ARG, "%lld tiles: 2^31 or more", static_cast<ll>(tiles));
   return MFR_OK;
 }
+// The most tiles of any kernel for `rows` rows and `width` values a row.
 int64_t row_tiles(int64_t rows, int E, int64_t width) { return expert_row_tiles(rows, E, kExpertTileRows) * ((width + 63) / 64); }
 
 int check_weight(const void* p, int64_t stride, int64_t expert_stride, int E, int64_t rows, int64_t width) {

@@ -16,9 +16,10 @@
 // store them meanwhile.
 //
 // What bounds it, on GB300: with few rows HBM (64 tokens of 256 experts, top-8, 1024 x 6144 weights: 375 us, every weight read
-// once); with many the tensor pipe, 92 % busy (8 experts of 768 rows, 7168 x 4096: 211 us, 1.70 PFLOP/s), beside copies of 64 bytes a
-// cycle and SM, which alone take 0.8 of that; the weights' gradient its results beside those copies (64 experts of 384 rows,
-// 4096 x 4096: 645 us; by pairs 720 to 750, of it 530 without stores and 404 without results).
+// once); with many the tensor pipe, active for 92 % of the time (8 experts of 768 rows, 7168 x 4096: 211 us, 1.70 PFLOP/s; the counter
+// counts instructions that wait for operands too), beside copies of 64 bytes a cycle and SM, which alone take 0.8 of that; the weights'
+// gradient its results beside those copies (64 experts of 384 rows, 4096 x 4096: 645 us by one CTA a tile; by pairs, as from 512 rows
+// on, 720 to 750, of it 530 without stores and 404 without results).
 #include "experts_device.cuh"
 
 namespace mfr {
@@ -413,7 +414,9 @@ cudaError_t launch_rows(int act, int64_t R, int E, const void* rows, int64_t row
 // The tile by the rows that an expert has: with few of them the stages hold little but weights, as many as fit; with many, a pair
 // of CTAs halves the copies of the columns' operand.  Measured, 64 experts of 4096 x 4096 in BF16 (floor 317 us): 2 rows each
 // 310 us by the small tile and 317 by the pair's, 16 rows 319 and 325, 32 rows 324 and 328, 48 rows (two small tiles an expert)
-// 379 and 331.  Rows vary from expert to expert, so the border is well below 32.
+// 379 and 331.  Rows vary from expert to expert, so the border is well below 32.  R is the buffer's rows: those of routes elsewhere
+// and of the experts' alignment count too, so a decode step in a buffer aligned to 128 goes by the pair's tile (64 tokens of 256 experts,
+// top-8, 1024 x 6144: 377 us by it, 382 by the small one without alignment).
 template <int D>
 cudaError_t launch_by_rows(int act, int64_t R, int E, const void* rows, int64_t rows_stride, Params& p, bool pdl, cudaStream_t stream) {
   if (R <= int64_t{16} * E) return launch_rows<D, 1, 32>(act, R, E, rows, rows_stride, p, pdl, stream);
@@ -505,8 +508,8 @@ cudaError_t launch_expert_weight_grad(const mfr_expert_matmul_backward_args& a, 
   p.test_extra = (a.flags & MFR_FLAG_TEST_STREAM_TIMEOUT) != 0;
   // A pair's tiles cost more of a turnaround and fewer copies.  Measured, 32 experts of 4096 x 4096: 128 rows each 181 us by one CTA
   // a tile and 311 by pairs, 256 rows 248 and 354, 384 to 483 rows 436 and 437, 512 rows 408 and 391, 768 rows 563 and 492.  The rows
-  // of the call are a little more than the experts', by their alignment.  (With at most 128 rows of weights the pair's second CTA
-  // would have none.)
+  // of the call are the buffer's: more than the experts' by their alignment and by routes elsewhere, which moves the border down by as
+  // much.  (With at most 128 rows of weights the pair's second CTA would have none.)
   const bool pair = a.num_rows >= int64_t{512} * a.E && a.n_out > kTileM;
   return pair ? launch_weights<2>(a, p, stream) : launch_weights<1>(a, p, stream);
 }

@@ -11,8 +11,8 @@
 // before this one writes them in tiles, once for all columns' tiles.
 //
 // What bounds it, on GB300: with few rows HBM (16 tokens of 256 experts, top-8, 7168 x 2048 weights: 123.5 us, the floor); with many
-// the stages' turnaround, 0.35 us (8 experts of 768 rows, 7168 x 4096: 78 us, 4.6 PFLOP/s), gated the weights' scales on top of
-// it (99 us).
+// the stages, 0.35 us each (8 experts of 768 rows, 7168 x 4096: 78 us, 4.6 PFLOP/s): their copies, 34816 bytes a CTA, take most of that
+// at the 60 bytes a cycle that come from L2, the instructions 384 cycles; gated the weights' scales on top of it (99 us).
 #include "experts_device.cuh"
 
 namespace mfr {

@@ -3,8 +3,7 @@
 // A row is taken by `tpr` threads of a CTA (whole warps), so that no thread divides by a row's length.
 // Measured on GB300, 32768 rows: the gate's gradient of 2048 values 123 us (0.96 of the copy bandwidth); 7168 values to NVFP4 112 us
 // and back 110 (floor 89 each), both held up by their instructions.
-#include "experts_launch.h"
-#include "gate_device.cuh"
+#include "experts_device.cuh"
 
 namespace mfr {
 namespace {
@@ -97,7 +96,7 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const __grid_const
 // ------------------------------------------------------------------------------------------------
 
 constexpr int kPieces = 4;           // of 8 values, that a thread has in flight
-constexpr int kFp4Blocks = 152 * 8;  // CTAs at most: some turns of those that a GB300 holds at once
+constexpr int kFp4BlocksPerSm = 8;   // at most: some turns of the CTAs that an SM holds at once
 
 struct Fp4Params {
   const uint8_t* x;   // quantize: read; dequantize: written
@@ -110,7 +109,7 @@ struct Fp4Params {
   int64_t rows_up;    // with the tiles' last rows
   int64_t total;      // rows_up of all matrices
   int64_t sf_bytes;   // of a matrix
-  int32_t H, blocks, blocks_up, layout, tpr, act;
+  int32_t H, blocks, blocks_up, layout, tpr;
 };
 
 // Row i of all matrices'; `real` false behind a matrix's last row, `live` false for a row of no route too.
@@ -312,8 +311,8 @@ Fp4Params fp4_params(const mfr_nvfp4_args& a, bool padding) {
 // CTAs that stay for several rows: what a thread works out once (the divisions above all) is a third of its instructions when
 // it has one row.
 dim3 fp4_grid(const Fp4Params& p, const RowShape& s) {
-  const int64_t all = (p.total + s.rows - 1) / s.rows, most = kFp4Blocks;
-  return dim3(static_cast<unsigned>(all < most ? all : most));
+  const int64_t all = (p.total + s.rows - 1) / s.rows, most = int64_t{kFp4BlocksPerSm} * sm_count();
+  return dim3(static_cast<unsigned>(all < most || most == 0 ? all : most));
 }
 
 }  // namespace
