@@ -128,6 +128,32 @@ def test_nvfp4_product(mfr, counts, n_in, n_out, gated):
     ref.close("out", out, y, err)
 
 
+@pytest.mark.parametrize("align", [8, 128])
+def test_a_decode_step_in_a_padded_buffer(mfr, align):
+    """Few rows an expert, each expert's from a multiple of `align` on: the buffer's rows choose another kernel at 128, and the results
+    are the same."""
+    counts, n_in, n_out = [1, 0, 2, 7, 1, 0, 0, 3, 16, 1, 5, 0] * 4, 832, 384
+    got = {}
+    for a in (1, align):
+        g, off, R, o, c = _case(counts, 4, a)
+        live = ~ref.free_rows(off, counts, R).cuda()
+        n = sum(counts)
+        some, w = _whole(g, n, n_in), _whole(g, len(counts), 2 * n_out, n_in)
+        sc, sf, _ = _fp4(g, n, n_in)
+        wc, wf, _ = _fp4(g, len(counts), 2 * n_out, n_in)
+        x, codes, scales = torch.full((R, n_in), float("nan"), dtype=HF, device="cuda"), torch.full((R, n_in // 2), 0x77, dtype=torch.uint8, device="cuda"), \
+            torch.full((R, n_in // 16), 0x7f, dtype=torch.uint8, device="cuda")
+        x[live], codes[live], scales[live] = some, sc, sf
+        tiled = torch.zeros(len(counts), 2 * n_out * n_in // 16, dtype=torch.uint8, device="cuda")
+        tiled[:, ref.tile_at(2 * n_out, n_in // 16).cuda()] = wf
+        y = [mfr.moe_expert_matmul(x, w, o, c), mfr.moe_expert_matmul_nvfp4(codes, scales, wc, tiled, o, c, dtype=HF)]
+        y.append(mfr.moe_expert_matmul_backward(y[0].clamp(-2, 2), None, w, o, c, want_d_weight=False)[0])
+        assert all((t[~live] == 0).all() for t in y)
+        got[a] = [t[live] for t in y]
+    assert (mfr.moe_expert_matmul_nvfp4_workspace_bytes(len(counts), R, n_in) > 0) == (align == 128)
+    assert all(t.abs().max() <= 2048 and torch.equal(t, u) for t, u in zip(got[1], got[align]))
+
+
 def test_gradients_on_two_streams_at_once(mfr):
     counts = [300, 5, 0, 250]
     g, off, R, o, c = _case(counts, 8)
